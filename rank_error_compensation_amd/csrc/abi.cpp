@@ -14,7 +14,9 @@
 #include "glowq.h"
 #include "glowq_internal.h"
 #include "glowq_offline.h"
+#include "layer.h"
 #include "mid.h"
+#include "w8a8.h"
 
 using namespace glowq;
 
@@ -29,6 +31,7 @@ constexpr int64_t kMaxMomentElems = (int64_t)1 << 31;  // N d (int32 offsets sta
 // tiles in int32; calls past these bounds are rejected before any HIP call.
 constexpr int64_t kMaxActElems = (int64_t)1 << 30;     // T d
 constexpr int64_t kMaxTiles = ((int64_t)1 << 31) - 1;  // 16-token tiles x 16-row tiles
+constexpr int64_t kMaxGateElems = (int64_t)1 << 33;    // gated activation: values of a call (one launch)
 
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
@@ -68,6 +71,7 @@ struct Call {
     void* const* y;
     bool w4a8;  // 8-bit activations (glowq_group_forward_w4a8)
     bool mx8;   // MXFP4 weights x MXFP8 activations (glowq_group_forward_mx8)
+    bool w8a8;  // INT8 weights x 8-bit activations (glowq_group_forward_w8a8)
 };
 
 int validate(const Call& c, void* workspace, size_t ws_bytes) {
@@ -84,7 +88,8 @@ int validate(const Call& c, void* workspace, size_t ws_bytes) {
     for (int i = 0; i < c.m; ++i) {
         const glowq_qweight& w = c.w[i];
         if (w.q == nullptr || w.sz == nullptr) return GLOWQ_ERR_INVALID_ARG;
-        if (w.format < GLOWQ_FMT_INT4_G128 || w.format > GLOWQ_FMT_MXFP6_E3M2 || w.reserved != 0)
+        if (w.format < GLOWQ_FMT_INT4_G128 || w.format > (c.w8a8 ? GLOWQ_FMT_INT8_CHANNEL : GLOWQ_FMT_MXFP6_E3M2) ||
+            w.reserved != 0)
             return GLOWQ_ERR_INVALID_ARG;
         if (w.format != c.w[0].format) return GLOWQ_ERR_UNSUPPORTED;  // one format per call
         if (c.T > 0 && c.y[i] == nullptr) return GLOWQ_ERR_INVALID_ARG;
@@ -98,6 +103,7 @@ int validate(const Call& c, void* workspace, size_t ws_bytes) {
     if (c.x != nullptr && !aligned(c.x, 16)) return GLOWQ_ERR_ALIGN;
     if (c.w4a8 && (c.d > kW4a8MaxD || c.w[0].format != GLOWQ_FMT_INT4_G128)) return GLOWQ_ERR_UNSUPPORTED;
     if (c.mx8 && c.w[0].format == GLOWQ_FMT_INT4_G128) return GLOWQ_ERR_UNSUPPORTED;  // MX weights only
+    if (c.w8a8 && (c.d > kW8MaxD || c.w[0].format != GLOWQ_FMT_INT8_CHANNEL)) return GLOWQ_ERR_UNSUPPORTED;
     if (c.correct) {
         if (c.a == nullptr || c.b == nullptr) return GLOWQ_ERR_INVALID_ARG;
         for (int i = 0; i < c.m; ++i)
@@ -110,9 +116,10 @@ int validate(const Call& c, void* workspace, size_t ws_bytes) {
             if (!aligned(c.b[p], 16)) return GLOWQ_ERR_ALIGN;
     }
     if (c.T > 0) {
-        // W4A8 calls always need their workspace (the activation codes); the others only to correct
+        // 8-bit activation calls always need their workspace (the activation codes); the others only to correct
         const size_t need = c.w4a8  ? glowq_w4a8_workspace_bytes(c.T, c.d, c.correct ? c.r : 0)
                             : c.mx8 ? glowq_mx8_workspace_bytes(c.T, c.d, c.correct ? c.r : 0)
+                            : c.w8a8 ? glowq_w8a8_workspace_bytes(c.T, c.d, c.correct ? c.r : 0)
                                     : (c.correct ? glowq_workspace_bytes(c.T, c.r, c.n_proj) : 0);
         if (need > 0) {
             if (workspace == nullptr || ws_bytes < need) return GLOWQ_ERR_WORKSPACE;
@@ -408,6 +415,7 @@ Call make_group(const void* x, int64_t T, int64_t d, int32_t m, const glowq_qwei
     c.y = y;
     c.w4a8 = false;
     c.mx8 = false;
+    c.w8a8 = false;
     return c;
 }
 
@@ -506,6 +514,83 @@ int run_w4a8(const Call& c, void* workspace, hipStream_t stream) {
     f.m_tiles = (int32_t)ceil_div(c.T, 16 * tt);
     f.n_tiles = (int32_t)(tiles * f.m_tiles);
     return (c.mx8 ? launch_mx8(f, stream) : launch_w4a8(f, stream)) == hipSuccess ? GLOWQ_OK : GLOWQ_ERR_HIP;
+}
+
+// W8A8 tile: 16 to 64 tokens by one or two 16-row tiles per workgroup.
+void choose_w8a8_shape(const Call& c, int& tt, int& rr) {
+    tt = c.T <= 16 ? 1 : (c.T <= 32 ? 2 : 4);
+    rr = tt == 1 ? 1 : 2;
+}
+
+// W8A8 form.  Workspace: codes int8 [T][d] | scales fp32 [T] | projection and its split-K partials.
+int run_w8a8(const Call& c, void* workspace, hipStream_t stream) {
+    if (c.T == 0) return GLOWQ_OK;
+    uint8_t* base = static_cast<uint8_t*>(workspace);
+    int8_t* xq = reinterpret_cast<int8_t*>(base);
+    base += round256((size_t)c.T * c.d);
+    float* xscale = reinterpret_cast<float*>(base);
+    base += round256((size_t)c.T * 4u);
+    void* R = c.correct ? base : nullptr;
+    if (launch_quant_q8(static_cast<const _Float16*>(c.x), (int)c.T, (int)c.d, xq, xscale, stream) != hipSuccess)
+        return GLOWQ_ERR_HIP;
+    if (c.correct && launch_projection(c, R, stream) != hipSuccess) return GLOWQ_ERR_HIP;
+    ForwardArgs f;
+    std::memset(&f, 0, sizeof(f));
+    f.T = (int32_t)c.T;
+    f.d = (int32_t)c.d;
+    f.G = (int32_t)(c.d / kGroup);
+    f.r = c.correct ? c.r : 0;
+    f.r_pad = c.correct ? (int32_t)r_pad_of(c.r) : 0;
+    f.n_mod = c.m;
+    f.R = R;
+    f.n_proj = 1;
+    f.xq = xq;
+    f.xscale = xscale;
+    f.fmt = kFmtInt8;
+    int tt = 1, rr = 1;
+    choose_w8a8_shape(c, tt, rr);
+    f.tile_tt = tt;
+    f.tile_rr = rr;
+    int64_t tiles = 0;
+    for (int i = 0; i < c.m; ++i) {
+        ModuleArgs& M = f.mod[i];
+        M.q = static_cast<const uint8_t*>(c.w[i].q);
+        M.sz = static_cast<const uint8_t*>(c.w[i].sz);
+        M.a = c.correct ? static_cast<const _Float16*>(c.a[i]) : nullptr;
+        M.y = static_cast<_Float16*>(c.y[i]);
+        M.n_out = (int32_t)c.w[i].n_out;
+        M.n_tiles16 = (int32_t)ceil_div(c.w[i].n_out, 16);
+        M.tile_begin = (int32_t)tiles;
+        f.tile_begin[i] = (int32_t)tiles;
+        tiles += ceil_div(M.n_tiles16, rr);
+    }
+    f.m_tiles = (int32_t)ceil_div(c.T, 16 * tt);
+    f.n_tiles = (int32_t)(tiles * f.m_tiles);
+    return launch_w8a8(f, stream) == hipSuccess ? GLOWQ_OK : GLOWQ_ERR_HIP;
+}
+
+// Arguments shared by the calls that move routed rows.
+int validate_rows(int64_t T, int64_t top_k, int64_t n_rows, int64_t d, int32_t dtype) {
+    if (dtype != GLOWQ_DTYPE_F16 && dtype != GLOWQ_DTYPE_F32) return GLOWQ_ERR_INVALID_ARG;
+    if (T < 0 || n_rows < 0 || d < 1 || top_k < 1) return GLOWQ_ERR_SHAPE;
+    if (top_k > kMoeMaxTopK || T > kMaxT || n_rows > kMaxT * 8 || T * top_k > kMaxT * 8 || d > kMaxD)
+        return GLOWQ_ERR_UNSUPPORTED;
+    return GLOWQ_OK;
+}
+
+int validate_moe_workspace(const void* workspace, size_t bytes, size_t need) {
+    if (workspace == nullptr || bytes < need) return GLOWQ_ERR_WORKSPACE;
+    return aligned(workspace, 256) ? GLOWQ_OK : GLOWQ_ERR_ALIGN;
+}
+
+inline int32_t* error_word(void* workspace) { return static_cast<int32_t*>(workspace) + kSyncError; }
+
+// Workgroups and pairs per workgroup of a routing-list call.
+void sort_plan(int64_t n, int64_t& blocks, int64_t& chunk) {
+    blocks = 1, chunk = n;
+    if (n <= kSortOnePairs) return;
+    chunk = ceil_div(ceil_div(n, kSortMaxBlocks), kSortThreads) * kSortThreads;
+    blocks = ceil_div(n, chunk);
 }
 
 }  // namespace
@@ -658,6 +743,198 @@ int glowq_moe_forward(const void* x, int64_t T, int64_t d, int32_t n_exp, int32_
     if (launch_moe_gemm(a, (int64_t)rbs * (ceil_div(n_rows, rows_per_item) + active_max), stream) != hipSuccess)
         return GLOWQ_ERR_HIP;
     return GLOWQ_OK;
+}
+
+size_t glowq_moe_sort_workspace_bytes(int64_t T, int64_t top_k, int32_t n_exp) {
+    if (validate_rows(T, top_k, 0, 1, GLOWQ_DTYPE_F16) != GLOWQ_OK) return 0;
+    if (n_exp < 1 || n_exp > GLOWQ_MOE_MAX_EXPERTS) return 0;
+    int64_t blocks, chunk;
+    sort_plan(T * top_k, blocks, chunk);
+    return kWsHeader + (blocks > 1 ? round256((size_t)blocks * (size_t)(n_exp + 1) * 4u) : 0);
+}
+
+int glowq_moe_sort(const int32_t* expert_ids_dev, int64_t T, int64_t top_k, int32_t n_exp, int32_t* offsets_dev,
+                   int32_t* row_token_dev, int32_t* pair_row_dev, void* workspace, size_t workspace_bytes,
+                   hipStream_t stream) {
+    const int v = validate_rows(T, top_k, 0, 1, GLOWQ_DTYPE_F16);
+    if (v != GLOWQ_OK) return v;
+    if (n_exp < 1 || n_exp > GLOWQ_MOE_MAX_EXPERTS) return GLOWQ_ERR_UNSUPPORTED;
+    if (offsets_dev == nullptr) return GLOWQ_ERR_INVALID_ARG;
+    if (T > 0 && (expert_ids_dev == nullptr || row_token_dev == nullptr || pair_row_dev == nullptr))
+        return GLOWQ_ERR_INVALID_ARG;
+    if (!aligned(expert_ids_dev, 4) || !aligned(offsets_dev, 4) || !aligned(row_token_dev, 4) || !aligned(pair_row_dev, 4))
+        return GLOWQ_ERR_ALIGN;
+    const int w = validate_moe_workspace(workspace, workspace_bytes, glowq_moe_sort_workspace_bytes(T, top_k, n_exp));
+    if (w != GLOWQ_OK) return w;
+    int64_t blocks, chunk;
+    sort_plan(T * top_k, blocks, chunk);
+    SortArgs a;
+    a.ids = expert_ids_dev;
+    a.n = (int32_t)(T * top_k);
+    a.top_k = (int32_t)top_k;
+    a.n_exp = n_exp;
+    a.n_blocks = (int32_t)blocks;
+    a.chunk = (int32_t)chunk;
+    a.part = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + kWsHeader);
+    a.offsets = offsets_dev;
+    a.row_token = row_token_dev;
+    a.pair_row = pair_row_dev;
+    a.err = error_word(workspace);
+    return launch_moe_sort(a, stream) == hipSuccess ? GLOWQ_OK : GLOWQ_ERR_HIP;
+}
+
+int glowq_moe_dispatch(const void* x, int64_t T, int64_t d, int32_t dtype, const int32_t* row_token_dev, int64_t n_rows,
+                       void* rows, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    const int v = validate_rows(T, 1, n_rows, d, dtype);
+    if (v != GLOWQ_OK) return v;
+    if (n_rows == 0) return GLOWQ_OK;
+    if (T < 1) return GLOWQ_ERR_SHAPE;
+    if (x == nullptr || row_token_dev == nullptr || rows == nullptr) return GLOWQ_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || !aligned(row_token_dev, 4) || !aligned(rows, 16)) return GLOWQ_ERR_ALIGN;
+    const int w = validate_moe_workspace(workspace, workspace_bytes, kWsHeader);
+    if (w != GLOWQ_OK) return w;
+    RowsArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.x = x;
+    a.row_token = row_token_dev;
+    a.out = rows;
+    a.T = (int32_t)T;
+    a.top_k = 1;
+    a.n_rows = (int32_t)n_rows;
+    a.d = d;
+    a.dtype = dtype;
+    a.err = error_word(workspace);
+    return launch_moe_dispatch(a, stream) == hipSuccess ? GLOWQ_OK : GLOWQ_ERR_HIP;
+}
+
+int glowq_moe_combine(const void* rows, int64_t n_rows, const int32_t* pair_row_dev, const float* weights_dev,
+                      const void* add, int64_t T, int64_t top_k, int64_t d, int32_t dtype, void* y, void* workspace,
+                      size_t workspace_bytes, hipStream_t stream) {
+    const int v = validate_rows(T, top_k, n_rows, d, dtype);
+    if (v != GLOWQ_OK) return v;
+    if (T == 0) return GLOWQ_OK;
+    if ((n_rows > 0 && rows == nullptr) || pair_row_dev == nullptr || y == nullptr) return GLOWQ_ERR_INVALID_ARG;
+    if (!aligned(rows, 16) || !aligned(pair_row_dev, 4) || !aligned(weights_dev, 4) || !aligned(add, 16) || !aligned(y, 16))
+        return GLOWQ_ERR_ALIGN;
+    const int w = validate_moe_workspace(workspace, workspace_bytes, kWsHeader);
+    if (w != GLOWQ_OK) return w;
+    RowsArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.x = rows;
+    a.add = add;
+    a.pair_row = pair_row_dev;
+    a.w = weights_dev;
+    a.out = y;
+    a.T = (int32_t)T;
+    a.top_k = (int32_t)top_k;
+    a.n_rows = (int32_t)n_rows;
+    a.d = d;
+    a.dtype = dtype;
+    a.err = error_word(workspace);
+    return launch_moe_combine(a, stream) == hipSuccess ? GLOWQ_OK : GLOWQ_ERR_HIP;
+}
+
+int glowq_moe_combine_backward(const void* dy, const void* rows, int64_t n_rows, const int32_t* pair_row_dev,
+                               const int32_t* row_token_dev, const float* weights_dev, int64_t T, int64_t top_k, int64_t d,
+                               int32_t dtype, void* d_rows, float* d_weights_dev, void* workspace, size_t workspace_bytes,
+                               hipStream_t stream) {
+    const int v = validate_rows(T, top_k, n_rows, d, dtype);
+    if (v != GLOWQ_OK) return v;
+    if (T == 0) return GLOWQ_OK;
+    if (dy == nullptr || pair_row_dev == nullptr || d_weights_dev == nullptr ||
+        (n_rows > 0 && (rows == nullptr || row_token_dev == nullptr || d_rows == nullptr)))
+        return GLOWQ_ERR_INVALID_ARG;
+    if (!aligned(dy, 16) || !aligned(rows, 16) || !aligned(pair_row_dev, 4) || !aligned(row_token_dev, 4) ||
+        !aligned(weights_dev, 4) || !aligned(d_rows, 16) || !aligned(d_weights_dev, 4))
+        return GLOWQ_ERR_ALIGN;
+    const int w = validate_moe_workspace(workspace, workspace_bytes, kWsHeader);
+    if (w != GLOWQ_OK) return w;
+    RowsArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.x = dy;
+    a.rows = rows;
+    a.row_token = row_token_dev;
+    a.pair_row = pair_row_dev;
+    a.w = weights_dev;
+    a.out = d_rows;
+    a.dw = d_weights_dev;
+    a.T = (int32_t)T;
+    a.top_k = (int32_t)top_k;
+    a.n_rows = (int32_t)n_rows;
+    a.d = d;
+    a.dtype = dtype;
+    a.err = error_word(workspace);
+    return launch_moe_combine_backward(a, stream) == hipSuccess ? GLOWQ_OK : GLOWQ_ERR_HIP;
+}
+
+int glowq_swiglu(const void* gate, const void* up, int64_t n, int32_t dtype, void* h, hipStream_t stream) {
+    if (dtype != GLOWQ_DTYPE_F16 && dtype != GLOWQ_DTYPE_F32) return GLOWQ_ERR_INVALID_ARG;
+    if (n < 0) return GLOWQ_ERR_SHAPE;
+    if (n > kMaxGateElems) return GLOWQ_ERR_UNSUPPORTED;
+    if (n == 0) return GLOWQ_OK;
+    if (gate == nullptr || up == nullptr || h == nullptr) return GLOWQ_ERR_INVALID_ARG;
+    if (!aligned(gate, 16) || !aligned(up, 16) || !aligned(h, 16)) return GLOWQ_ERR_ALIGN;
+    return launch_swiglu(gate, up, n, dtype, h, stream) == hipSuccess ? GLOWQ_OK : GLOWQ_ERR_HIP;
+}
+
+int glowq_swiglu_backward(const void* dh, const void* gate, const void* up, int64_t n, int32_t dtype, void* d_gate,
+                          void* d_up, hipStream_t stream) {
+    if (dtype != GLOWQ_DTYPE_F16 && dtype != GLOWQ_DTYPE_F32) return GLOWQ_ERR_INVALID_ARG;
+    if (n < 0) return GLOWQ_ERR_SHAPE;
+    if (n > kMaxGateElems) return GLOWQ_ERR_UNSUPPORTED;
+    if (n == 0) return GLOWQ_OK;
+    if (dh == nullptr || gate == nullptr || up == nullptr || d_gate == nullptr || d_up == nullptr)
+        return GLOWQ_ERR_INVALID_ARG;
+    if (!aligned(dh, 16) || !aligned(gate, 16) || !aligned(up, 16) || !aligned(d_gate, 16) || !aligned(d_up, 16))
+        return GLOWQ_ERR_ALIGN;
+    return launch_swiglu_backward(dh, gate, up, n, dtype, d_gate, d_up, stream) == hipSuccess ? GLOWQ_OK : GLOWQ_ERR_HIP;
+}
+
+size_t glowq_w8_q_bytes(int64_t n_out, int64_t k_in) {
+    if (n_out < 1 || n_out > kMaxRows || k_in < kGroup || k_in % kGroup != 0 || k_in > kW8MaxD) return 0;
+    return (size_t)ceil_div(n_out, 16) * (size_t)(k_in / kGroup) * (size_t)kW8Block;
+}
+
+size_t glowq_w8_sz_bytes(int64_t n_out) {
+    if (n_out < 1 || n_out > kMaxRows) return 0;
+    return (size_t)ceil_div(n_out, 16) * 64u;
+}
+
+int glowq_repack_w8(const void* codes_dev, const float* scales_dev, int64_t n_out, int64_t k_in, void* q_dev,
+                    void* sz_dev, int32_t* flag_dev, hipStream_t stream) {
+    if (!codes_dev || !scales_dev || !q_dev || !sz_dev || !flag_dev) return GLOWQ_ERR_INVALID_ARG;
+    if (n_out < 1 || k_in < kGroup || k_in % kGroup != 0) return GLOWQ_ERR_SHAPE;
+    if (n_out > kMaxRows || k_in > kW8MaxD) return GLOWQ_ERR_UNSUPPORTED;
+    if (!aligned(codes_dev, 16) || !aligned(scales_dev, 4) || !aligned(q_dev, 16) || !aligned(sz_dev, 16) ||
+        !aligned(flag_dev, 4))
+        return GLOWQ_ERR_ALIGN;
+    if (launch_flag_clear(flag_dev, stream) != hipSuccess) return GLOWQ_ERR_HIP;
+    if (launch_repack_w8(static_cast<const int8_t*>(codes_dev), scales_dev, n_out, k_in, static_cast<uint8_t*>(q_dev),
+                         static_cast<float*>(sz_dev), flag_dev, stream) != hipSuccess)
+        return GLOWQ_ERR_HIP;
+    int32_t flag = 0;
+    if (hipMemcpyAsync(&flag, flag_dev, sizeof(flag), hipMemcpyDeviceToHost, stream) != hipSuccess)
+        return GLOWQ_ERR_HIP;
+    if (hipStreamSynchronize(stream) != hipSuccess) return GLOWQ_ERR_HIP;
+    return flag ? GLOWQ_ERR_RANGE : GLOWQ_OK;
+}
+
+size_t glowq_w8a8_workspace_bytes(int64_t T, int64_t d, int32_t r) {
+    if (T <= 0 || T > kMaxT || d < kGroup || d % kGroup != 0 || d > kW8MaxD || r < 0 || r > GLOWQ_MAX_RANK) return 0;
+    size_t n = round256((size_t)T * d) + round256((size_t)T * 4u);
+    if (r > 0) n += prefill_r_bytes(T, r, 1) + prefill_part_bytes(T, r, 1);
+    return n;
+}
+
+int glowq_group_forward_w8a8(const void* x, int64_t T, int64_t d, int32_t m, const glowq_qweight* w,
+                             const void* b_shared, const void* const* a, int32_t r, int32_t restore,
+                             void* workspace, size_t workspace_bytes, void* const* y, hipStream_t stream) {
+    const void* bp[1] = {b_shared};
+    Call c = make_group(x, T, d, m, w, bp, 1, a, r, restore, y);
+    c.w8a8 = true;
+    const int v = validate(c, workspace, workspace_bytes);
+    if (v != GLOWQ_OK) return v;
+    return run_w8a8(c, workspace, stream);
 }
 
 size_t glowq_q_bytes(int64_t n_out, int64_t k_in) {

@@ -1,0 +1,18 @@
+// The 8-bit integer group forward (w8a8.hip): layout constants and launchers.
+#pragma once
+
+#include "glowq_internal.h"
+
+namespace glowq {
+
+constexpr int kFmtInt8 = 4;        // GLOWQ_FMT_INT8_CHANNEL
+constexpr int kW8Block = 2048;     // bytes of one 16-row x 128-input weight block
+constexpr int kW8Waves = 8;        // wavefronts that split the input groups of a small tile
+constexpr int64_t kW8MaxD = 16384; // a token's row in the quantiser's registers; int32 sums exact
+
+hipError_t launch_repack_w8(const int8_t* codes, const float* scales, int64_t n_out, int64_t k_in, uint8_t* q, float* sz,
+                            int32_t* flag, hipStream_t stream);
+hipError_t launch_quant_q8(const _Float16* x, int T, int d, int8_t* xq, float* xscale, hipStream_t stream);
+hipError_t launch_w8a8(const ForwardArgs& a, hipStream_t stream);
+
+}  // namespace glowq

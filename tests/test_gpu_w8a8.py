@@ -1,0 +1,194 @@
+"""8-bit integer group forward (glowq_group_forward_w8a8) against a plain fp64 reference: exact token
+codes and scales in the workspace, every output within the bound of its roundings."""
+import numpy as np
+import pytest
+import torch
+
+import layer_ref as R
+from gpu_util import glowq, log
+from oracle import glowq_ref as G
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    glowq()
+    yield
+    torch.cuda.synchronize()
+
+
+class Unit:
+    """Seeded int8 modules over d inputs with factors of rank r."""
+
+    def __init__(self, T, d, rows, r, seed, extremes=False):
+        gen = torch.Generator().manual_seed(seed)
+        rn = lambda *s: torch.randn(*s, generator=gen)
+        self.T, self.d, self.rows, self.r = T, d, rows, r
+        self.x = (rn(T, d) * (0.2 + rn(1, d).abs())).half()
+        self.codes = [torch.randint(-128, 128, (n, d), generator=gen, dtype=torch.int32).to(torch.int8) for n in rows]
+        if extremes:
+            for q in self.codes:
+                q[0] = -128
+                q[-1] = 127
+        self.scales = [0.001 + 0.002 * torch.rand(n, generator=gen) for n in rows]
+        self.b = (rn(r, d) / d ** 0.5).half()
+        self.a = [(rn(n, r) * 0.3).half() for n in rows]
+        g = glowq()
+        self.w = [g.QWeight.from_int8(q, s) for q, s in zip(self.codes, self.scales)]
+
+    def run(self, restore=True, x=None, **kw):
+        g = glowq()
+        x = self.x.cuda() if x is None else x
+        on = restore and self.r > 0
+        return g.group_forward_w8a8(x, self.w, self.b.cuda() if on else None, [t.cuda() for t in self.a] if on else [],
+                                    self.r, restore, **kw)
+
+    def check(self, ys, restore, what, rows=None):
+        x = self.x if rows is None else self.x[rows]
+        ref, bound = R.w8a8(x, self.codes, self.scales, self.b, self.a, restore and self.r > 0)
+        for i, (y, yr, bd) in enumerate(zip(ys, ref, bound)):
+            R.within(y if rows is None else y[rows], yr, bd, f"{what} module {i}")
+
+
+# one token to several token tiles of every kernel, ragged tokens and rows, one to eight modules,
+# one input group (d = 128) to many, ranks that fill no, part of and several correction steps
+SHAPES = [(1, 128, [16], 0), (1, 256, [1], 8), (1, 4096, [520, 17, 130], 64), (2, 384, [40, 24], 8), (15, 1152, [100], 24),
+          (16, 1024, [520, 17], 64), (17, 512, [96, 64, 40], 32), (31, 640, [33] * 8, 16), (33, 640, [100], 24),
+          (48, 2176, [300], 128), (64, 1024, [1024, 512, 512], 64), (65, 256, [48, 32], 16), (130, 384, [300, 200], 40),
+          (300, 512, [2048, 2048], 128), (8, 2048, [64], 256), (257, 896, [1030, 515], 64), (513, 128, [770], 256),
+          (700, 1280, [2050], 8), (96, 14336, [272], 64), (5, 16384, [48], 64)]
+
+
+@pytest.mark.parametrize("T,d,rows,r", SHAPES)
+def test_w8a8_matches_reference(T, d, rows, r):
+    u = Unit(T, d, rows, r, 1000 + T + d)
+    g = glowq()
+    for restore in (True, False):
+        n = g.w8a8_workspace_bytes(T, d, r if restore else 0)
+        ws = torch.full((n,), 0x5A, dtype=torch.uint8, device="cuda")  # the contents need no initialisation
+        log(f"w8a8 T={T} d={d} rows={rows} r={r} restore={restore}")
+        ys = u.run(restore, workspace=ws)
+        torch.cuda.synchronize()
+        codes, scale = G.quantize_x_int8(u.x)
+        raw = ws.cpu().numpy()
+        assert np.array_equal(raw[: T * d].view(np.int8).reshape(T, d), codes)
+        o = (T * d + 255) // 256 * 256
+        assert np.array_equal(raw[o: o + 4 * T].view(np.uint32), scale.astype(np.float32).reshape(-1).view(np.uint32))
+        u.check(ys, restore, f"restore={restore}")
+
+
+def test_w8a8_large_grid():
+    """Many tiles of every size: 2048 tokens on 4096 + 1000 rows, sampled tokens against the reference."""
+    u = Unit(2048, 512, [4096, 1000], 64, 7)
+    rows = torch.tensor([0, 1, 127, 128, 1000, 1023, 1024, 2047])
+    u.check(u.run(True), True, "large", rows)
+
+
+def test_w8a8_largest_sums_are_exact():
+    """d = 16384 with every weight code -128 or 127 and equal activations: the largest int32 sums."""
+    T, d = 18, 16384
+    u = Unit(T, d, [32], 0, 8, extremes=True)
+    u.codes[0][: 16] = -128
+    u.codes[0][16:] = 127
+    u.x = torch.ones(T, d).half()
+    u.x[3] = -1.0
+    g = glowq()
+    u.w = [g.QWeight.from_int8(u.codes[0], u.scales[0])]
+    u.check(u.run(False), False, "extremes")
+
+
+@pytest.mark.parametrize("T", [3, 20, 70, 300])
+def test_w8a8_zero_and_non_finite_tokens(T):
+    """A zero token: zeros plus its (zero) correction.  A token with an infinity or a NaN: NaN in its
+    own rows, no other row changed."""
+    u = Unit(T, 512, [96, 33], 16, 9)
+    u.x[1] = 0
+    for restore in (True, False):
+        clean = u.run(restore)
+        u.check(clean, restore, f"zero token restore={restore}")
+        x = u.x.clone()
+        x[0, 5] = float("inf")
+        x[2, 511] = float("nan")
+        ys = u.run(restore, x=x.cuda())
+        for y, c in zip(ys, clean):
+            assert torch.isnan(y[0]).all() and torch.isnan(y[2]).all()
+            assert torch.equal(y[1], c[1]) and torch.equal(y[3:], c[3:])
+
+
+@pytest.mark.parametrize("T", [2, 70])
+def test_w8a8_overflowing_outputs_are_infinite(T):
+    u = Unit(T, 256, [40], 0, 10)
+    big = [s * 3e6 for s in u.scales]
+    g = glowq()
+    u.w = [g.QWeight.from_int8(u.codes[0], big[0])]
+    y = u.run(False)[0].cpu()
+    ref, _ = R.w8a8(u.x, u.codes, big, None, [], False)
+    far = np.abs(ref[0]) > 66000.0
+    assert far.any() and torch.isinf(y[torch.from_numpy(far)]).all()
+    assert np.array_equal(np.sign(ref[0][far]), np.sign(y.double().numpy()[far]))
+
+
+def test_w8a8_empty_and_repeatable():
+    u = Unit(40, 384, [72, 16], 32, 11)
+    assert [tuple(y.shape) for y in u.run(True, x=u.x.cuda()[:0])] == [(0, 72), (0, 16)]
+    a, b = u.run(True), u.run(True)
+    for s, t in zip(a, b):
+        assert torch.equal(s, t)
+
+
+@pytest.mark.parametrize("T", [1, 16, 33, 100, 600])
+def test_w8a8_tokens_do_not_depend_on_the_batch(T):
+    """The integer sums are exact whatever the tile: without the correction a token's row is the same
+    bit for bit in every batch size."""
+    u = Unit(600, 1024, [400], 0, 12)
+    full = u.run(False)[0]
+    part = u.run(False, x=u.x.cuda()[:T].contiguous())[0]
+    assert torch.equal(part, full[:T])
+
+
+def test_w8a8_repack_rejects_non_finite_scales():
+    g = glowq()
+    for v in (float("inf"), float("nan")):
+        s = torch.ones(20)
+        s[13] = v
+        with pytest.raises(g.GlowQError) as e:
+            g.QWeight.from_int8(torch.zeros(20, 128, dtype=torch.int8), s)
+        assert e.value.status == g.ERR_RANGE
+
+
+@pytest.mark.parametrize("T", [1, 40, 400])
+def test_w8a8_graph_replays_and_streams(T):
+    """A captured call replayed with new inputs and eager calls between, and a call on another stream
+    than the current one, equal the eager call bit for bit."""
+    u = Unit(T, 1024, [272, 48], 64, 13)
+    g = glowq()
+    x = u.x.cuda()
+    b, a = u.b.cuda(), [t.cuda() for t in u.a]
+    ws = torch.empty(g.w8a8_workspace_bytes(T, 1024, 64), dtype=torch.uint8, device="cuda")
+    ys = [torch.empty(T, n, dtype=torch.float16, device="cuda") for n in u.rows]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        g.group_forward_w8a8(x, u.w, b, a, 64, workspace=ws, y=ys)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            g.group_forward_w8a8(x, u.w, b, a, 64, workspace=ws, y=ys)
+    torch.cuda.current_stream().wait_stream(s)
+    for k in range(4):
+        x.copy_(torch.roll(u.x.cuda(), k, 1))
+        want = g.group_forward_w8a8(x, u.w, b, a, 64)
+        for y in ys:
+            y.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        for y, v in zip(ys, want):
+            assert torch.equal(y, v), k
+    other = torch.cuda.Stream()
+    other.wait_stream(torch.cuda.current_stream())
+    got = g.group_forward_w8a8(x, u.w, b, a, 64, stream=other)
+    other.synchronize()
+    for y, v in zip(got, want):
+        assert torch.equal(y, v)
