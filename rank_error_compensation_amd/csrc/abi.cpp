@@ -516,10 +516,31 @@ int run_w4a8(const Call& c, void* workspace, hipStream_t stream) {
     return (c.mx8 ? launch_mx8(f, stream) : launch_w4a8(f, stream)) == hipSuccess ? GLOWQ_OK : GLOWQ_ERR_HIP;
 }
 
-// W8A8 tile: 16 to 64 tokens by one or two 16-row tiles per workgroup.
-void choose_w8a8_shape(const Call& c, int& tt, int& rr) {
-    tt = c.T <= 16 ? 1 : (c.T <= 32 ? 2 : 4);
-    rr = tt == 1 ? 1 : 2;
+// K ranges' int32 tiles of a call of more than 64 tokens: bounded by the workspace that
+// glowq_w8a8_workspace_bytes reserves for them.
+constexpr size_t kW8PartBytes = (size_t)32 << 20;
+constexpr int64_t kW8TileMinT = 65;
+
+W8Shape choose_w8a8_shape(const Call& c) {
+    W8Shape s = {c.T <= 16 ? 1 : (c.T <= 32 ? 2 : 4), c.T <= 16 ? 1 : 2, 1, (int)(c.d / kGroup), 0};
+    if (c.T < kW8TileMinT) return s;
+    auto tiles = [&](int tt, int rr) {
+        int64_t n = 0;
+        for (int i = 0; i < c.m; ++i) n += ceil_div(ceil_div(c.w[i].n_out, 16), rr);
+        return n * ceil_div(c.T, 16 * tt);
+    };
+    s.tt = s.rr = 16;
+    if (tiles(16, 16) >= 256) return s;
+    s.tt = s.rr = 8;
+    const int64_t n = tiles(8, 8), G = c.d / kGroup;
+    if (n < 256) {
+        int64_t ks = std::min<int64_t>(ceil_div(256, n), std::max<int64_t>(1, G / 8));
+        while (ks > 1 && (size_t)(n * ks) * 65536u > kW8PartBytes) --ks;
+        s.gk = (int)ceil_div(G, ks);
+        s.ks = (int)ceil_div(G, s.gk);
+        if (s.ks > 1) s.part = (size_t)(n * s.ks) * 65536u;
+    }
+    return s;
 }
 
 // W8A8 form.  Workspace: codes int8 [T][d] | scales fp32 [T] | projection and its split-K partials.
@@ -547,10 +568,13 @@ int run_w8a8(const Call& c, void* workspace, hipStream_t stream) {
     f.xq = xq;
     f.xscale = xscale;
     f.fmt = kFmtInt8;
-    int tt = 1, rr = 1;
-    choose_w8a8_shape(c, tt, rr);
-    f.tile_tt = tt;
-    f.tile_rr = rr;
+    const W8Shape s = choose_w8a8_shape(c);
+    f.tile_tt = s.tt;
+    f.tile_rr = s.rr;
+    f.tile_ks = s.ks;
+    f.dec_gk = s.gk;
+    if (c.correct) base += prefill_r_bytes(c.T, c.r, 1) + prefill_part_bytes(c.T, c.r, 1);
+    f.ypart = reinterpret_cast<float*>(base);
     int64_t tiles = 0;
     for (int i = 0; i < c.m; ++i) {
         ModuleArgs& M = f.mod[i];
@@ -562,10 +586,11 @@ int run_w8a8(const Call& c, void* workspace, hipStream_t stream) {
         M.n_tiles16 = (int32_t)ceil_div(c.w[i].n_out, 16);
         M.tile_begin = (int32_t)tiles;
         f.tile_begin[i] = (int32_t)tiles;
-        tiles += ceil_div(M.n_tiles16, rr);
+        tiles += ceil_div(M.n_tiles16, s.rr);
     }
-    f.m_tiles = (int32_t)ceil_div(c.T, 16 * tt);
-    f.n_tiles = (int32_t)(tiles * f.m_tiles);
+    f.m_tiles = (int32_t)ceil_div(c.T, 16 * s.tt);
+    // small tiles: work tiles of the launch; large ones: columns (row blocks x K ranges)
+    f.n_tiles = (int32_t)(s.rr >= 8 ? tiles * s.ks : tiles * f.m_tiles);
     return launch_w8a8(f, stream) == hipSuccess ? GLOWQ_OK : GLOWQ_ERR_HIP;
 }
 
@@ -923,6 +948,7 @@ size_t glowq_w8a8_workspace_bytes(int64_t T, int64_t d, int32_t r) {
     if (T <= 0 || T > kMaxT || d < kGroup || d % kGroup != 0 || d > kW8MaxD || r < 0 || r > GLOWQ_MAX_RANK) return 0;
     size_t n = round256((size_t)T * d) + round256((size_t)T * 4u);
     if (r > 0) n += prefill_r_bytes(T, r, 1) + prefill_part_bytes(T, r, 1);
+    if (T >= kW8TileMinT) n += kW8PartBytes;
     return n;
 }
 

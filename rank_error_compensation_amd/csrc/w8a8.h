@@ -8,7 +8,16 @@ namespace glowq {
 constexpr int kFmtInt8 = 4;        // GLOWQ_FMT_INT8_CHANNEL
 constexpr int kW8Block = 2048;     // bytes of one 16-row x 128-input weight block
 constexpr int kW8Waves = 8;        // wavefronts that split the input groups of a small tile
+// Large tiles, as ForwardArgs::tile_rr row tiles per workgroup: 16 is 256 tokens x 256 rows on eight
+// wavefronts, 8 is 128 x 128 on four.
 constexpr int64_t kW8MaxD = 16384; // a token's row in the quantiser's registers; int32 sums exact
+
+// Launch shape of a call.
+struct W8Shape {
+    int tt, rr;      // 16-token tiles and 16-row tiles per workgroup
+    int ks, gk;      // K ranges over workgroups, input groups per range
+    size_t part;     // bytes of the ranges' int32 tiles
+};
 
 hipError_t launch_repack_w8(const int8_t* codes, const float* scales, int64_t n_out, int64_t k_in, uint8_t* q, float* sz,
                             int32_t* flag, hipStream_t stream);

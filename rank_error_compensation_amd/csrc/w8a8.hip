@@ -15,6 +15,8 @@
 // operand m, lane l (16 bytes at 1024 m + 16 l) is row 16 rt + l % 16, inputs 128 g + 64 m +
 // 16 (l / 16) .. + 15.  Activation codes stay in their natural order [T][d], whose 16-byte pieces
 // are the other operand.  Scales: 16 fp32 per row tile.  Rows >= n_out are zero.
+#include <type_traits>
+
 #include "glowq_internal.h"
 #include "w8a8.h"
 
@@ -26,6 +28,19 @@ namespace {
 
 __device__ __forceinline__ i4v mfma_i8(i4v a, i4v b, i4v c) {
     return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
+}
+
+// Four consecutive rows of token t, rounded to fp16.
+__device__ __forceinline__ void store_rows(const ModuleArgs& M, int t, int row0, const f4& v) {
+    _Float16* yrow = M.y + (size_t)t * M.n_out;
+    if ((M.n_out & 3) == 0 && row0 + 3 < M.n_out) {
+        const h2 lo = {(_Float16)v[0], (_Float16)v[1]}, hi = {(_Float16)v[2], (_Float16)v[3]};
+        *reinterpret_cast<u2*>(yrow + row0) = u2{as_u32(lo), as_u32(hi)};
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (row0 + i < M.n_out) yrow[row0 + i] = (_Float16)v[i];
+    }
 }
 
 // --------------------------------------------------------------------- load step
@@ -204,16 +219,252 @@ __global__ __launch_bounds__(64 * kW8Waves) void w8a8_split_kernel(const Forward
             v = mfma16(av, bv, v);
         }
     }
-    if (!ok) return;
-    _Float16* yrow = M.y + (size_t)t * M.n_out;
-    if ((M.n_out & 3) == 0 && row0 + 3 < M.n_out) {
-        const h2 lo = {(_Float16)v[0], (_Float16)v[1]}, hi = {(_Float16)v[2], (_Float16)v[3]};
-        *reinterpret_cast<u2*>(yrow + row0) = u2{as_u32(lo), as_u32(hi)};
-    } else {
+    if (ok) store_rows(M, t, row0, v);
+}
+
+// --------------------------------------------------------------------- large tiles
+// 16 TT WM tokens x 64 WN rows per workgroup: WM x WN wavefronts, each 16 TT tokens x 4 row tiles.
+// The token codes of an input group (128 bytes a token) go HBM/L2 -> LDS by the load unit into a ring
+// of four stages; a wavefront's weight operands come straight into registers, one group ahead (the WM
+// wavefronts that share rows find them in the L1 cache), so that LDS carries only the codes: a code
+// byte read feeds 4 matrix-core steps.  In a stage, row r keeps its 16-byte chunk c at position
+// c ^ f(r), f(r) = (r % 8) ^ ((r / 8) % 2): the 16 rows of an operand read fall in distinct banks.
+// Tokens past T read token T - 1 and row tiles past the module its last tile; neither is stored.
+//
+// With args.tile_ks > 1 the input groups are split over workgroups: each writes its exact int32
+// tile to the workspace, and w8a8_join_kernel adds them and finishes.
+typedef __attribute__((address_space(3))) void lds_void;
+template <int I>
+using ic = std::integral_constant<int, I>;
+
+// Column of the launch (row block of a module and K range) and token block of a workgroup: XCD x
+// (workgroups b with b % 8 == x) takes the columns x, x + 8, ..., eight token blocks at a time, so
+// that a column's weights stay in one L2 and its workgroups run together.
+__device__ __forceinline__ bool w8_place(const ForwardArgs& args, int& mb, int& col) {
+    const int cols = args.n_tiles, MT = args.m_tiles;
+    const int xcd = blockIdx.x & 7, local = blockIdx.x >> 3;
+    const int mine = (cols - xcd + 7) >> 3;  // columns of this XCD
+    if (mine <= 0) return false;
+    const int per = 8 * mine;
+    const int ms = local / per, in = local - ms * per;
+    const int width = min(8, MT - 8 * ms);
+    if (width <= 0) return false;
+    const int c = in / width;
+    if (c >= mine) return false;
+    mb = 8 * ms + (in - c * width);
+    col = xcd + 8 * c;
+    return true;
+}
+
+template <int WM, int WN, int TT>
+__global__ __launch_bounds__(64 * WM * WN, WM * WN <= 4 ? 2 : 1) void w8a8_tile_kernel(const ForwardArgs args) {
+    constexpr int RR = 4, NW = WM * WN, BM = 16 * TT * WM, SB = BM * 128;
+    constexpr int NC = BM / 8 / NW;  // 1 KB code copies per wavefront and group
+    static_assert(NC * 8 * NW == BM && NC + 2 * RR < 64, "copies");
+    __shared__ __attribute__((aligned(16))) uint8_t st0[SB];
+    __shared__ __attribute__((aligned(16))) uint8_t st1[SB];
+    __shared__ __attribute__((aligned(16))) uint8_t st2[SB];
+    __shared__ __attribute__((aligned(16))) uint8_t st3[SB];
+    int mb, col;
+    if (!w8_place(args, mb, col)) return;
+    const int ks = args.tile_ks, nbl = col / ks, kr = col - nbl * ks;
+    const ModuleArgs M = args.mod[module_of(args, nbl)];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int wm = wave % WM, wn = wave / WM;
+    const int T = args.T, d = args.d, NT = M.n_tiles16;
+    const int m0 = mb * BM, rt0 = (nbl - M.tile_begin) * RR * WN + wn * RR;
+    const int g_begin = kr * args.dec_gk, g_end = min(g_begin + args.dec_gk, args.G);
+
+    // code copy i of wave w fills rows 8 (NC w + i) .. + 7 of the stage; lane l lands at row + l / 8,
+    // position l % 8, holding the row's chunk (l % 8) ^ f(row)
+    uint32_t xoff[NC];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (row0 + i < M.n_out) yrow[row0 + i] = (_Float16)v[i];
+    for (int i = 0; i < NC; ++i) {
+        const int row = 8 * (NC * wave + i) + (lane >> 3);
+        const int f = (row & 7) ^ ((row >> 3) & 1);
+        xoff[i] = (uint32_t)(min(m0 + row, T - 1) * d + 16 * ((lane & 7) ^ f));
     }
+    const int fr = (lane & 7) ^ ((lane >> 3) & 1);
+    const int rbase = (16 * TT * wm + (lane & 15)) * 128;
+    const int rofs0 = rbase + 16 * ((lane >> 4) ^ fr), rofs1 = rbase + 16 * ((4 + (lane >> 4)) ^ fr);
+    const int rtb = min(rt0, NT - 1);
+    uint32_t woff[RR];
+#pragma unroll
+    for (int rr = 0; rr < RR; ++rr) woff[rr] = (uint32_t)((min(rt0 + rr, NT - 1) - rtb) * kW8Block + lane * 16);
+
+    auto copy = [&](int g, uint8_t* stg) {
+        const int8_t* xb = args.xq + (size_t)min(g, g_end - 1) * kGroup;
+#pragma unroll
+        for (int i = 0; i < NC; ++i)
+            __builtin_amdgcn_global_load_lds((const void*)(xb + xoff[i]), (lds_void*)(stg + 8 * (NC * wave + i) * 128), 16, 0,
+                                             0);
+    };
+    i4v w[2][RR][2];
+    auto wload = [&](int g, int slot) {
+        const uint8_t* qb = M.q + ((size_t)min(g, g_end - 1) * NT + rtb) * kW8Block;
+#pragma unroll
+        for (int rr = 0; rr < RR; ++rr)
+#pragma unroll
+            for (int m = 0; m < 2; ++m) w[slot][rr][m] = *reinterpret_cast<const i4v*>(qb + woff[rr] + 1024 * m);
+    };
+    i4v acc[TT][RR];
+#pragma unroll
+    for (int tt = 0; tt < TT; ++tt)
+#pragma unroll
+        for (int rr = 0; rr < RR; ++rr) acc[tt][rr] = i4v{0, 0, 0, 0};
+
+    copy(g_begin, st0);
+    wload(g_begin, 0);
+    copy(g_begin + 1, st1);
+
+    // group g in stage S = (g - g_begin) % 4, weights in slot S % 2.  At the barrier the copies of g and
+    // the weights of g have landed: only the NC copies of g + 1, issued last, may be in flight.  Then
+    // the weights of g + 1 and the copies of g + 2 are issued; their stage was last read in group g - 2.
+    auto step = [&](int g, auto Sc) {
+        constexpr int S = decltype(Sc)::value;
+        uint8_t* cur = S == 0 ? st0 : (S == 1 ? st1 : (S == 2 ? st2 : st3));
+        uint8_t* nxt = S == 0 ? st2 : (S == 1 ? st3 : (S == 2 ? st0 : st1));
+        __builtin_amdgcn_s_waitcnt(0x0F70 | NC);  // vmcnt(NC)
+        __builtin_amdgcn_s_barrier();
+        wload(g + 1, (S + 1) & 1);
+        __builtin_amdgcn_sched_barrier(0);
+        copy(g + 2, nxt);
+        __builtin_amdgcn_sched_barrier(0);
+        i4v x[2][2];
+        x[0][0] = *reinterpret_cast<const i4v*>(cur + rofs0);
+        x[0][1] = *reinterpret_cast<const i4v*>(cur + rofs1);
+#pragma unroll
+        for (int tt = 0; tt < TT; ++tt) {
+            if (tt + 1 < TT) {
+                x[(tt + 1) & 1][0] = *reinterpret_cast<const i4v*>(cur + rofs0 + (tt + 1) * 2048);
+                x[(tt + 1) & 1][1] = *reinterpret_cast<const i4v*>(cur + rofs1 + (tt + 1) * 2048);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int rr = 0; rr < RR; ++rr) acc[tt][rr] = mfma_i8(w[S & 1][rr][m], x[tt & 1][m], acc[tt][rr]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    int g = g_begin;
+    for (; g + 4 <= g_end; g += 4) {
+        step(g, ic<0>{});
+        step(g + 1, ic<1>{});
+        step(g + 2, ic<2>{});
+        step(g + 3, ic<3>{});
+    }
+    if (g < g_end) step(g, ic<0>{});
+    if (g + 1 < g_end) step(g + 1, ic<1>{});
+    if (g + 2 < g_end) step(g + 2, ic<2>{});
+    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): no copy may land in LDS after the workgroup ends
+
+    if (ks > 1) {
+        i4v* part = reinterpret_cast<i4v*>(args.ypart) + ((((size_t)mb * (args.n_tiles / ks) + nbl) * ks + kr) * NW + wave) * (TT * RR * 64);
+#pragma unroll
+        for (int tt = 0; tt < TT; ++tt)
+#pragma unroll
+            for (int rr = 0; rr < RR; ++rr) part[(tt * RR + rr) * 64 + lane] = acc[tt][rr];
+        return;
+    }
+    const int tok0 = m0 + 16 * TT * wm + (lane & 15);
+    f4 v[TT][RR];
+    f4 sw[RR];
+#pragma unroll
+    for (int rr = 0; rr < RR; ++rr)
+        sw[rr] = *reinterpret_cast<const f4*>(M.sz + (size_t)min(rt0 + rr, NT - 1) * 64 + 16 * (lane >> 4));
+#pragma unroll
+    for (int tt = 0; tt < TT; ++tt) {
+        const int t = tok0 + 16 * tt;
+        const float st = args.xscale[min(t, T - 1)];
+#pragma unroll
+        for (int rr = 0; rr < RR; ++rr)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[tt][rr][i] = (float)acc[tt][rr][i] * sw[rr][i] * st;
+    }
+    if (args.r > 0 && M.a != nullptr) {
+        const int r = args.r, rp = args.r_pad, kofs = 8 * (lane >> 4);
+        const _Float16* R = reinterpret_cast<const _Float16*>(args.R);
+        const h8 zero8 = {0, 0, 0, 0, 0, 0, 0, 0};
+        for (int kb = 0; kb < rp / 32; ++kb) {
+            const int c = 32 * kb + kofs;
+            h8 av[RR];
+#pragma unroll
+            for (int rr = 0; rr < RR; ++rr) {
+                const int row = (rt0 + rr) * 16 + (lane & 15);
+                av[rr] = (row < M.n_out && c < r) ? load_h8(M.a + (size_t)row * r + c) : zero8;
+            }
+#pragma unroll
+            for (int tt = 0; tt < TT; ++tt) {
+                const int t = tok0 + 16 * tt;
+                const h8 bv = t < T ? load_h8(R + (size_t)t * rp + c) : zero8;
+#pragma unroll
+                for (int rr = 0; rr < RR; ++rr) v[tt][rr] = mfma16(av[rr], bv, v[tt][rr]);
+            }
+        }
+    }
+#pragma unroll
+    for (int tt = 0; tt < TT; ++tt) {
+        const int t = tok0 + 16 * tt;
+        if (t >= T) continue;
+#pragma unroll
+        for (int rr = 0; rr < RR; ++rr)
+            if (rt0 + rr < NT) store_rows(M, t, (rt0 + rr) * 16 + 4 * (lane >> 4), v[tt][rr]);
+    }
+}
+
+// Sums of the K ranges of one 16-token x 64-row piece per wavefront (pieces numbered as the tile
+// kernel stores them), scales, correction, one rounding to fp16.
+__global__ __launch_bounds__(256) void w8a8_join_kernel(const ForwardArgs args, int wm_n, int wn_n, int tt_n, int pieces) {
+    constexpr int RR = 4;
+    const int lane = threadIdx.x & 63;
+    const int piece = (int)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    if (piece >= pieces) return;
+    const int nw = wm_n * wn_n, ks = args.tile_ks, cols = args.n_tiles / ks;
+    const int tt = piece % tt_n, wave = piece / tt_n % nw, tile = piece / tt_n / nw;
+    const int mb = tile / cols, nbl = tile - mb * cols;
+    const ModuleArgs M = args.mod[module_of(args, nbl)];
+    const int rt0 = (nbl - M.tile_begin) * RR * wn_n + (wave / wm_n) * RR;
+    const int t = (mb * wm_n + wave % wm_n) * 16 * tt_n + 16 * tt + (lane & 15);
+    if (rt0 >= M.n_tiles16) return;
+    const bool ok = t < args.T;
+    const i4v* part = reinterpret_cast<const i4v*>(args.ypart);
+    i4v sum[RR];
+#pragma unroll
+    for (int rr = 0; rr < RR; ++rr) sum[rr] = i4v{0, 0, 0, 0};
+    for (int k = 0; k < ks; ++k) {
+        const i4v* p = part + ((((size_t)tile * ks + k) * nw + wave) * tt_n + tt) * (RR * 64) + lane;
+#pragma unroll
+        for (int rr = 0; rr < RR; ++rr) sum[rr] += p[rr * 64];
+    }
+    const float st = ok ? args.xscale[t] : 0.f;
+    f4 v[RR];
+#pragma unroll
+    for (int rr = 0; rr < RR; ++rr) {
+        const f4 sw = *reinterpret_cast<const f4*>(M.sz + (size_t)min(rt0 + rr, M.n_tiles16 - 1) * 64 + 16 * (lane >> 4));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[rr][i] = (float)sum[rr][i] * sw[i] * st;
+    }
+    if (args.r > 0 && M.a != nullptr) {
+        const int r = args.r, rp = args.r_pad;
+        const _Float16* R = reinterpret_cast<const _Float16*>(args.R);
+        const h8 zero8 = {0, 0, 0, 0, 0, 0, 0, 0};
+        for (int kb = 0; kb < rp / 32; ++kb) {
+            const int c = 32 * kb + 8 * (lane >> 4);
+            const h8 bv = ok ? load_h8(R + (size_t)t * rp + c) : zero8;
+#pragma unroll
+            for (int rr = 0; rr < RR; ++rr) {
+                const int row = (rt0 + rr) * 16 + (lane & 15);
+                const h8 av = (row < M.n_out && c < r) ? load_h8(M.a + (size_t)row * r + c) : zero8;
+                v[rr] = mfma16(av, bv, v[rr]);
+            }
+        }
+    }
+    if (!ok) return;
+#pragma unroll
+    for (int rr = 0; rr < RR; ++rr)
+        if (rt0 + rr < M.n_tiles16) store_rows(M, t, (rt0 + rr) * 16 + 4 * (lane >> 4), v[rr]);
 }
 
 }  // namespace
@@ -236,7 +487,22 @@ hipError_t launch_quant_q8(const _Float16* x, int T, int d, int8_t* xq, float* x
     return hipGetLastError();
 }
 
+template <int WM, int WN, int TT>
+static hipError_t launch_tile(const ForwardArgs& a, hipStream_t stream) {
+    // every XCD takes ceil(columns / 8) columns of every token block; those it has not return at once
+    const int64_t grid = 8 * ceil_div(a.n_tiles, 8) * a.m_tiles;
+    if (grid * 64 * WM * WN > (int64_t)UINT32_MAX) return hipErrorInvalidConfiguration;
+    hipLaunchKernelGGL((w8a8_tile_kernel<WM, WN, TT>), dim3((unsigned)grid), dim3(64 * WM * WN), 0, stream, a);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || a.tile_ks == 1) return e;
+    const int pieces = a.m_tiles * (a.n_tiles / a.tile_ks) * WM * WN * TT;
+    hipLaunchKernelGGL(w8a8_join_kernel, dim3((unsigned)ceil_div(pieces, 4)), dim3(256), 0, stream, a, WM, WN, TT, pieces);
+    return hipGetLastError();
+}
+
 hipError_t launch_w8a8(const ForwardArgs& a, hipStream_t stream) {
+    if (a.tile_rr == 16) return launch_tile<2, 4, 8>(a, stream);
+    if (a.tile_rr == 8) return launch_tile<2, 2, 4>(a, stream);
     const dim3 grid((unsigned)a.n_tiles), block(64 * kW8Waves);
     switch (a.tile_tt * 4 + a.tile_rr) {
         case 4 + 1: hipLaunchKernelGGL((w8a8_split_kernel<1, 1>), grid, block, 0, stream, a); break;
