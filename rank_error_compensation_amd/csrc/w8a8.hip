@@ -13,8 +13,14 @@
 // Weight layout: G x NT blocks of 2048 bytes, block (g, rt) at (g NT + rt) 2048 holding rows
 // 16 rt .. + 15 and inputs 128 g .. + 127 as two 1024-byte operands of v_mfma_i32_16x16x64_i8:
 // operand m, lane l (16 bytes at 1024 m + 16 l) is row 16 rt + l % 16, inputs 128 g + 64 m +
-// 16 (l / 16) .. + 15.  Activation codes stay in their natural order [T][d], whose 16-byte pieces
-// are the other operand.  Scales: 16 fp32 per row tile.  Rows >= n_out are zero.
+// 16 (l / 16) .. + 15.  Scales: 16 fp32 per row tile.  Rows >= n_out are zero.
+//
+// Code layout (workspace): [T][d], 16-byte pieces of the other operand in an order that suits LDS: of
+// the eight pieces of token t's input group, piece c (inputs 16 c .. + 15) is at position c ^ f(t),
+// f(t) = (t % 8) ^ ((t / 8) % 2).  A tile's rows then go to LDS as they lie in memory (the load unit
+// takes 64 lanes of consecutive 16 bytes in 16 cycles, permuted ones in about 80: the 256 x 256 tile
+// that permuted on the way took 269 us at 22016 x 4096, T = 2048), and the 16 rows of an operand read
+// fall in distinct banks.
 #include <type_traits>
 
 #include "glowq_internal.h"
@@ -25,6 +31,9 @@ namespace glowq {
 typedef int32_t i4v __attribute__((ext_vector_type(4)));
 
 namespace {
+
+// f(t) of the code layout.
+__device__ __forceinline__ int code_swizzle(int t) { return (t & 7) ^ ((t >> 3) & 1); }
 
 __device__ __forceinline__ i4v mfma_i8(i4v a, i4v b, i4v c) {
     return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
@@ -122,7 +131,7 @@ __global__ __launch_bounds__(kQ8Threads) void quant_q8_kernel(const _Float16* __
                 }
                 w[j] = word;
             }
-            *reinterpret_cast<u4*>(xq + (size_t)t * d + 16 * (size_t)c) = w;
+            *reinterpret_cast<u4*>(xq + (size_t)t * d + 16 * (size_t)(c ^ code_swizzle(t))) = w;
         }
     }
 }
@@ -150,11 +159,14 @@ __global__ __launch_bounds__(64 * kW8Waves) void w8a8_split_kernel(const Forward
     const size_t qstride = (size_t)M.n_tiles16 * kW8Block;
     const int8_t* xp[TT];
     bool t_ok[TT];
+    int xofs[2];  // this lane's pieces of a group: f depends on the token's place in its 16-token tile alone
+#pragma unroll
+    for (int m = 0; m < 2; ++m) xofs[m] = 16 * ((4 * m + (lane >> 4)) ^ code_swizzle(lane & 15));
 #pragma unroll
     for (int tt = 0; tt < TT; ++tt) {
         const int t = m0 + 16 * tt + (lane & 15);
         t_ok[tt] = t < T;
-        xp[tt] = args.xq + (size_t)(t_ok[tt] ? t : 0) * d + 16 * (lane >> 4);
+        xp[tt] = args.xq + (size_t)(t_ok[tt] ? t : 0) * d;
     }
     i4v acc[TT][RR];
 #pragma unroll
@@ -174,7 +186,7 @@ __global__ __launch_bounds__(64 * kW8Waves) void w8a8_split_kernel(const Forward
                     w[u][rr][m] = *reinterpret_cast<const i4v*>(qp[rr] + (size_t)g * qstride + 1024 * m);
 #pragma unroll
                 for (int tt = 0; tt < TT; ++tt)
-                    x[u][tt][m] = t_ok[tt] ? *reinterpret_cast<const i4v*>(xp[tt] + (size_t)g * kGroup + 64 * m) : zero;
+                    x[u][tt][m] = t_ok[tt] ? *reinterpret_cast<const i4v*>(xp[tt] + (size_t)g * kGroup + xofs[m]) : zero;
             }
         }
 #pragma unroll
@@ -227,8 +239,7 @@ __global__ __launch_bounds__(64 * kW8Waves) void w8a8_split_kernel(const Forward
 // The token codes of an input group (128 bytes a token) go HBM/L2 -> LDS by the load unit into a ring
 // of four stages; a wavefront's weight operands come straight into registers, one group ahead (the WM
 // wavefronts that share rows find them in the L1 cache), so that LDS carries only the codes: a code
-// byte read feeds 4 matrix-core steps.  In a stage, row r keeps its 16-byte chunk c at position
-// c ^ f(r), f(r) = (r % 8) ^ ((r / 8) % 2): the 16 rows of an operand read fall in distinct banks.
+// byte read feeds 4 matrix-core steps.
 // Tokens past T read token T - 1 and row tiles past the module its last tile; neither is stored.
 //
 // With args.tile_ks > 1 the input groups are split over workgroups: each writes its exact int32
@@ -276,22 +287,19 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN <= 4 ? 2 : 1) void w8a8_tile_
     const int m0 = mb * BM, rt0 = (nbl - M.tile_begin) * RR * WN + wn * RR;
     const int g_begin = kr * args.dec_gk, g_end = min(g_begin + args.dec_gk, args.G);
 
-    // code copy i of wave w fills rows 8 (NC w + i) .. + 7 of the stage; lane l lands at row + l / 8,
-    // position l % 8, holding the row's chunk (l % 8) ^ f(row)
+    // code copy i of wave w fills rows 8 (NC w + i) .. + 7 of the stage, as they lie in memory
     uint32_t xoff[NC];
 #pragma unroll
-    for (int i = 0; i < NC; ++i) {
-        const int row = 8 * (NC * wave + i) + (lane >> 3);
-        const int f = (row & 7) ^ ((row >> 3) & 1);
-        xoff[i] = (uint32_t)(min(m0 + row, T - 1) * d + 16 * ((lane & 7) ^ f));
-    }
-    const int fr = (lane & 7) ^ ((lane >> 3) & 1);
+    for (int i = 0; i < NC; ++i)
+        xoff[i] = (uint32_t)(min(m0 + 8 * (NC * wave + i) + (lane >> 3), T - 1) * d + 16 * (lane & 7));
+    const int fr = code_swizzle(lane & 15);
     const int rbase = (16 * TT * wm + (lane & 15)) * 128;
     const int rofs0 = rbase + 16 * ((lane >> 4) ^ fr), rofs1 = rbase + 16 * ((4 + (lane >> 4)) ^ fr);
-    const int rtb = min(rt0, NT - 1);
-    uint32_t woff[RR];
+    // row tiles are the wavefront's own, so weight addresses are scalar but for the lane's 16 bytes
+    uint32_t rofs[RR];
 #pragma unroll
-    for (int rr = 0; rr < RR; ++rr) woff[rr] = (uint32_t)((min(rt0 + rr, NT - 1) - rtb) * kW8Block + lane * 16);
+    for (int rr = 0; rr < RR; ++rr) rofs[rr] = (uint32_t)min(rt0 + rr, NT - 1);
+    const uint32_t lofs = lane * 16;
 
     auto copy = [&](int g, uint8_t* stg) {
         const int8_t* xb = args.xq + (size_t)min(g, g_end - 1) * kGroup;
@@ -302,11 +310,12 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN <= 4 ? 2 : 1) void w8a8_tile_
     };
     i4v w[2][RR][2];
     auto wload = [&](int g, int slot) {
-        const uint8_t* qb = M.q + ((size_t)min(g, g_end - 1) * NT + rtb) * kW8Block;
 #pragma unroll
-        for (int rr = 0; rr < RR; ++rr)
+        for (int rr = 0; rr < RR; ++rr) {
+            const uint8_t* qb = M.q + ((size_t)min(g, g_end - 1) * NT + rofs[rr]) * kW8Block;
 #pragma unroll
-            for (int m = 0; m < 2; ++m) w[slot][rr][m] = *reinterpret_cast<const i4v*>(qb + woff[rr] + 1024 * m);
+            for (int m = 0; m < 2; ++m) w[slot][rr][m] = *reinterpret_cast<const i4v*>(qb + 1024 * m + lofs);
+        }
     };
     i4v acc[TT][RR];
 #pragma unroll
@@ -331,6 +340,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN <= 4 ? 2 : 1) void w8a8_tile_
         __builtin_amdgcn_sched_barrier(0);
         copy(g + 2, nxt);
         __builtin_amdgcn_sched_barrier(0);
+        if (g >= g_end) return;
         i4v x[2][2];
         x[0][0] = *reinterpret_cast<const i4v*>(cur + rofs0);
         x[0][1] = *reinterpret_cast<const i4v*>(cur + rofs1);
@@ -348,16 +358,14 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN <= 4 ? 2 : 1) void w8a8_tile_
             __builtin_amdgcn_sched_barrier(0);
         }
     };
-    int g = g_begin;
-    for (; g + 4 <= g_end; g += 4) {
+    // whole turns of the ring; steps past the range only keep time (a tail of its own made the
+    // compiler move and spill accumulators)
+    for (int g = g_begin; g < g_end; g += 4) {
         step(g, ic<0>{});
         step(g + 1, ic<1>{});
         step(g + 2, ic<2>{});
         step(g + 3, ic<3>{});
     }
-    if (g < g_end) step(g, ic<0>{});
-    if (g + 1 < g_end) step(g + 1, ic<1>{});
-    if (g + 2 < g_end) step(g + 2, ic<2>{});
     __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): no copy may land in LDS after the workgroup ends
 
     if (ks > 1) {
@@ -368,49 +376,97 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN <= 4 ? 2 : 1) void w8a8_tile_
             for (int rr = 0; rr < RR; ++rr) part[(tt * RR + rr) * 64 + lane] = acc[tt][rr];
         return;
     }
-    const int tok0 = m0 + 16 * TT * wm + (lane & 15);
-    f4 v[TT][RR];
-    f4 sw[RR];
-#pragma unroll
-    for (int rr = 0; rr < RR; ++rr)
-        sw[rr] = *reinterpret_cast<const f4*>(M.sz + (size_t)min(rt0 + rr, NT - 1) * 64 + 16 * (lane >> 4));
-#pragma unroll
-    for (int tt = 0; tt < TT; ++tt) {
-        const int t = tok0 + 16 * tt;
-        const float st = args.xscale[min(t, T - 1)];
+    // The scaled sums take the integer sums' registers (as bits): the tile is all a wavefront can hold.
+    // The empty asm keeps each product where it is written (it was sunk into the branches below, with
+    // both forms of the tile live), and gives each part its own addresses instead of kept ones.
+    {
+        const int tok0 = m0 + 16 * TT * wm + (lane & 15);
+        f4 sw[RR];
+        float st[TT];
 #pragma unroll
         for (int rr = 0; rr < RR; ++rr)
+            sw[rr] = *reinterpret_cast<const f4*>(M.sz + (size_t)min(rt0 + rr, NT - 1) * 64 + 16 * (lane >> 4));
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[tt][rr][i] = (float)acc[tt][rr][i] * sw[rr][i] * st;
-    }
-    if (args.r > 0 && M.a != nullptr) {
-        const int r = args.r, rp = args.r_pad, kofs = 8 * (lane >> 4);
-        const _Float16* R = reinterpret_cast<const _Float16*>(args.R);
-        const h8 zero8 = {0, 0, 0, 0, 0, 0, 0, 0};
-        for (int kb = 0; kb < rp / 32; ++kb) {
-            const int c = 32 * kb + kofs;
-            h8 av[RR];
+        for (int tt = 0; tt < TT; ++tt) st[tt] = args.xscale[min(tok0 + 16 * tt, T - 1)];
+#pragma unroll
+        for (int tt = 0; tt < TT; ++tt) {
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int rr = 0; rr < RR; ++rr) {
-                const int row = (rt0 + rr) * 16 + (lane & 15);
-                av[rr] = (row < M.n_out && c < r) ? load_h8(M.a + (size_t)row * r + c) : zero8;
-            }
+                f4 v;
 #pragma unroll
-            for (int tt = 0; tt < TT; ++tt) {
-                const int t = tok0 + 16 * tt;
-                const h8 bv = t < T ? load_h8(R + (size_t)t * rp + c) : zero8;
-#pragma unroll
-                for (int rr = 0; rr < RR; ++rr) v[tt][rr] = mfma16(av[rr], bv, v[tt][rr]);
+                for (int i = 0; i < 4; ++i) v[i] = (float)acc[tt][rr][i] * sw[rr][i] * st[tt];
+                asm volatile("" : "+v"(v));
+                acc[tt][rr] = __builtin_bit_cast(i4v, v);
             }
         }
     }
+    __builtin_amdgcn_sched_barrier(0);
+    if (args.r > 0 && M.a != nullptr) {
+        // rows past the module and tokens past T repeat the last one; their results are not stored.
+        // Columns r .. r_pad - 1 of R are zero, and so must A's be
+        int l = lane;
+        asm volatile("" : "+v"(l));
+        const int r = args.r, rp = args.r_pad, kofs = 8 * (l >> 4), row0 = min(rt0, NT - 1) * 16;
+        const uint8_t* Rb = reinterpret_cast<const uint8_t*>(args.R);
+        const uint8_t* Ab = reinterpret_cast<const uint8_t*>(M.a + (size_t)row0 * r);
+        const h8 zero8 = {0, 0, 0, 0, 0, 0, 0, 0};
+        uint32_t roff[TT], aoff[RR];
 #pragma unroll
-    for (int tt = 0; tt < TT; ++tt) {
-        const int t = tok0 + 16 * tt;
+        for (int tt = 0; tt < TT; ++tt)
+            roff[tt] = (uint32_t)(min(m0 + 16 * TT * wm + 16 * tt + (l & 15), T - 1) * rp) * 2u;
+#pragma unroll
+        for (int rr = 0; rr < RR; ++rr) aoff[rr] = (uint32_t)((min((rt0 + rr) * 16 + (l & 15), M.n_out - 1) - row0) * r) * 2u;
+#pragma unroll 1
+        for (int kb = 0; kb < rp / 32; ++kb) {
+            const int c = 32 * kb + kofs;
+            h8 av[RR], bv[TT];
+#pragma unroll
+            for (int rr = 0; rr < RR; ++rr) {
+                const h8 v = load_h8(Ab + (aoff[rr] + 2u * (uint32_t)min(c, r - 8)));
+                av[rr] = c < r ? v : zero8;
+            }
+#pragma unroll
+            for (int tt = 0; tt < TT; ++tt) bv[tt] = load_h8(Rb + (roff[tt] + 2u * (uint32_t)c));
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int tt = 0; tt < TT; ++tt)
+#pragma unroll
+                for (int rr = 0; rr < RR; ++rr)
+                    acc[tt][rr] = __builtin_bit_cast(i4v, mfma16(av[rr], bv[tt], __builtin_bit_cast(f4, acc[tt][rr])));
+        }
+    }
+    // To memory through the wavefront's own part of the (finished) ring: [16 TT tokens][64 rows] fp16,
+    // a token's eight 16-byte pieces p at p ^ (token % 8), then whole 128-byte lines.
+    __builtin_amdgcn_s_barrier();
+    constexpr int kPart = 16 * TT * 128, kPer = SB / kPart;
+    static_assert(NW * kPart <= 4 * SB && SB % kPart == 0, "a part per wavefront");
+    const int sel = wave / kPer;
+    uint8_t* out = (sel == 0 ? st0 : (sel == 1 ? st1 : (sel == 2 ? st2 : st3))) + (wave % kPer) * kPart;
+#pragma unroll
+    for (int tt = 0; tt < TT; ++tt)
+#pragma unroll
+        for (int rr = 0; rr < RR; ++rr) {
+            const f4 v = __builtin_bit_cast(f4, acc[tt][rr]);
+            const h2 lo = {(_Float16)v[0], (_Float16)v[1]}, hi = {(_Float16)v[2], (_Float16)v[3]};
+            const int p = 2 * rr + (lane >> 5);
+            *reinterpret_cast<u2*>(out + (16 * tt + (lane & 15)) * 128 + 16 * (p ^ (lane & 7)) + 8 * ((lane >> 4) & 1)) =
+                u2{as_u32(lo), as_u32(hi)};
+        }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    const int row0 = rt0 * 16 + 8 * (lane & 7);
+    const bool vec = (M.n_out & 7) == 0 && row0 + 7 < M.n_out;
+#pragma unroll 4
+    for (int i = 0; i < 2 * TT; ++i) {
+        const int tl = 8 * i + (lane >> 3), t = m0 + 16 * TT * wm + tl;
+        const uint8_t* piece = out + tl * 128 + 16 * ((lane & 7) ^ (tl & 7));
         if (t >= T) continue;
-#pragma unroll
-        for (int rr = 0; rr < RR; ++rr)
-            if (rt0 + rr < NT) store_rows(M, t, (rt0 + rr) * 16 + 4 * (lane >> 4), v[tt][rr]);
+        _Float16* y = M.y + (size_t)t * M.n_out + row0;
+        if (vec) *reinterpret_cast<h8*>(y) = *reinterpret_cast<const h8*>(piece);
+        else {
+#pragma unroll 1
+            for (int e = 0; e < min(8, M.n_out - row0); ++e) y[e] = reinterpret_cast<const _Float16*>(piece)[e];
+        }
     }
 }
 
@@ -501,7 +557,7 @@ static hipError_t launch_tile(const ForwardArgs& a, hipStream_t stream) {
 }
 
 hipError_t launch_w8a8(const ForwardArgs& a, hipStream_t stream) {
-    if (a.tile_rr == 16) return launch_tile<2, 4, 8>(a, stream);
+    if (a.tile_rr == 16) return launch_tile<1, 4, 8>(a, stream);
     if (a.tile_rr == 8) return launch_tile<2, 2, 4>(a, stream);
     const dim3 grid((unsigned)a.n_tiles), block(64 * kW8Waves);
     switch (a.tile_tt * 4 + a.tile_rr) {
