@@ -519,11 +519,13 @@ int run_w4a8(const Call& c, void* workspace, hipStream_t stream) {
 // K ranges' int32 tiles of a call of more than 64 tokens: bounded by the workspace that
 // glowq_w8a8_workspace_bytes reserves for them.
 constexpr size_t kW8PartBytes = (size_t)32 << 20;
-constexpr int64_t kW8TileMinT = 65;
+inline size_t w8_part_bytes(int64_t T, int32_t r, int ks) {
+    return round256((size_t)ks * (size_t)T * (size_t)r_pad_of(r) * 4u);
+}
 
 W8Shape choose_w8a8_shape(const Call& c) {
     W8Shape s = {c.T <= 16 ? 1 : (c.T <= 32 ? 2 : 4), c.T <= 16 ? 1 : 2, 1, (int)(c.d / kGroup), 0};
-    if (c.T < kW8TileMinT) return s;
+    if (c.T <= kW8SmallT) return s;
     auto tiles = [&](int tt, int rr) {
         int64_t n = 0;
         for (int i = 0; i < c.m; ++i) n += ceil_div(ceil_div(c.w[i].n_out, 16), rr);
@@ -543,7 +545,8 @@ W8Shape choose_w8a8_shape(const Call& c) {
     return s;
 }
 
-// W8A8 form.  Workspace: codes int8 [T][d] | scales fp32 [T] | projection and its split-K partials.
+// W8A8 form.  Workspace: codes int8 [T][d] | scales fp32 [T] | fp16 projection [T][r_pad]
+// | K ranges' int32 tiles.
 int run_w8a8(const Call& c, void* workspace, hipStream_t stream) {
     if (c.T == 0) return GLOWQ_OK;
     uint8_t* base = static_cast<uint8_t*>(workspace);
@@ -551,20 +554,39 @@ int run_w8a8(const Call& c, void* workspace, hipStream_t stream) {
     base += round256((size_t)c.T * c.d);
     float* xscale = reinterpret_cast<float*>(base);
     base += round256((size_t)c.T * 4u);
-    void* R = c.correct ? base : nullptr;
-    if (launch_quant_q8(static_cast<const _Float16*>(c.x), (int)c.T, (int)c.d, xq, xscale, stream) != hipSuccess)
-        return GLOWQ_ERR_HIP;
-    if (c.correct && launch_projection(c, R, stream) != hipSuccess) return GLOWQ_ERR_HIP;
+    const int32_t r = c.correct ? c.r : 0, rp = c.correct ? (int32_t)r_pad_of(c.r) : 0;
+    const PrepPlan pp = w8a8_prep_plan(c.T, c.d, r);
+    PrepArgs pa;
+    std::memset(&pa, 0, sizeof(pa));
+    pa.x = static_cast<const _Float16*>(c.x);
+    pa.b = c.correct ? static_cast<const _Float16*>(c.b[0]) : nullptr;
+    pa.T = (int32_t)c.T;
+    pa.d = (int32_t)c.d;
+    pa.r = r;
+    pa.rp = rp;
+    pa.range = pp.range;
+    pa.ks = pp.ks;
+    pa.xq = xq;
+    pa.xscale = xscale;
+    if (c.correct) {
+        if (c.T <= kW8SmallT || pp.ks > 1) {
+            pa.part = reinterpret_cast<float*>(base);
+            base += w8_part_bytes(c.T, r, pp.ks);
+        }
+        pa.R = reinterpret_cast<_Float16*>(base);
+        base += prefill_r_bytes(c.T, r, 1);
+    }
+    if (launch_w8a8_prep(pa, pp, stream) != hipSuccess) return GLOWQ_ERR_HIP;
     ForwardArgs f;
     std::memset(&f, 0, sizeof(f));
     f.T = (int32_t)c.T;
     f.d = (int32_t)c.d;
     f.G = (int32_t)(c.d / kGroup);
-    f.r = c.correct ? c.r : 0;
-    f.r_pad = c.correct ? (int32_t)r_pad_of(c.r) : 0;
+    f.r = r;
+    f.r_pad = rp;
     f.n_mod = c.m;
-    f.R = R;
-    f.n_proj = 1;
+    f.R = c.T <= kW8SmallT ? static_cast<void*>(pa.part) : static_cast<void*>(pa.R);
+    f.n_proj = pp.ks;  // fp32 K ranges of R (small calls)
     f.xq = xq;
     f.xscale = xscale;
     f.fmt = kFmtInt8;
@@ -573,7 +595,6 @@ int run_w8a8(const Call& c, void* workspace, hipStream_t stream) {
     f.tile_rr = s.rr;
     f.tile_ks = s.ks;
     f.dec_gk = s.gk;
-    if (c.correct) base += prefill_r_bytes(c.T, c.r, 1) + prefill_part_bytes(c.T, c.r, 1);
     f.ypart = reinterpret_cast<float*>(base);
     int64_t tiles = 0;
     for (int i = 0; i < c.m; ++i) {
@@ -947,8 +968,8 @@ int glowq_repack_w8(const void* codes_dev, const float* scales_dev, int64_t n_ou
 size_t glowq_w8a8_workspace_bytes(int64_t T, int64_t d, int32_t r) {
     if (T <= 0 || T > kMaxT || d < kGroup || d % kGroup != 0 || d > kW8MaxD || r < 0 || r > GLOWQ_MAX_RANK) return 0;
     size_t n = round256((size_t)T * d) + round256((size_t)T * 4u);
-    if (r > 0) n += prefill_r_bytes(T, r, 1) + prefill_part_bytes(T, r, 1);
-    if (T >= kW8TileMinT) n += kW8PartBytes;
+    if (r > 0) n += w8_part_bytes(T, r, w8a8_prep_plan(T, d, r).ks) + prefill_r_bytes(T, r, 1);
+    if (T > kW8SmallT) n += kW8PartBytes;
     return n;
 }
 

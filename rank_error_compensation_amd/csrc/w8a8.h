@@ -21,7 +21,26 @@ struct W8Shape {
 
 hipError_t launch_repack_w8(const int8_t* codes, const float* scales, int64_t n_out, int64_t k_in, uint8_t* q, float* sz,
                             int32_t* flag, hipStream_t stream);
-hipError_t launch_quant_q8(const _Float16* x, int T, int d, int8_t* xq, float* xscale, hipStream_t stream);
+// Token codes and scales and, for r > 0, the projection, one launch.  Up to kW8SmallT tokens the K
+// ranges' fp32 sums [ks][T][rp] stay in `part` for the product to add; above, they are joined into the
+// fp16 R [T][rp] by a second launch (written directly with one range).
+constexpr int64_t kW8SmallT = 64;
+struct PrepPlan {
+    int tt, nj;     // 16-token tiles and 16-column tiles of R per workgroup
+    int range, ks;  // inputs per K range, ranges
+};
+PrepPlan w8a8_prep_plan(int64_t T, int64_t d, int32_t r);
+struct PrepArgs {
+    const _Float16* x;  // [T][d]
+    const _Float16* b;  // [r][d]
+    int32_t T, d, r, rp;
+    int32_t range, ks;
+    int8_t* xq;
+    float* xscale;
+    float* part;   // [ks][T][rp], nullptr for one range rounded directly
+    _Float16* R;
+};
+hipError_t launch_w8a8_prep(const PrepArgs& a, const PrepPlan& p, hipStream_t stream);
 hipError_t launch_w8a8(const ForwardArgs& a, hipStream_t stream);
 
 }  // namespace glowq

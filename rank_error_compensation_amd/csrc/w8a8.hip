@@ -14,13 +14,8 @@
 // 16 rt .. + 15 and inputs 128 g .. + 127 as two 1024-byte operands of v_mfma_i32_16x16x64_i8:
 // operand m, lane l (16 bytes at 1024 m + 16 l) is row 16 rt + l % 16, inputs 128 g + 64 m +
 // 16 (l / 16) .. + 15.  Scales: 16 fp32 per row tile.  Rows >= n_out are zero.
-//
-// Code layout (workspace): [T][d], 16-byte pieces of the other operand in an order that suits LDS: of
-// the eight pieces of token t's input group, piece c (inputs 16 c .. + 15) is at position c ^ f(t),
-// f(t) = (t % 8) ^ ((t / 8) % 2).  A tile's rows then go to LDS as they lie in memory (the load unit
-// takes 64 lanes of consecutive 16 bytes in 16 cycles, permuted ones in about 80: the 256 x 256 tile
-// that permuted on the way took 269 us at 22016 x 4096, T = 2048), and the 16 rows of an operand read
-// fall in distinct banks.
+// Activation codes lie in their natural order [T][d]; its 16-byte pieces are the other operand.
+#include <algorithm>
 #include <type_traits>
 
 #include "glowq_internal.h"
@@ -31,9 +26,6 @@ namespace glowq {
 typedef int32_t i4v __attribute__((ext_vector_type(4)));
 
 namespace {
-
-// f(t) of the code layout.
-__device__ __forceinline__ int code_swizzle(int t) { return (t & 7) ^ ((t >> 3) & 1); }
 
 __device__ __forceinline__ i4v mfma_i8(i4v a, i4v b, i4v c) {
     return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
@@ -74,66 +66,181 @@ __global__ __launch_bounds__(256) void repack_w8_scales_kernel(const float* __re
     sz[i] = s;
 }
 
-// --------------------------------------------------------------------- token codes
-constexpr int kQ8Threads = 256;
-constexpr int kQ8Chunks = 4;  // 16-input chunks per thread: d <= 4 * 16 * 256 = 16384
+// --------------------------------------------------------------------- token codes and projection
+// One launch, two kinds of workgroups (both read X, neither needs the other): first those of the
+// projection R = X B^T, then one per token for its scale and codes.
+constexpr int kPrepThreads = 512;
+constexpr int kPrepWaves = kPrepThreads / 64;
+constexpr int kPrepChunks = 8;  // 8-input chunks per thread at most
+constexpr int kPrepMaxD = 16384;
 
-// One workgroup per token: the largest magnitude (as fp16 bits, so that infinities and NaN order
-// above every number), the scale, the codes.
-__global__ __launch_bounds__(kQ8Threads) void quant_q8_kernel(const _Float16* __restrict__ x, int d, int8_t* __restrict__ xq,
-                                                              float* __restrict__ xscale) {
-    __shared__ uint32_t red[kQ8Threads / 64];
-    const int t = blockIdx.x, tid = threadIdx.x;
-    const int n16 = d / 16;
-    const _Float16* row = x + (size_t)t * d;
-    h8 v[kQ8Chunks][2];
+// round_half_even(x / scale), the quotient the IEEE one, of eight values as bytes.  u = x (1 / scale)
+// is within 127 (2^-23 + 2^-24) < 2^-15 of it, so both round alike unless u lies that close to a tie;
+// only then (one value in 10^4) the eight are divided.  |x| <= amax keeps every code in -127 .. 127.
+// Adding 1.5 2^23 rounds to a whole number whose low byte is the code.
+__device__ __forceinline__ u2 codes_of(const h8& x, float scale, float inv) {
+    constexpr float kWhole = 12582912.0f;
+    uint32_t f[8];
+    float near = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const float v = fmaf((float)x[e], inv, kWhole);
+        near = fmaxf(near, fabsf(fmaf((float)x[e], inv, -(v - kWhole))));
+        f[e] = __builtin_bit_cast(uint32_t, v);
+    }
+    if (__builtin_expect(near > 0.5f - 0x1p-14f, 0)) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = __builtin_bit_cast(uint32_t, (float)x[e] / scale + kWhole);
+    }
+    u2 w;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+        w[j] = __builtin_amdgcn_perm(__builtin_amdgcn_perm(f[4 * j + 3], f[4 * j + 2], 0x0c0c0400),
+                                     __builtin_amdgcn_perm(f[4 * j + 1], f[4 * j], 0x0c0c0400), 0x05040100);
+    return w;
+}
+
+// kPrepThreads / TPT tokens from t0 on: each by TPT threads with C chunks of eight
+// inputs (TPT C >= d / 8): the largest magnitude (as fp16 bits, so that infinities and NaN order above
+// every number), the scale, the codes.
+template <int TPT, int C>
+__device__ void quant_tokens(const _Float16* __restrict__ x, int t0, int T, int d, int8_t* __restrict__ xq,
+                             float* __restrict__ xscale, uint32_t* red) {
+    const int tid = threadIdx.x, sub = tid & (TPT - 1), t = t0 + tid / TPT;
+    const int n8 = t < T ? d / 8 : 0;
+    const _Float16* row = x + (size_t)min(t, T - 1) * d;
+    h8 v[C];
     uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < kQ8Chunks; ++i) {
-        const int c = tid + kQ8Threads * i;
-        if (c < n16) {
+    for (int i = 0; i < C; ++i) {
+        const int c = sub + TPT * i;
+        v[i] = c < n8 ? load_h8(row + 8 * c) : h8{0, 0, 0, 0, 0, 0, 0, 0};
+    }
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                v[i][h] = load_h8(row + 16 * c + 8 * h);
-                const u4 bits = __builtin_bit_cast(u4, v[i][h]) & 0x7FFF7FFFu;
+    for (int i = 0; i < C; ++i) {
+        const u4 bits = __builtin_bit_cast(u4, v[i]) & 0x7FFF7FFFu;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) top = max(top, max(bits[e] & 0xFFFFu, bits[e] >> 16));
-            }
-        }
+        for (int e = 0; e < 4; ++e) top = max(top, max(bits[e] & 0xFFFFu, bits[e] >> 16));
     }
 #pragma unroll
     for (int off = 32; off > 0; off >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, off, 64));
-    if ((tid & 63) == 0) red[tid >> 6] = top;
-    __syncthreads();
-    top = max(max(red[0], red[1]), max(red[2], red[3]));
+    if constexpr (TPT > 64) {
+        if ((tid & 63) == 0) red[tid >> 6] = top;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < TPT / 64; ++w) top = max(top, red[tid / TPT * (TPT / 64) + w]);
+    }
     const float amax = (float)__builtin_bit_cast(_Float16, (uint16_t)top);
     const bool finite = top < 0x7C00u;
     const float scale = finite ? amax / 127.0f : __builtin_nanf("");  // IEEE division
-    if (tid == 0) xscale[t] = scale;
+    if (sub == 0 && t < T) xscale[t] = scale;
     const bool some = finite && scale > 0.f;
+    const float inv = some ? 1.0f / scale : 0.f;
 #pragma unroll
-    for (int i = 0; i < kQ8Chunks; ++i) {
-        const int c = tid + kQ8Threads * i;
-        if (c < n16) {
-            u4 w;
+    for (int i = 0; i < C; ++i) {
+        const int c = sub + TPT * i;
+        if (c < n8)
+            *reinterpret_cast<u2*>(xq + (size_t)t * d + 8 * (size_t)c) = some ? codes_of(v[i], scale, inv) : u2{0u, 0u};
+    }
+}
+
+// Sums of R over the 32-input steps [s_begin, s_end) for 16 TT tokens and 16 NJ rank columns: the
+// wavefronts take steps in turn (U in flight) and add their tiles through LDS in wavefront order.
+// part != nullptr: fp32 sums of this range to part [T][rp]; else one rounding to fp16 into R.
+// Columns r .. r_pad - 1 are zero.
+template <int TT, int NJ>
+__device__ void project_tile(const PrepArgs& a, int tb, int jb, int s_begin, int s_end, float* part, f4* red) {
+    constexpr int U = TT * NJ == 1 ? 8 : 4, N = TT * NJ;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int kofs = 8 * (lane >> 4), T = a.T, d = a.d, r = a.r, rp = a.rp;
+    const _Float16 *xr[TT], *br[NJ];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                uint32_t word = 0;
+    for (int tt = 0; tt < TT; ++tt) xr[tt] = a.x + (size_t)min(16 * (TT * tb + tt) + (lane & 15), T - 1) * d + kofs;
 #pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    const int e = 4 * j + b;
-                    int code = 0;
-                    if (some) {
-                        const float rq = __builtin_rintf((float)v[i][e >> 3][e & 7] / scale);
-                        code = (int)fminf(127.f, fmaxf(-127.f, rq));
-                    }
-                    word |= (uint32_t)(code & 0xFF) << (8 * b);
-                }
-                w[j] = word;
+    for (int j = 0; j < NJ; ++j) br[j] = a.b + (size_t)min(16 * (NJ * jb + j) + (lane & 15), r - 1) * d + kofs;
+    f4 acc[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) acc[i] = f4{0.f, 0.f, 0.f, 0.f};
+    for (int s0 = s_begin + wave; s0 < s_end; s0 += U * kPrepWaves) {
+        h8 xv[U][TT], bv[U][NJ];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int k = 32 * min(s0 + u * kPrepWaves, s_end - 1);
+#pragma unroll
+            for (int tt = 0; tt < TT; ++tt) xv[u][tt] = load_h8(xr[tt] + k);
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) bv[u][j] = load_h8(br[j] + k);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (s0 + u * kPrepWaves < s_end) {
+#pragma unroll
+                for (int tt = 0; tt < TT; ++tt)
+#pragma unroll
+                    for (int j = 0; j < NJ; ++j) acc[tt * NJ + j] = mfma16(xv[u][tt], bv[u][j], acc[tt * NJ + j]);
             }
-            *reinterpret_cast<u4*>(xq + (size_t)t * d + 16 * (size_t)(c ^ code_swizzle(t))) = w;
+    }
+    // the upper half's tiles into the lower half, then wavefront i < N sums tile i (half the LDS of one
+    // step: the token workgroups of the same launch need the room to run side by side)
+    constexpr int H = kPrepWaves / 2;
+    if (wave >= H) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) red[((wave - H) * N + i) * 64 + lane] = acc[i];
+    }
+    __syncthreads();
+    if (wave < H) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            f4* own = red + (wave * N + i) * 64 + lane;
+            *own = acc[i] + *own;
         }
     }
+    __syncthreads();
+    if (wave >= N) return;
+    f4 v = red[wave * 64 + lane];
+#pragma unroll
+    for (int w = 1; w < H; ++w) v += red[(w * N + wave) * 64 + lane];
+    const int col = 16 * (NJ * jb + wave % NJ) + (lane & 15);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int t = 16 * (TT * tb + wave / NJ) + 4 * (lane >> 4) + i;
+        const float o = col < r ? v[i] : 0.f;
+        if (t < T && col < rp) {
+            if (part != nullptr) part[(size_t)t * rp + col] = o;
+            else a.R[(size_t)t * rp + col] = (_Float16)o;
+        }
+    }
+}
+
+// TPT: threads per token of the code workgroups.
+template <int TT, int NJ, int TPT>
+__global__ __launch_bounds__(kPrepThreads) void prep_kernel(const PrepArgs a, int proj_blocks) {
+    __shared__ f4 red[kPrepWaves / 2 * TT * NJ * 64];
+    int blk = blockIdx.x;
+    if (blk >= proj_blocks) {
+        constexpr int C = (kPrepMaxD / 8 + TPT - 1) / TPT < kPrepChunks ? (kPrepMaxD / 8 + TPT - 1) / TPT : kPrepChunks;
+        quant_tokens<TPT, C>(a.x, (blk - proj_blocks) * (kPrepThreads / TPT), a.T, a.d, a.xq, a.xscale,
+                             reinterpret_cast<uint32_t*>(red));
+        return;
+    }
+    const int cols = (a.rp / 16 + NJ - 1) / NJ;
+    const int k = blk % a.ks, rest = blk / a.ks, jb = rest % cols, tb = rest / cols;
+    const int per = a.range / 32;
+    project_tile<TT, NJ>(a, tb, jb, k * per, min((k + 1) * per, a.d / 32),
+                         a.part != nullptr ? a.part + (size_t)k * a.T * a.rp : nullptr, red);
+}
+
+// R = the K ranges' sums added in order, rounded once to fp16.
+__global__ __launch_bounds__(256) void prep_join_kernel(const PrepArgs a) {
+    const size_t n = (size_t)a.T * a.rp / 4, i = (size_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= n) return;
+    const f4* p = reinterpret_cast<const f4*>(a.part) + i;
+    f4 v = p[0];
+#pragma unroll 4
+    for (int k = 1; k < a.ks; ++k) v += p[(size_t)k * n];
+    const h2 lo = {(_Float16)v[0], (_Float16)v[1]}, hi = {(_Float16)v[2], (_Float16)v[3]};
+    reinterpret_cast<u2*>(a.R)[i] = u2{as_u32(lo), as_u32(hi)};
 }
 
 // --------------------------------------------------------------------- product
@@ -159,14 +266,11 @@ __global__ __launch_bounds__(64 * kW8Waves) void w8a8_split_kernel(const Forward
     const size_t qstride = (size_t)M.n_tiles16 * kW8Block;
     const int8_t* xp[TT];
     bool t_ok[TT];
-    int xofs[2];  // this lane's pieces of a group: f depends on the token's place in its 16-token tile alone
-#pragma unroll
-    for (int m = 0; m < 2; ++m) xofs[m] = 16 * ((4 * m + (lane >> 4)) ^ code_swizzle(lane & 15));
 #pragma unroll
     for (int tt = 0; tt < TT; ++tt) {
         const int t = m0 + 16 * tt + (lane & 15);
         t_ok[tt] = t < T;
-        xp[tt] = args.xq + (size_t)(t_ok[tt] ? t : 0) * d;
+        xp[tt] = args.xq + (size_t)(t_ok[tt] ? t : 0) * d + 16 * (lane >> 4);
     }
     i4v acc[TT][RR];
 #pragma unroll
@@ -186,7 +290,7 @@ __global__ __launch_bounds__(64 * kW8Waves) void w8a8_split_kernel(const Forward
                     w[u][rr][m] = *reinterpret_cast<const i4v*>(qp[rr] + (size_t)g * qstride + 1024 * m);
 #pragma unroll
                 for (int tt = 0; tt < TT; ++tt)
-                    x[u][tt][m] = t_ok[tt] ? *reinterpret_cast<const i4v*>(xp[tt] + (size_t)g * kGroup + xofs[m]) : zero;
+                    x[u][tt][m] = t_ok[tt] ? *reinterpret_cast<const i4v*>(xp[tt] + (size_t)g * kGroup + 64 * m) : zero;
             }
         }
 #pragma unroll
@@ -220,14 +324,27 @@ __global__ __launch_bounds__(64 * kW8Waves) void w8a8_split_kernel(const Forward
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = (float)sum[i] * sw[i] * st;
     if (args.r > 0 && M.a != nullptr) {
+        // R as the K ranges' fp32 sums, added in order and rounded once to fp16 here (few tokens: a
+        // launch that only joined them would take longer)
         const int r = args.r, rp = args.r_pad, kofs = 8 * (lane >> 4);
-        const _Float16* R = reinterpret_cast<const _Float16*>(args.R);
         const h8 zero8 = {0, 0, 0, 0, 0, 0, 0, 0};
         const int arow = rt * 16 + (lane & 15);
+        const float* R = static_cast<const float*>(args.R) + (size_t)min(t, T - 1) * rp;
         for (int kb = 0; kb < rp / 32; ++kb) {
             const int col = 32 * kb + kofs;
             const h8 av = (arow < M.n_out && col < r) ? load_h8(M.a + (size_t)arow * r + col) : zero8;
-            const h8 bv = ok ? load_h8(R + (size_t)t * rp + col) : zero8;
+            f4 lo = *reinterpret_cast<const f4*>(R + col), hi = *reinterpret_cast<const f4*>(R + col + 4);
+            for (int k = 1; k < args.n_proj; ++k) {
+                const float* p = R + (size_t)k * T * rp + col;
+                lo += *reinterpret_cast<const f4*>(p);
+                hi += *reinterpret_cast<const f4*>(p + 4);
+            }
+            h8 bv;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                bv[i] = (_Float16)lo[i];
+                bv[4 + i] = (_Float16)hi[i];
+            }
             v = mfma16(av, bv, v);
         }
     }
@@ -239,7 +356,8 @@ __global__ __launch_bounds__(64 * kW8Waves) void w8a8_split_kernel(const Forward
 // The token codes of an input group (128 bytes a token) go HBM/L2 -> LDS by the load unit into a ring
 // of four stages; a wavefront's weight operands come straight into registers, one group ahead (the WM
 // wavefronts that share rows find them in the L1 cache), so that LDS carries only the codes: a code
-// byte read feeds 4 matrix-core steps.
+// byte read feeds 4 matrix-core steps.  In a stage, row r keeps its 16-byte piece c at position
+// c ^ f(r), f(r) = (r % 8) ^ ((r / 8) % 2): the 16 rows of an operand read fall in distinct banks.
 // Tokens past T read token T - 1 and row tiles past the module its last tile; neither is stored.
 //
 // With args.tile_ks > 1 the input groups are split over workgroups: each writes its exact int32
@@ -287,12 +405,15 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN <= 4 ? 2 : 1) void w8a8_tile_
     const int m0 = mb * BM, rt0 = (nbl - M.tile_begin) * RR * WN + wn * RR;
     const int g_begin = kr * args.dec_gk, g_end = min(g_begin + args.dec_gk, args.G);
 
-    // code copy i of wave w fills rows 8 (NC w + i) .. + 7 of the stage, as they lie in memory
+    // code copy i of wave w fills rows 8 (NC w + i) .. + 7 of the stage; lane l lands at row + l / 8,
+    // position l % 8, holding the row's piece (l % 8) ^ f(row)
     uint32_t xoff[NC];
 #pragma unroll
-    for (int i = 0; i < NC; ++i)
-        xoff[i] = (uint32_t)(min(m0 + 8 * (NC * wave + i) + (lane >> 3), T - 1) * d + 16 * (lane & 7));
-    const int fr = code_swizzle(lane & 15);
+    for (int i = 0; i < NC; ++i) {
+        const int row = 8 * (NC * wave + i) + (lane >> 3);
+        xoff[i] = (uint32_t)(min(m0 + row, T - 1) * d + 16 * ((lane & 7) ^ (row & 7) ^ ((row >> 3) & 1)));
+    }
+    const int fr = (lane & 7) ^ ((lane >> 3) & 1);
     const int rbase = (16 * TT * wm + (lane & 15)) * 128;
     const int rofs0 = rbase + 16 * ((lane >> 4) ^ fr), rofs1 = rbase + 16 * ((4 + (lane >> 4)) ^ fr);
     // row tiles are the wavefront's own, so weight addresses are scalar but for the lane's 16 bytes
@@ -350,12 +471,10 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN <= 4 ? 2 : 1) void w8a8_tile_
                 x[(tt + 1) & 1][0] = *reinterpret_cast<const i4v*>(cur + rofs0 + (tt + 1) * 2048);
                 x[(tt + 1) & 1][1] = *reinterpret_cast<const i4v*>(cur + rofs1 + (tt + 1) * 2048);
             }
-            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int m = 0; m < 2; ++m)
 #pragma unroll
                 for (int rr = 0; rr < RR; ++rr) acc[tt][rr] = mfma_i8(w[S & 1][rr][m], x[tt & 1][m], acc[tt][rr]);
-            __builtin_amdgcn_sched_barrier(0);
         }
     };
     // whole turns of the ring; steps past the range only keep time (a tail of its own made the
@@ -537,9 +656,48 @@ hipError_t launch_repack_w8(const int8_t* codes, const float* scales, int64_t n_
     return hipGetLastError();
 }
 
-hipError_t launch_quant_q8(const _Float16* x, int T, int d, int8_t* xq, float* xscale, hipStream_t stream) {
-    if (d % kGroup != 0 || d > kQ8Chunks * 16 * kQ8Threads) return hipErrorInvalidValue;
-    hipLaunchKernelGGL(quant_q8_kernel, dim3((unsigned)T), dim3(kQ8Threads), 0, stream, x, d, xq, xscale);
+template <int TT, int NJ, int TPT>
+static void launch_prep_n(const PrepArgs& a, hipStream_t stream) {
+    const int64_t proj = a.r > 0 ? ceil_div(a.T, 16 * TT) * ceil_div(a.rp / 16, NJ) * a.ks : 0;
+    const int64_t tokens = ceil_div(a.T, kPrepThreads / TPT);
+    hipLaunchKernelGGL((prep_kernel<TT, NJ, TPT>), dim3((unsigned)(proj + tokens)), dim3(kPrepThreads), 0, stream, a,
+                       (int)proj);
+}
+
+// Few tokens: a workgroup for each.  Many: as few threads per token as hold its row (64 values each).
+template <int TT, int NJ>
+static void launch_prep_t(const PrepArgs& a, hipStream_t stream) {
+    if constexpr (NJ == 1) launch_prep_n<TT, NJ, kPrepThreads>(a, stream);
+    else if (a.T <= 256) launch_prep_n<TT, NJ, kPrepThreads>(a, stream);
+    else if (a.d <= 64 * 64) launch_prep_n<TT, NJ, 64>(a, stream);
+    else if (a.d <= 128 * 64) launch_prep_n<TT, NJ, 128>(a, stream);
+    else launch_prep_n<TT, NJ, 256>(a, stream);
+}
+
+PrepPlan w8a8_prep_plan(int64_t T, int64_t d, int32_t r) {
+    PrepPlan p = {1, T <= kW8SmallT ? 1 : 4, (int)d, 1};
+    if (r == 0) return p;
+    if (T <= kW8SmallT) {  // one batch of loads per wavefront
+        p.range = 32 * 8 * kPrepWaves;
+    } else {
+        p.tt = T >= 1024 ? 2 : 1;
+        const int64_t blocks = ceil_div(T, 16 * p.tt) * ceil_div((int64_t)r, 64);
+        const int64_t want = std::max<int64_t>(1, 512 / blocks);
+        p.range = (int)std::max<int64_t>(32 * 4 * kPrepWaves, ceil_div(ceil_div(d, want), 32) * 32);
+    }
+    p.range = std::min<int>(p.range, (int)d);
+    p.ks = (int)ceil_div(d, p.range);
+    return p;
+}
+
+hipError_t launch_w8a8_prep(const PrepArgs& a, const PrepPlan& p, hipStream_t stream) {
+    if (a.d % kGroup != 0 || a.d > kPrepMaxD) return hipErrorInvalidValue;
+    if (p.nj == 1) launch_prep_t<1, 1>(a, stream);
+    else if (p.tt == 1) launch_prep_t<1, 4>(a, stream);
+    else launch_prep_t<2, 4>(a, stream);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || a.r == 0 || p.nj == 1 || a.part == nullptr) return e;
+    hipLaunchKernelGGL(prep_join_kernel, dim3((unsigned)ceil_div((int64_t)a.T * a.rp / 4, 256)), dim3(256), 0, stream, a);
     return hipGetLastError();
 }
 

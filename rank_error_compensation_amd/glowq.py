@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 from typing import List, Optional, Sequence
 
@@ -89,8 +90,8 @@ EXPORTS = {
     "glowq_w8_sz_bytes": (_sz, [_i64]),
     "glowq_repack_w8": (ctypes.c_int, [_vp, _vp, _i64, _i64, _vp, _vp, _vp, _vp]),
     "glowq_w8a8_workspace_bytes": (_sz, [_i64, _i64, _i32]),
-    "glowq_group_forward_w8a8": (ctypes.c_int, [_vp, _i64, _i64, _i32, ctypes.POINTER(QWeightC), _vp,
-                                                ctypes.POINTER(_vp), _i32, _i32, _vp, _sz, ctypes.POINTER(_vp), _vp]),
+    # host arrays as addresses (packed bytes or ctypes arrays)
+    "glowq_group_forward_w8a8": (ctypes.c_int, [_vp, _i64, _i64, _i32, _vp, _vp, _vp, _i32, _i32, _vp, _sz, _vp, _vp]),
     "glowq_moe_sort_workspace_bytes": (_sz, [_i64, _i64, _i32]),
     "glowq_moe_sort": (ctypes.c_int, [_vp, _i64, _i64, _i32, _vp, _vp, _vp, _vp, _sz, _vp]),
     "glowq_moe_dispatch": (ctypes.c_int, [_vp, _i64, _i64, _i32, _vp, _i64, _vp, _vp, _sz, _vp]),
@@ -177,34 +178,31 @@ _DTYPES = {torch.float16: DTYPE_F16, torch.float32: DTYPE_F32}
 
 def _same_place(what: str, first: torch.Tensor, *others) -> None:
     """Dense GPU tensors of one device (None allowed among the others)."""
-    _require(first.is_cuda and first.is_contiguous(), ERR_INVALID_ARG, f"{what}: dense GPU tensors")
-    dev = first.device
+    dev = first.get_device() if first.is_cuda else -1
+    if dev < 0 or not first.is_contiguous():
+        raise GlowQError(ERR_INVALID_ARG, f"{what}: dense GPU tensors")
     for t in others:
-        if t is not None and (t.device != dev or not t.is_contiguous()):
+        if t is not None and (t.get_device() != dev or not t.is_contiguous()):
             raise GlowQError(ERR_INVALID_ARG, f"{what}: dense tensors on one device")
 
 
-class _On:
-    """The device of a call's tensors made current and, when a stream is given, that stream too, so
-    that what the call allocates belongs to the stream it is used on."""
-    __slots__ = ("ctx",)
+def _elsewhere(t: torch.Tensor, stream):
+    """None where the call can go to the current stream of the current device; else the context that
+    makes the tensors' device, or the given stream, current -- so that what the call allocates belongs
+    to the stream that uses it."""
+    if stream is not None:
+        _require(stream.device == t.device, ERR_INVALID_ARG, "stream of another device than the tensors")
+        return torch.cuda.stream(stream)
+    return torch.cuda.device(t.device) if t.get_device() != torch.cuda.current_device() else None
 
-    def __init__(self, t: torch.Tensor, stream):
-        if stream is not None:
-            _require(stream.device == t.device, ERR_INVALID_ARG, "stream of another device than the tensors")
-            self.ctx = torch.cuda.stream(stream)
-        elif t.get_device() != torch.cuda.current_device():
-            self.ctx = torch.cuda.device(t.device)
-        else:
-            self.ctx = None
 
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+
+def _current(t: torch.Tensor) -> int:
+    """Handle of the current stream of the tensor's device."""
+    dev = t.get_device()
+    return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
 
 
 # --------------------------------------------------------------------------- weights
@@ -276,7 +274,8 @@ class QWeight:
         qb, zb = L.glowq_w8_q_bytes(n_out, k_in), L.glowq_w8_sz_bytes(n_out)
         if qb == 0 or zb == 0:
             raise GlowQError(ERR_SHAPE, "glowq_w8_q_bytes")
-        with _On(c, None):
+        _require(c.is_cuda, ERR_INVALID_ARG, "from_int8: a GPU device")
+        with torch.cuda.device(c.device):
             q_dev = torch.empty(qb, dtype=torch.uint8, device=c.device)
             sz_dev = torch.empty(zb, dtype=torch.uint8, device=c.device)
             flag = torch.empty(1, dtype=torch.int32, device=c.device)
@@ -532,39 +531,51 @@ def w8a8_workspace_bytes(T: int, d: int, r: int) -> int:
     return int(lib().glowq_w8a8_workspace_bytes(T, d, r))
 
 
+_WEIGHT = struct.Struct("QQqqii")
+
+
 def group_forward_w8a8(x: torch.Tensor, weights: Sequence[QWeight], b: Optional[torch.Tensor],
                        a: Sequence[torch.Tensor], r: int, restore: bool = True,
                        workspace: Optional[torch.Tensor] = None, y: Optional[List[torch.Tensor]] = None,
                        stream=None) -> List[torch.Tensor]:
     """glowq_group_forward_w8a8: 8-bit integer weights (QWeight.from_int8) and activations, scales
     per output row and per token, the correction on the fp16 activations."""
-    m = len(weights)
-    a = list(a) if a is not None else []
-    _same_place("group_forward_w8a8", x, b, workspace, *a, *(y or ()))
-    _require(x.dim() == 2 and x.dtype == torch.float16, ERR_INVALID_ARG, "group_forward_w8a8: x fp16 [T][d]")
+    what = "group_forward_w8a8"
+    a = a or ()
+    _same_place(what, x, b, workspace, *a, *(y or ()), *[w.q for w in weights], *[w.sz for w in weights])
+    ctx = _elsewhere(x, stream)
+    if ctx is not None:
+        with ctx:
+            return group_forward_w8a8(x, weights, b, a, r, restore, workspace, y)
+    if x.dim() != 2 or x.dtype != torch.float16:
+        raise GlowQError(ERR_INVALID_ARG, f"{what}: x fp16 [T][d]")
     T, d = x.shape
-    for w in weights:
-        _require(w.q.device == x.device, ERR_INVALID_ARG, "group_forward_w8a8: weights on the device of x")
-    if restore and r > 0:
-        _require(b is not None and len(a) == m, ERR_INVALID_ARG, "group_forward_w8a8: a factor per module")
-        _require(b.dtype == torch.float16 and all(t.dtype == torch.float16 for t in a), ERR_INVALID_ARG,
-                 "group_forward_w8a8: fp16 factors")
-        _require(tuple(b.shape) == (r, d) and all(tuple(t.shape) == (w.n_out, r) for t, w in zip(a, weights)), ERR_SHAPE,
-                 "group_forward_w8a8: b [r][d], a[i] [n_out][r]")
-    with _On(x, stream):
-        if y is None:
-            y = _outs(x, weights, None)
-        else:
-            _require(len(y) == m and all(t.dtype == torch.float16 and tuple(t.shape) == (T, w.n_out)
-                                         for t, w in zip(y, weights)), ERR_SHAPE, "group_forward_w8a8: y[i] fp16 [T][n_out]")
-        if workspace is None and T > 0:
-            n = w8a8_workspace_bytes(T, d, r if restore else 0)
-            workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=x.device)
-        wc = _arr(QWeightC, [w.c() for w in weights])
-        ac = _arr(_vp, [t.data_ptr() for t in a]) if a else None
-        yc = _arr(_vp, [t.data_ptr() for t in y])
-        check(lib().glowq_group_forward_w8a8(_ptr(x), T, d, m, wc, _ptr(b), ac, r, int(bool(restore)), _ptr(workspace),
-                                             _bytes(workspace), yc, _stream()), "glowq_group_forward_w8a8")
+    m = len(weights)
+    correct = bool(restore) and r > 0
+    ap = None
+    if correct:
+        if b is None or len(a) != m or b.dtype != torch.float16:
+            raise GlowQError(ERR_INVALID_ARG, f"{what}: fp16 factors, one per module")
+        _require(b.shape == (r, d), ERR_SHAPE, f"{what}: b [r][d]")
+        for t, w in zip(a, weights):
+            if t.dtype != torch.float16 or t.shape != (w.n_out, r):
+                raise GlowQError(ERR_SHAPE, f"{what}: a[i] fp16 [n_out][r]")
+        ap = struct.pack(f"{m}Q", *[t.data_ptr() for t in a])
+    if y is None:
+        y = [x.new_empty((T, w.n_out)) for w in weights]
+    else:
+        _require(len(y) == m, ERR_SHAPE, f"{what}: an output per module")
+        for t, w in zip(y, weights):
+            _require(t.dtype == torch.float16 and t.shape == (T, w.n_out), ERR_SHAPE, f"{what}: y[i] fp16 [T][n_out]")
+    if workspace is None and T > 0:
+        workspace = torch.empty(max(w8a8_workspace_bytes(T, d, r if correct else 0), 256), dtype=torch.uint8,
+                                device=x.device)
+    wp = b"".join([_WEIGHT.pack(w.q.data_ptr(), w.sz.data_ptr(), w.n_out, w.k_in, w.fmt, 0) for w in weights])
+    yp = struct.pack(f"{m}Q", *[t.data_ptr() for t in y])
+    st = lib().glowq_group_forward_w8a8(x.data_ptr(), T, d, m, wp, _addr(b), ap, r, 1 if correct else 0,
+                                        _addr(workspace), _bytes(workspace), yp, _current(x))
+    if st != OK:
+        check(st, "glowq_group_forward_w8a8")
     return y
 
 
@@ -624,22 +635,28 @@ def _moe_ws(workspace: Optional[torch.Tensor], like: torch.Tensor, n: int) -> to
 
 def _new(out: Optional[torch.Tensor], shape, dtype, like: torch.Tensor, what: str) -> torch.Tensor:
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
-    _require(out.dtype == dtype and tuple(out.shape) == tuple(shape), ERR_SHAPE, f"{what}: out {list(shape)} {dtype}")
+        return like.new_empty(shape, dtype=dtype)
+    if out.dtype != dtype or out.shape != shape:
+        raise GlowQError(ERR_SHAPE, f"{what}: out {list(shape)} {dtype}")
     return out
 
 
 def _row_dtype(what: str, t: torch.Tensor) -> int:
-    _require(t.dim() == 2 and t.dtype in _DTYPES, ERR_INVALID_ARG, f"{what}: fp16 or fp32 rows [n][d]")
-    return _DTYPES[t.dtype]
+    dt = _DTYPES.get(t.dtype)
+    if dt is None or t.dim() != 2:
+        raise GlowQError(ERR_INVALID_ARG, f"{what}: fp16 or fp32 rows [n][d]")
+    return dt
 
 
 def _pairs(what: str, pair_row: torch.Tensor, weights: Optional[torch.Tensor]):
-    _require(pair_row.dim() == 2 and pair_row.dtype == torch.int32, ERR_INVALID_ARG, f"{what}: int32 lists [T][top_k]")
+    if pair_row.dim() != 2 or pair_row.dtype != torch.int32:
+        raise GlowQError(ERR_INVALID_ARG, f"{what}: int32 lists [T][top_k]")
     if weights is not None:
-        _require(weights.dtype == torch.float32, ERR_INVALID_ARG, f"{what}: fp32 weights")
-        _require(weights.shape == pair_row.shape, ERR_SHAPE, f"{what}: weights [T][top_k]")
-    return int(pair_row.shape[0]), int(pair_row.shape[1])
+        if weights.dtype != torch.float32:
+            raise GlowQError(ERR_INVALID_ARG, f"{what}: fp32 weights")
+        if weights.shape != pair_row.shape:
+            raise GlowQError(ERR_SHAPE, f"{what}: weights [T][top_k]")
+    return pair_row.shape
 
 
 _MOE_HEADER = 8192
@@ -654,14 +671,21 @@ def moe_sort(expert_ids: torch.Tensor, n_exp: int, workspace: Optional[torch.Ten
     int32 [T top_k], pair_row int32 [T][top_k]); `out` may hold the three."""
     T, k = _pairs("moe_sort", expert_ids, None)
     _same_place("moe_sort", expert_ids, workspace, *(out or ()))
-    with _On(expert_ids, stream):
-        off, tok, pr = out if out is not None else (None, None, None)
-        off = _new(off, (n_exp + 1,), torch.int32, expert_ids, "moe_sort")
-        tok = _new(tok, (T * k,), torch.int32, expert_ids, "moe_sort")
-        pr = _new(pr, (T, k), torch.int32, expert_ids, "moe_sort")
-        ws = _moe_ws(workspace, expert_ids, max(moe_sort_workspace_bytes(T, k, n_exp), _MOE_HEADER))
-        check(lib().glowq_moe_sort(expert_ids.data_ptr(), T, k, n_exp, off.data_ptr(), tok.data_ptr(), pr.data_ptr(),
-                                   ws.data_ptr(), _bytes(ws), _stream()), "glowq_moe_sort")
+    ctx = _elsewhere(expert_ids, stream)
+    if ctx is not None:
+        with ctx:
+            return moe_sort(expert_ids, n_exp, workspace, out)
+    if out is None:
+        off, tok, pr = expert_ids.new_empty(n_exp + 1), expert_ids.new_empty(T * k), expert_ids.new_empty((T, k))
+    else:
+        off, tok, pr = (_new(o, s, torch.int32, expert_ids, "moe_sort") for o, s in zip(out, ((n_exp + 1,), (T * k,), (T, k))))
+    ws = workspace
+    if ws is None:
+        ws = _moe_ws(None, expert_ids, max(moe_sort_workspace_bytes(T, k, n_exp), _MOE_HEADER))
+    st = lib().glowq_moe_sort(expert_ids.data_ptr(), T, k, n_exp, off.data_ptr(), tok.data_ptr(), pr.data_ptr(),
+                              ws.data_ptr(), _bytes(ws), _current(expert_ids))
+    if st != OK:
+        check(st, "glowq_moe_sort")
     return off, tok, pr
 
 
@@ -669,14 +693,21 @@ def moe_dispatch(x: torch.Tensor, row_token: torch.Tensor, workspace: Optional[t
                  out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """glowq_moe_dispatch: rows [n_rows][d] = x[row_token], zeros for token -1 (row_token int32 [n_rows])."""
     dt = _row_dtype("moe_dispatch", x)
-    _require(row_token.dim() == 1 and row_token.dtype == torch.int32, ERR_INVALID_ARG, "moe_dispatch: int32 list [n_rows]")
+    if row_token.dim() != 1 or row_token.dtype != torch.int32:
+        raise GlowQError(ERR_INVALID_ARG, "moe_dispatch: int32 list [n_rows]")
     _same_place("moe_dispatch", x, row_token, workspace, out)
-    (T, d), n = x.shape, row_token.shape[0]
-    with _On(x, stream):
-        out = _new(out, (n, d), x.dtype, x, "moe_dispatch")
-        ws = _moe_ws(workspace, x, _MOE_HEADER)
-        check(lib().glowq_moe_dispatch(x.data_ptr(), T, d, dt, row_token.data_ptr(), n, out.data_ptr(), ws.data_ptr(),
-                                       _bytes(ws), _stream()), "glowq_moe_dispatch")
+    ctx = _elsewhere(x, stream)
+    if ctx is not None:
+        with ctx:
+            return moe_dispatch(x, row_token, workspace, out)
+    T, d = x.shape
+    n = row_token.shape[0]
+    out = _new(out, (n, d), x.dtype, x, "moe_dispatch")
+    ws = _moe_ws(workspace, x, _MOE_HEADER)
+    st = lib().glowq_moe_dispatch(x.data_ptr(), T, d, dt, row_token.data_ptr(), n, out.data_ptr(), ws.data_ptr(),
+                                  _bytes(ws), _current(x))
+    if st != OK:
+        check(st, "glowq_moe_dispatch")
     return out
 
 
@@ -687,21 +718,26 @@ def moe_combine(rows: torch.Tensor, pair_row: torch.Tensor, weights: Optional[to
     dt = _row_dtype("moe_combine", rows)
     T, k = _pairs("moe_combine", pair_row, weights)
     _same_place("moe_combine", rows, pair_row, weights, add, workspace, out)
+    ctx = _elsewhere(rows, stream)
+    if ctx is not None:
+        with ctx:
+            return moe_combine(rows, pair_row, weights, add, workspace, out)
     n, d = rows.shape
-    if add is not None:
-        _require(add.dtype == rows.dtype and tuple(add.shape) == (T, d), ERR_SHAPE, "moe_combine: add [T][d]")
-    with _On(rows, stream):
-        out = _new(out, (T, d), rows.dtype, rows, "moe_combine")
-        ws = _moe_ws(workspace, rows, _MOE_HEADER)
-        check(lib().glowq_moe_combine(rows.data_ptr(), n, pair_row.data_ptr(), _addr(weights), _addr(add), T, k, d, dt,
-                                      out.data_ptr(), ws.data_ptr(), _bytes(ws), _stream()), "glowq_moe_combine")
+    if add is not None and (add.dtype != rows.dtype or add.shape != (T, d)):
+        raise GlowQError(ERR_SHAPE, "moe_combine: add [T][d]")
+    out = _new(out, (T, d), rows.dtype, rows, "moe_combine")
+    ws = _moe_ws(workspace, rows, _MOE_HEADER)
+    st = lib().glowq_moe_combine(rows.data_ptr(), n, pair_row.data_ptr(), _addr(weights), _addr(add), T, k, d, dt,
+                                 out.data_ptr(), ws.data_ptr(), _bytes(ws), _current(rows))
+    if st != OK:
+        check(st, "glowq_moe_combine")
     return out
 
 
 def moe_dispatch_backward(d_rows: torch.Tensor, pair_row: torch.Tensor, workspace: Optional[torch.Tensor] = None,
                           out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Gradient of moe_dispatch: dx [T][d] = sum_j d_rows[pair_row[:, j]] (glowq_moe_combine without weights)."""
-    return moe_combine(d_rows, pair_row, None, workspace=workspace, out=out, stream=stream)
+    return moe_combine(d_rows, pair_row, None, None, workspace, out, stream)
 
 
 def moe_combine_backward(dy: torch.Tensor, rows: torch.Tensor, pair_row: torch.Tensor, row_token: torch.Tensor,
@@ -709,42 +745,55 @@ def moe_combine_backward(dy: torch.Tensor, rows: torch.Tensor, pair_row: torch.T
                          stream=None):
     """glowq_moe_combine_backward: (d_rows [n_rows][d], d_weights fp32 [T][top_k]) for dy [T][d]; rows of
     token -1 get zeros, rows that no pair takes are left as they were (`out` may hold the two tensors)."""
-    dt = _row_dtype("moe_combine_backward", rows)
-    T, k = _pairs("moe_combine_backward", pair_row, weights)
+    what = "moe_combine_backward"
+    dt = _row_dtype(what, rows)
+    T, k = _pairs(what, pair_row, weights)
+    _same_place(what, rows, dy, pair_row, row_token, weights, workspace, *(out or ()))
+    ctx = _elsewhere(rows, stream)
+    if ctx is not None:
+        with ctx:
+            return moe_combine_backward(dy, rows, pair_row, row_token, weights, workspace, out)
     n, d = rows.shape
-    _same_place("moe_combine_backward", rows, dy, pair_row, row_token, weights, workspace, *(out or ()))
-    _require(dy.dtype == rows.dtype and tuple(dy.shape) == (T, d), ERR_SHAPE, "moe_combine_backward: dy [T][d]")
-    _require(row_token.dtype == torch.int32 and row_token.dim() == 1, ERR_INVALID_ARG,
-             "moe_combine_backward: int32 list [n_rows]")
-    _require(row_token.shape[0] == n, ERR_SHAPE, "moe_combine_backward: row_token [n_rows]")
-    with _On(rows, stream):
-        d_rows, d_w = out if out is not None else (None, None)
-        d_rows = _new(d_rows, (n, d), rows.dtype, rows, "moe_combine_backward")
-        d_w = _new(d_w, (T, k), torch.float32, rows, "moe_combine_backward")
-        ws = _moe_ws(workspace, rows, _MOE_HEADER)
-        check(lib().glowq_moe_combine_backward(dy.data_ptr(), rows.data_ptr(), n, pair_row.data_ptr(),
-                                               row_token.data_ptr(), _addr(weights), T, k, d, dt, d_rows.data_ptr(),
-                                               d_w.data_ptr(), ws.data_ptr(), _bytes(ws), _stream()),
-              "glowq_moe_combine_backward")
+    if dy.dtype != rows.dtype or dy.shape != (T, d):
+        raise GlowQError(ERR_SHAPE, f"{what}: dy [T][d]")
+    if row_token.dtype != torch.int32 or row_token.dim() != 1:
+        raise GlowQError(ERR_INVALID_ARG, f"{what}: int32 list [n_rows]")
+    _require(row_token.shape[0] == n, ERR_SHAPE, f"{what}: row_token [n_rows]")
+    d_rows, d_w = out if out is not None else (None, None)
+    d_rows = _new(d_rows, (n, d), rows.dtype, rows, what)
+    d_w = _new(d_w, (T, k), torch.float32, rows, what)
+    ws = _moe_ws(workspace, rows, _MOE_HEADER)
+    st = lib().glowq_moe_combine_backward(dy.data_ptr(), rows.data_ptr(), n, pair_row.data_ptr(), row_token.data_ptr(),
+                                          _addr(weights), T, k, d, dt, d_rows.data_ptr(), d_w.data_ptr(), ws.data_ptr(),
+                                          _bytes(ws), _current(rows))
+    if st != OK:
+        check(st, "glowq_moe_combine_backward")
     return d_rows, d_w
 
 
 # --------------------------------------------------------------------------- gated activation
 def _gate_dtype(what: str, first: torch.Tensor, *others) -> int:
-    _require(first.dtype in _DTYPES, ERR_INVALID_ARG, f"{what}: fp16 or fp32")
+    dt = _DTYPES.get(first.dtype)
+    if dt is None:
+        raise GlowQError(ERR_INVALID_ARG, f"{what}: fp16 or fp32")
     for t in others:
-        _require(t.dtype == first.dtype and t.shape == first.shape, ERR_SHAPE, f"{what}: tensors of one type and shape")
-    return _DTYPES[first.dtype]
+        if t.dtype != first.dtype or t.shape != first.shape:
+            raise GlowQError(ERR_SHAPE, f"{what}: tensors of one type and shape")
+    return dt
 
 
 def swiglu(gate: torch.Tensor, up: torch.Tensor, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """glowq_swiglu: gate sigmoid(gate) up, elementwise."""
     dt = _gate_dtype("swiglu", gate, up)
     _same_place("swiglu", gate, up, out)
-    with _On(gate, stream):
-        out = _new(out, gate.shape, gate.dtype, gate, "swiglu")
-        check(lib().glowq_swiglu(gate.data_ptr(), up.data_ptr(), gate.numel(), dt, out.data_ptr(), _stream()),
-              "glowq_swiglu")
+    ctx = _elsewhere(gate, stream)
+    if ctx is not None:
+        with ctx:
+            return swiglu(gate, up, out)
+    out = _new(out, gate.shape, gate.dtype, gate, "swiglu")
+    st = lib().glowq_swiglu(gate.data_ptr(), up.data_ptr(), gate.numel(), dt, out.data_ptr(), _current(gate))
+    if st != OK:
+        check(st, "glowq_swiglu")
     return out
 
 
@@ -752,12 +801,17 @@ def swiglu_backward(dh: torch.Tensor, gate: torch.Tensor, up: torch.Tensor, out=
     """glowq_swiglu_backward: (d_gate, d_up) for dh (`out` may hold the two tensors)."""
     dt = _gate_dtype("swiglu_backward", gate, up, dh)
     _same_place("swiglu_backward", gate, up, dh, *(out or ()))
-    with _On(gate, stream):
-        dg, du = out if out is not None else (None, None)
-        dg = _new(dg, gate.shape, gate.dtype, gate, "swiglu_backward")
-        du = _new(du, gate.shape, gate.dtype, gate, "swiglu_backward")
-        check(lib().glowq_swiglu_backward(dh.data_ptr(), gate.data_ptr(), up.data_ptr(), gate.numel(), dt, dg.data_ptr(),
-                                          du.data_ptr(), _stream()), "glowq_swiglu_backward")
+    ctx = _elsewhere(gate, stream)
+    if ctx is not None:
+        with ctx:
+            return swiglu_backward(dh, gate, up, out)
+    dg, du = out if out is not None else (None, None)
+    dg = _new(dg, gate.shape, gate.dtype, gate, "swiglu_backward")
+    du = _new(du, gate.shape, gate.dtype, gate, "swiglu_backward")
+    st = lib().glowq_swiglu_backward(dh.data_ptr(), gate.data_ptr(), up.data_ptr(), gate.numel(), dt, dg.data_ptr(),
+                                     du.data_ptr(), _current(gate))
+    if st != OK:
+        check(st, "glowq_swiglu_backward")
     return dg, du
 
 

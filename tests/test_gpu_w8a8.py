@@ -74,10 +74,7 @@ def test_w8a8_matches_reference(T, d, rows, r):
         torch.cuda.synchronize()
         codes, scale = G.quantize_x_int8(u.x)
         raw = ws.cpu().numpy()
-        t = np.arange(T)[:, None]
-        place = np.arange(8)[None, :] ^ (t % 8) ^ (t // 8 % 2)  # documented: where piece c of a group lies
-        pieces = raw[: T * d].view(np.int8).reshape(T, d // 128, 8, 16)
-        assert np.array_equal(np.stack([pieces[i][:, place[i]].reshape(d) for i in range(T)]), codes)
+        assert np.array_equal(raw[: T * d].view(np.int8).reshape(T, d), codes)
         o = (T * d + 255) // 256 * 256
         assert np.array_equal(raw[o: o + 4 * T].view(np.uint32), scale.astype(np.float32).reshape(-1).view(np.uint32))
         u.check(ys, restore, f"restore={restore}")
