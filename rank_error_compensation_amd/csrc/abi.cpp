@@ -531,9 +531,10 @@ W8Shape choose_w8a8_shape(const Call& c) {
         for (int i = 0; i < c.m; ++i) n += ceil_div(ceil_div(c.w[i].n_out, 16), rr);
         return n * ceil_div(c.T, 16 * tt);
     };
-    s.tt = s.rr = 16;
-    if (tiles(16, 16) >= 256) return s;
-    s.tt = s.rr = 8;
+    s.tt = 8;
+    s.rr = 16;
+    if (tiles(8, 16) >= 512) return s;
+    s.rr = 8;
     const int64_t n = tiles(8, 8), G = c.d / kGroup;
     if (n < 256) {
         int64_t ks = std::min<int64_t>(ceil_div(256, n), std::max<int64_t>(1, G / 8));
