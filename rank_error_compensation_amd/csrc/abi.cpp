@@ -519,8 +519,11 @@ int run_w4a8(const Call& c, void* workspace, hipStream_t stream) {
 // K ranges' int32 tiles of a call of more than 64 tokens: bounded by the workspace that
 // glowq_w8a8_workspace_bytes reserves for them.
 constexpr size_t kW8PartBytes = (size_t)32 << 20;
+// row stride of the projection: whole 64-column blocks, as the large tiles take them
+inline int64_t w8_r_pad(int32_t r) { return ceil_div(r, 64) * 64; }
+inline size_t w8_r_bytes(int64_t T, int32_t r) { return round256((size_t)T * (size_t)w8_r_pad(r) * 2u); }
 inline size_t w8_part_bytes(int64_t T, int32_t r, int ks) {
-    return round256((size_t)ks * (size_t)T * (size_t)r_pad_of(r) * 4u);
+    return round256((size_t)ks * (size_t)T * (size_t)w8_r_pad(r) * 4u);
 }
 
 W8Shape choose_w8a8_shape(const Call& c) {
@@ -555,7 +558,7 @@ int run_w8a8(const Call& c, void* workspace, hipStream_t stream) {
     base += round256((size_t)c.T * c.d);
     float* xscale = reinterpret_cast<float*>(base);
     base += round256((size_t)c.T * 4u);
-    const int32_t r = c.correct ? c.r : 0, rp = c.correct ? (int32_t)r_pad_of(c.r) : 0;
+    const int32_t r = c.correct ? c.r : 0, rp = c.correct ? (int32_t)w8_r_pad(r) : 0;
     const PrepPlan pp = w8a8_prep_plan(c.T, c.d, r);
     PrepArgs pa;
     std::memset(&pa, 0, sizeof(pa));
@@ -575,7 +578,7 @@ int run_w8a8(const Call& c, void* workspace, hipStream_t stream) {
             base += w8_part_bytes(c.T, r, pp.ks);
         }
         pa.R = reinterpret_cast<_Float16*>(base);
-        base += prefill_r_bytes(c.T, r, 1);
+        base += w8_r_bytes(c.T, r);
     }
     if (launch_w8a8_prep(pa, pp, stream) != hipSuccess) return GLOWQ_ERR_HIP;
     ForwardArgs f;
@@ -969,7 +972,7 @@ int glowq_repack_w8(const void* codes_dev, const float* scales_dev, int64_t n_ou
 size_t glowq_w8a8_workspace_bytes(int64_t T, int64_t d, int32_t r) {
     if (T <= 0 || T > kMaxT || d < kGroup || d % kGroup != 0 || d > kW8MaxD || r < 0 || r > GLOWQ_MAX_RANK) return 0;
     size_t n = round256((size_t)T * d) + round256((size_t)T * 4u);
-    if (r > 0) n += w8_part_bytes(T, r, w8a8_prep_plan(T, d, r).ks) + prefill_r_bytes(T, r, 1);
+    if (r > 0) n += w8_part_bytes(T, r, w8a8_prep_plan(T, d, r).ks) + w8_r_bytes(T, r);
     if (T > kW8SmallT) n += kW8PartBytes;
     return n;
 }

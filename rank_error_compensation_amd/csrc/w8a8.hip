@@ -140,7 +140,8 @@ __device__ void quant_tokens(const _Float16* __restrict__ x, int t0, int T, int 
     for (int i = 0; i < C; ++i) {
         const int c = sub + TPT * i;
         if (c < n8)
-            *reinterpret_cast<u2*>(xq + (size_t)t * d + 8 * (size_t)c) = some ? codes_of(v[i], scale, inv) : u2{0u, 0u};
+            *reinterpret_cast<u2*>(xq + (size_t)t * d + 8 * (size_t)c) =
+                some ? codes_of(v[i], scale, inv) : u2{0u, 0u};
     }
 }
 
@@ -385,58 +386,62 @@ __device__ __forceinline__ bool w8_place(const ForwardArgs& args, int& mb, int& 
     return true;
 }
 
-template <int WM, int WN, int TT>
-__global__ __launch_bounds__(64 * WM * WN, WM * WN <= 4 ? 2 : 1) void w8a8_tile_kernel(const ForwardArgs args) {
+enum : int { kW8Plain = 0, kW8Correct = 1, kW8Split = 2 };  // what follows the integer sums
+
+template <int WM, int WN, int TT, int MODE>
+__global__ __launch_bounds__(64 * WM * WN, 2) void w8a8_tile_kernel(const ForwardArgs args) {
     constexpr int RR = 4, NW = WM * WN, BM = 16 * TT * WM, SB = BM * 128;
     constexpr int NC = BM / 8 / NW;  // 1 KB code copies per wavefront and group
-    static_assert(NC * 8 * NW == BM && NC + 2 * RR < 64, "copies");
+    static_assert(NC * 8 * NW == BM && NC + 3 * RR < 63 && BM % 64 == 0, "copies");
     __shared__ __attribute__((aligned(16))) uint8_t st0[SB];
     __shared__ __attribute__((aligned(16))) uint8_t st1[SB];
     __shared__ __attribute__((aligned(16))) uint8_t st2[SB];
     __shared__ __attribute__((aligned(16))) uint8_t st3[SB];
+    __shared__ __attribute__((aligned(16))) float row_scale[NW * 64];
+    __shared__ __attribute__((aligned(16))) float tok_scale[BM];
     int mb, col;
     if (!w8_place(args, mb, col)) return;
-    const int ks = args.tile_ks, nbl = col / ks, kr = col - nbl * ks;
+    const int ks = MODE == kW8Split ? args.tile_ks : 1, nbl = col / ks, kr = col - nbl * ks;
     const ModuleArgs M = args.mod[module_of(args, nbl)];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int wm = wave % WM, wn = wave / WM;
     const int T = args.T, d = args.d, NT = M.n_tiles16;
     const int m0 = mb * BM, rt0 = (nbl - M.tile_begin) * RR * WN + wn * RR;
-    const int g_begin = kr * args.dec_gk, g_end = min(g_begin + args.dec_gk, args.G);
-
-    // code copy i of wave w fills rows 8 (NC w + i) .. + 7 of the stage; lane l lands at row + l / 8,
+    const int g_begin = kr * args.dec_gk, n_g = min(args.dec_gk, args.G - g_begin);
+    // copy i of wave w fills rows 8 (NC w + i) .. + 7 of the stage; lane l lands at row + l / 8,
     // position l % 8, holding the row's piece (l % 8) ^ f(row)
     uint32_t xoff[NC];
+    const uint32_t piece = 16 * ((lane & 7) ^ (lane >> 3));  // f(row) for even i; odd i flips bit 0
+    static_assert(NC % 2 == 0, "row 8 (NC w + i) has parity i");
 #pragma unroll
-    for (int i = 0; i < NC; ++i) {
-        const int row = 8 * (NC * wave + i) + (lane >> 3);
-        xoff[i] = (uint32_t)(min(m0 + row, T - 1) * d + 16 * ((lane & 7) ^ (row & 7) ^ ((row >> 3) & 1)));
-    }
+    for (int i = 0; i < NC; ++i)
+        xoff[i] = (uint32_t)(min(m0 + 8 * (NC * wave + i) + (lane >> 3), T - 1) * d) + (piece ^ (16 * (i & 1)));
     const int fr = (lane & 7) ^ ((lane >> 3) & 1);
     const int rbase = (16 * TT * wm + (lane & 15)) * 128;
     const int rofs0 = rbase + 16 * ((lane >> 4) ^ fr), rofs1 = rbase + 16 * ((4 + (lane >> 4)) ^ fr);
-    // row tiles are the wavefront's own, so weight addresses are scalar but for the lane's 16 bytes
-    uint32_t rofs[RR];
+    uint32_t rts[RR];  // the wavefront's row tiles (scalar: weight addresses are scalar but for the lane's 16 bytes)
 #pragma unroll
-    for (int rr = 0; rr < RR; ++rr) rofs[rr] = (uint32_t)min(rt0 + rr, NT - 1);
+    for (int rr = 0; rr < RR; ++rr) rts[rr] = (uint32_t)min(rt0 + rr, NT - 1);
     const uint32_t lofs = lane * 16;
 
-    auto copy = [&](int g, uint8_t* stg) {
-        const int8_t* xb = args.xq + (size_t)min(g, g_end - 1) * kGroup;
+    auto copy = [&](int v, uint8_t* stg) {
+        const int8_t* base = args.xq + (size_t)(g_begin + min(v, n_g - 1)) * kGroup;
 #pragma unroll
         for (int i = 0; i < NC; ++i)
-            __builtin_amdgcn_global_load_lds((const void*)(xb + xoff[i]), (lds_void*)(stg + 8 * (NC * wave + i) * 128), 16, 0,
+            __builtin_amdgcn_global_load_lds((const void*)(base + xoff[i]), (lds_void*)(stg + 8 * (NC * wave + i) * 128), 16, 0,
                                              0);
     };
-    i4v w[2][RR][2];
-    auto wload = [&](int g, int slot) {
+    // Operands in flight: where registers allow (TT = 4), whole groups three ahead, group v in slot v % 4;
+    // else halves, half h = 2 v + m in slot h % 4, three halves ahead.
+    constexpr bool kDeep = TT <= 4;
+    constexpr int kAhead = kDeep ? 3 : 2;  // groups the code copies are ahead
+    i4v w[kDeep ? 8 : 4][RR];
+    auto wload = [&](int v, int m, int slot) {
+        const size_t g = (size_t)(g_begin + min(v, n_g - 1)) * NT;
 #pragma unroll
-        for (int rr = 0; rr < RR; ++rr) {
-            const uint8_t* qb = M.q + ((size_t)min(g, g_end - 1) * NT + rofs[rr]) * kW8Block;
-#pragma unroll
-            for (int m = 0; m < 2; ++m) w[slot][rr][m] = *reinterpret_cast<const i4v*>(qb + 1024 * m + lofs);
-        }
+        for (int rr = 0; rr < RR; ++rr)
+            w[slot][rr] = *reinterpret_cast<const i4v*>(M.q + (g + rts[rr]) * kW8Block + 1024 * m + lofs);
     };
     i4v acc[TT][RR];
 #pragma unroll
@@ -444,50 +449,92 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN <= 4 ? 2 : 1) void w8a8_tile_
 #pragma unroll
         for (int rr = 0; rr < RR; ++rr) acc[tt][rr] = i4v{0, 0, 0, 0};
 
-    copy(g_begin, st0);
-    wload(g_begin, 0);
-    copy(g_begin + 1, st1);
+    {
+        const uint32_t rt = (uint32_t)min(rt0 + (lane >> 4), NT - 1);
+        __builtin_amdgcn_global_load_lds((const void*)(M.sz + (rt * 64 + (lane & 15) * 4)), (lds_void*)(row_scale + wave * 64),
+                                         4, 0, 0);
+        const int t0 = 64 * (wave % (BM / 64));
+        __builtin_amdgcn_global_load_lds((const void*)(args.xscale + min(m0 + t0 + lane, T - 1)),
+                                         (lds_void*)(tok_scale + t0), 4, 0, 0);
+    }
+    copy(0, st0);
+    wload(0, 0, 0);
+    wload(0, 1, 1);
+    copy(1, st1);
+    wload(1, 0, 2);
+    if constexpr (kDeep) {
+        wload(1, 1, 3);
+        copy(2, st2);
+        wload(2, 0, 4);
+        wload(2, 1, 5);
+    }
 
-    // group g in stage S = (g - g_begin) % 4, weights in slot S % 2.  At the barrier the copies of g and
-    // the weights of g have landed: only the NC copies of g + 1, issued last, may be in flight.  Then
-    // the weights of g + 1 and the copies of g + 2 are issued; their stage was last read in group g - 2.
-    auto step = [&](int g, auto Sc) {
+    // Group v in stage S = v % 4.  At the barrier its copies have landed: after them at most those of the
+    // kAhead - 1 groups behind it and the operands in flight were issued.  The copies of v + kAhead go to a
+    // stage whose last reads were before this barrier; operands go to slots whose last steps were issued.
+    auto step = [&](int v, auto Sc) {
         constexpr int S = decltype(Sc)::value;
-        uint8_t* cur = S == 0 ? st0 : (S == 1 ? st1 : (S == 2 ? st2 : st3));
-        uint8_t* nxt = S == 0 ? st2 : (S == 1 ? st3 : (S == 2 ? st0 : st1));
-        __builtin_amdgcn_s_waitcnt(0x0F70 | NC);  // vmcnt(NC)
+        constexpr int N = kDeep ? 2 * NC + 6 * RR : NC + 3 * RR;
+        static_assert(N < 64, "vmcnt");
+        uint8_t* const st[4] = {st0, st1, st2, st3};
+        uint8_t* cur = st[S];
+        uint8_t* nxt = st[(S + kAhead) & 3];
+        __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | ((N >> 4) << 14));  // vmcnt(N)
         __builtin_amdgcn_s_barrier();
-        wload(g + 1, (S + 1) & 1);
-        __builtin_amdgcn_sched_barrier(0);
-        copy(g + 2, nxt);
-        __builtin_amdgcn_sched_barrier(0);
-        if (g >= g_end) return;
-        i4v x[2][2];
-        x[0][0] = *reinterpret_cast<const i4v*>(cur + rofs0);
-        x[0][1] = *reinterpret_cast<const i4v*>(cur + rofs1);
+        if constexpr (kDeep) {
+            copy(v + 3, nxt);
+            wload(v + 3, 0, (2 * S + 6) & 7);
+            wload(v + 3, 1, (2 * S + 7) & 7);
+            __builtin_amdgcn_sched_barrier(0);
+            if (v >= n_g) return;
+            i4v x[2][2];
+            x[0][0] = *reinterpret_cast<const i4v*>(cur + rofs0);
+            x[0][1] = *reinterpret_cast<const i4v*>(cur + rofs1);
 #pragma unroll
-        for (int tt = 0; tt < TT; ++tt) {
-            if (tt + 1 < TT) {
-                x[(tt + 1) & 1][0] = *reinterpret_cast<const i4v*>(cur + rofs0 + (tt + 1) * 2048);
-                x[(tt + 1) & 1][1] = *reinterpret_cast<const i4v*>(cur + rofs1 + (tt + 1) * 2048);
+            for (int tt = 0; tt < TT; ++tt) {
+                if (tt + 1 < TT) {
+                    x[(tt + 1) & 1][0] = *reinterpret_cast<const i4v*>(cur + rofs0 + (tt + 1) * 2048);
+                    x[(tt + 1) & 1][1] = *reinterpret_cast<const i4v*>(cur + rofs1 + (tt + 1) * 2048);
+                }
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int rr = 0; rr < RR; ++rr) acc[tt][rr] = mfma_i8(w[2 * S + m][rr], x[tt & 1][m], acc[tt][rr]);
             }
+            __builtin_amdgcn_sched_barrier(0);
+            return;
+        }
 #pragma unroll
-            for (int m = 0; m < 2; ++m)
+        for (int m = 0; m < 2; ++m) {
+            wload(v + 1 + m, 1 - m, (2 * S + m + 3) & 3);
+            if (m == 0) copy(v + 2, nxt);
+            __builtin_amdgcn_sched_barrier(0);
+            if (v >= n_g) continue;
+            const int at = m == 0 ? rofs0 : rofs1;
+            constexpr int D = 4;  // operand reads in flight: D - 1 ahead of the steps that take them
+            i4v x[D];
 #pragma unroll
-                for (int rr = 0; rr < RR; ++rr) acc[tt][rr] = mfma_i8(w[S & 1][rr][m], x[tt & 1][m], acc[tt][rr]);
+            for (int tt = 0; tt < D - 1; ++tt) x[tt] = *reinterpret_cast<const i4v*>(cur + at + tt * 2048);
+#pragma unroll
+            for (int tt = 0; tt < TT; ++tt) {
+                if (tt + D - 1 < TT) x[(tt + D - 1) % D] = *reinterpret_cast<const i4v*>(cur + at + (tt + D - 1) * 2048);
+#pragma unroll
+                for (int rr = 0; rr < RR; ++rr) acc[tt][rr] = mfma_i8(w[(2 * S + m) & 3][rr], x[tt % D], acc[tt][rr]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            __builtin_amdgcn_sched_barrier(0);
         }
     };
     // whole turns of the ring; steps past the range only keep time (a tail of its own made the
     // compiler move and spill accumulators)
-    for (int g = g_begin; g < g_end; g += 4) {
-        step(g, ic<0>{});
-        step(g + 1, ic<1>{});
-        step(g + 2, ic<2>{});
-        step(g + 3, ic<3>{});
+    for (int v = 0; v < n_g; v += 4) {
+        step(v, ic<0>{});
+        step(v + 1, ic<1>{});
+        step(v + 2, ic<2>{});
+        step(v + 3, ic<3>{});
     }
-    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): no copy may land in LDS after the workgroup ends
-
-    if (ks > 1) {
+    if constexpr (MODE == kW8Split) {
+        __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): no copy may land in LDS after the workgroup ends
         i4v* part = reinterpret_cast<i4v*>(args.ypart) + ((((size_t)mb * (args.n_tiles / ks) + nbl) * ks + kr) * NW + wave) * (TT * RR * 64);
 #pragma unroll
         for (int tt = 0; tt < TT; ++tt)
@@ -495,65 +542,92 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN <= 4 ? 2 : 1) void w8a8_tile_
             for (int rr = 0; rr < RR; ++rr) part[(tt * RR + rr) * 64 + lane] = acc[tt][rr];
         return;
     }
+    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): no copy may land in LDS after this
+    __builtin_amdgcn_s_barrier();
+    // The correction: R's columns 64 j .. + 63 (128 bytes a token, as a group of codes) go to stage j (r <= 256),
+    // A's operands to registers, while the sums are scaled.  Rows of A past the module and tokens past T
+    // repeat the last one (their results are not stored); columns of A past r are taken as zero, R's are
+    // zero up to r_pad, here a multiple of 64.
+    const int r = args.r, rp = args.r_pad;
+    auto rcopy = [&](int j, uint8_t* stg) {
+        if (64 * j >= rp) return;
+        const uint8_t* base = reinterpret_cast<const uint8_t*>(args.R) + 128 * j;
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            const uint32_t t = (uint32_t)min(m0 + 8 * (NC * wave + i) + (lane >> 3), T - 1);
+            __builtin_amdgcn_global_load_lds((const void*)(base + (t * (uint32_t)rp * 2u + (piece ^ (16 * (i & 1))))),
+                                             (lds_void*)(stg + 8 * (NC * wave + i) * 128), 16, 0, 0);
+        }
+    };
+    const uint8_t* Ab = reinterpret_cast<const uint8_t*>(M.a) + (size_t)rts[0] * 32 * r;
+    auto aload = [&](int j, int m) {  // into slot m
+        const uint32_t c = (uint32_t)min(64 * j + 32 * m + 8 * (lane >> 4), r - 8);
+#pragma unroll
+        for (int rr = 0; rr < RR; ++rr) {
+            const uint32_t row = (uint32_t)min((rt0 + rr) * 16 + (lane & 15), M.n_out - 1) - rts[0] * 16;
+            w[m][rr] = *reinterpret_cast<const i4v*>(Ab + (row * (uint32_t)r + c) * 2u);
+        }
+    };
+    if constexpr (MODE == kW8Correct) {
+        rcopy(0, st0);
+        rcopy(1, st1);
+        rcopy(2, st2);
+        rcopy(3, st3);
+        aload(0, 0);
+        aload(0, 1);
+    }
+    __builtin_amdgcn_sched_barrier(0);
     // The scaled sums take the integer sums' registers (as bits): the tile is all a wavefront can hold.
     // The empty asm keeps each product where it is written (it was sunk into the branches below, with
-    // both forms of the tile live), and gives each part its own addresses instead of kept ones.
+    // both forms of the tile live).
     {
-        const int tok0 = m0 + 16 * TT * wm + (lane & 15);
         f4 sw[RR];
-        float st[TT];
 #pragma unroll
         for (int rr = 0; rr < RR; ++rr)
-            sw[rr] = *reinterpret_cast<const f4*>(M.sz + (size_t)min(rt0 + rr, NT - 1) * 64 + 16 * (lane >> 4));
-#pragma unroll
-        for (int tt = 0; tt < TT; ++tt) st[tt] = args.xscale[min(tok0 + 16 * tt, T - 1)];
+            sw[rr] = *reinterpret_cast<const f4*>(row_scale + wave * 64 + 16 * rr + 4 * (lane >> 4));
 #pragma unroll
         for (int tt = 0; tt < TT; ++tt) {
+            float st = tok_scale[16 * (TT * wm + tt) + (lane & 15)];
+            asm volatile("" : "+v"(st));
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int rr = 0; rr < RR; ++rr) {
                 f4 v;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] = (float)acc[tt][rr][i] * sw[rr][i] * st[tt];
+                for (int i = 0; i < 4; ++i) v[i] = (float)acc[tt][rr][i] * sw[rr][i] * st;
                 asm volatile("" : "+v"(v));
                 acc[tt][rr] = __builtin_bit_cast(i4v, v);
             }
+            __builtin_amdgcn_sched_barrier(0);
         }
     }
-    __builtin_amdgcn_sched_barrier(0);
-    if (args.r > 0 && M.a != nullptr) {
-        // rows past the module and tokens past T repeat the last one; their results are not stored.
-        // Columns r .. r_pad - 1 of R are zero, and so must A's be
-        int l = lane;
-        asm volatile("" : "+v"(l));
-        const int r = args.r, rp = args.r_pad, kofs = 8 * (l >> 4), row0 = min(rt0, NT - 1) * 16;
-        const uint8_t* Rb = reinterpret_cast<const uint8_t*>(args.R);
-        const uint8_t* Ab = reinterpret_cast<const uint8_t*>(M.a + (size_t)row0 * r);
-        const h8 zero8 = {0, 0, 0, 0, 0, 0, 0, 0};
-        uint32_t roff[TT], aoff[RR];
-#pragma unroll
-        for (int tt = 0; tt < TT; ++tt)
-            roff[tt] = (uint32_t)(min(m0 + 16 * TT * wm + 16 * tt + (l & 15), T - 1) * rp) * 2u;
-#pragma unroll
-        for (int rr = 0; rr < RR; ++rr) aoff[rr] = (uint32_t)((min((rt0 + rr) * 16 + (l & 15), M.n_out - 1) - row0) * r) * 2u;
+    if constexpr (MODE == kW8Correct) {
+        __builtin_amdgcn_s_waitcnt(0x0F70);
+        __builtin_amdgcn_s_barrier();
+        int j = 0;
 #pragma unroll 1
-        for (int kb = 0; kb < rp / 32; ++kb) {
-            const int c = 32 * kb + kofs;
-            h8 av[RR], bv[TT];
-#pragma unroll
-            for (int rr = 0; rr < RR; ++rr) {
-                const h8 v = load_h8(Ab + (aoff[rr] + 2u * (uint32_t)min(c, r - 8)));
-                av[rr] = c < r ? v : zero8;
+        do {
+            const uint8_t* cur = j == 0 ? st0 : (j == 1 ? st1 : (j == 2 ? st2 : st3));
+            if (j > 0) {
+                aload(j, 0);
+                aload(j, 1);
             }
 #pragma unroll
-            for (int tt = 0; tt < TT; ++tt) bv[tt] = load_h8(Rb + (roff[tt] + 2u * (uint32_t)c));
-            __builtin_amdgcn_sched_barrier(0);
+            for (int m = 0; m < 2; ++m) {
+                const bool in = 64 * j + 32 * m + 8 * (lane >> 4) < r;
+                h8 av[RR];
 #pragma unroll
-            for (int tt = 0; tt < TT; ++tt)
+                for (int rr = 0; rr < RR; ++rr) av[rr] = __builtin_bit_cast(h8, in ? w[m][rr] : i4v{0, 0, 0, 0});
 #pragma unroll
-                for (int rr = 0; rr < RR; ++rr)
-                    acc[tt][rr] = __builtin_bit_cast(i4v, mfma16(av[rr], bv[tt], __builtin_bit_cast(f4, acc[tt][rr])));
-        }
+                for (int tt = 0; tt < TT; ++tt) {
+                    const h8 xv = *reinterpret_cast<const h8*>(cur + (m == 0 ? rofs0 : rofs1) + tt * 2048);
+#pragma unroll
+                    for (int rr = 0; rr < RR; ++rr)
+                        acc[tt][rr] = __builtin_bit_cast(i4v, mfma16(av[rr], xv, __builtin_bit_cast(f4, acc[tt][rr])));
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            }
+        } while (64 * ++j < rp);
     }
     // To memory through the wavefront's own part of the (finished) ring: [16 TT tokens][64 rows] fp16,
     // a token's eight 16-byte pieces p at p ^ (token % 8), then whole 128-byte lines.
@@ -706,7 +780,10 @@ static hipError_t launch_tile(const ForwardArgs& a, hipStream_t stream) {
     // every XCD takes ceil(columns / 8) columns of every token block; those it has not return at once
     const int64_t grid = 8 * ceil_div(a.n_tiles, 8) * a.m_tiles;
     if (grid * 64 * WM * WN > (int64_t)UINT32_MAX) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL((w8a8_tile_kernel<WM, WN, TT>), dim3((unsigned)grid), dim3(64 * WM * WN), 0, stream, a);
+    const dim3 g((unsigned)grid), block(64 * WM * WN);
+    if (a.tile_ks > 1) hipLaunchKernelGGL((w8a8_tile_kernel<WM, WN, TT, kW8Split>), g, block, 0, stream, a);
+    else if (a.r > 0) hipLaunchKernelGGL((w8a8_tile_kernel<WM, WN, TT, kW8Correct>), g, block, 0, stream, a);
+    else hipLaunchKernelGGL((w8a8_tile_kernel<WM, WN, TT, kW8Plain>), g, block, 0, stream, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.tile_ks == 1) return e;
     const int pieces = a.m_tiles * (a.n_tiles / a.tile_ks) * WM * WN * TT;
