@@ -534,18 +534,25 @@ W8Shape choose_w8a8_shape(const Call& c) {
         for (int i = 0; i < c.m; ++i) n += ceil_div(ceil_div(c.w[i].n_out, 16), rr);
         return n * ceil_div(c.T, 16 * tt);
     };
+    // 128 x 256 tiles for more than one a CU (measured at d = 4096, r = 64: QKV 4096 + 2 x 1024 at T = 2048, 384 of
+    // them, 73 us, 79 with 128 x 128; gate/up 2 x 11008 at T = 300, 258 of them, 65 and 70; down 4096 <- 11008
+    // at T = 2048, 256 of them, 142 and 134)
     s.tt = 8;
     s.rr = 16;
-    if (tiles(8, 16) >= 512) return s;
+    if (tiles(8, 16) > 256) return s;
+    // Fewer: 128 x 128 tiles, K split until every CU has one, with ranges of at least 8 groups (4096 <- 4096 at
+    // T = 200, 64 tiles: 31 us in four ranges, 35 in two); two a CU only with ranges of 24 (4096 <- 14336 at
+    // T = 512, 128 tiles: 66 us in four ranges, 71 in two, 97 in one; 4096 <- 4096: 40, 37 and 39;
+    // 2 x 11008 <- 4096 at T = 128, 172 tiles: 46 in two, 39 in one)
     s.rr = 8;
     const int64_t n = tiles(8, 8), G = c.d / kGroup;
-    if (n < 256) {
-        int64_t ks = std::min<int64_t>(ceil_div(256, n), std::max<int64_t>(1, G / 8));
-        while (ks > 1 && (size_t)(n * ks) * 65536u > kW8PartBytes) --ks;
-        s.gk = (int)ceil_div(G, ks);
-        s.ks = (int)ceil_div(G, s.gk);
-        if (s.ks > 1) s.part = (size_t)(n * s.ks) * 65536u;
-    }
+    int64_t ks = std::min<int64_t>(256 / n, G / 8);
+    if (G / 24 >= 512 / n) ks = std::max<int64_t>(ks, 512 / n);
+    ks = std::max<int64_t>(ks, 1);
+    while (ks > 1 && (size_t)(n * ks) * 65536u > kW8PartBytes) --ks;
+    s.gk = (int)ceil_div(G, ks);
+    s.ks = (int)ceil_div(G, s.gk);
+    if (s.ks > 1) s.part = (size_t)(n * s.ks) * 65536u;
     return s;
 }
 
