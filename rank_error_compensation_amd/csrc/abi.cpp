@@ -519,6 +519,8 @@ int run_w4a8(const Call& c, void* workspace, hipStream_t stream) {
 // K ranges' int32 tiles of a call of more than 64 tokens: bounded by the workspace that
 // glowq_w8a8_workspace_bytes reserves for them.
 constexpr size_t kW8PartBytes = (size_t)32 << 20;
+constexpr int64_t kW8TinyT = 32;   // the small form alone up to here
+constexpr int64_t kW8SmallT = 64;  // and, by the number of tiles, up to here
 // row stride of the projection: whole 64-column blocks, as the large tiles take them
 inline int64_t w8_r_pad(int32_t r) { return ceil_div(r, 64) * 64; }
 inline size_t w8_r_bytes(int64_t T, int32_t r) { return round256((size_t)T * (size_t)w8_r_pad(r) * 2u); }
@@ -528,12 +530,18 @@ inline size_t w8_part_bytes(int64_t T, int32_t r, int ks) {
 
 W8Shape choose_w8a8_shape(const Call& c) {
     W8Shape s = {c.T <= 16 ? 1 : (c.T <= 32 ? 2 : 4), c.T <= 16 ? 1 : 2, 1, (int)(c.d / kGroup), 0};
-    if (c.T <= kW8SmallT) return s;
     auto tiles = [&](int tt, int rr) {
         int64_t n = 0;
         for (int i = 0; i < c.m; ++i) n += ceil_div(ceil_div(c.w[i].n_out, 16), rr);
         return n * ceil_div(c.T, 16 * tt);
     };
+    // Up to 64 tokens the small form, but past 32 tokens 64 x 128 tiles where they are many: the small form reads
+    // the codes anew for every 32 rows (2 x 11008 <- 4096 at T = 64, 172 tiles: 33 us, the small form 45; at
+    // T = 40: 32 and 36; Q/K/V 4096 + 2 x 1024, 48 tiles: 31 and 21)
+    if (c.T <= kW8SmallT) {
+        if (c.T > kW8TinyT && tiles(4, 8) >= 128) s.tt = 4, s.rr = 8;
+        return s;
+    }
     // 128 x 256 tiles for more than one a CU (measured at d = 4096, r = 64: QKV 4096 + 2 x 1024 at T = 2048, 384 of
     // them, 73 us, 79 with 128 x 128; gate/up 2 x 11008 at T = 300, 258 of them, 65 and 70; down 4096 <- 11008
     // at T = 2048, 256 of them, 142 and 134)
@@ -566,7 +574,9 @@ int run_w8a8(const Call& c, void* workspace, hipStream_t stream) {
     float* xscale = reinterpret_cast<float*>(base);
     base += round256((size_t)c.T * 4u);
     const int32_t r = c.correct ? c.r : 0, rp = c.correct ? (int32_t)w8_r_pad(r) : 0;
-    const PrepPlan pp = w8a8_prep_plan(c.T, c.d, r);
+    const W8Shape s = choose_w8a8_shape(c);
+    const bool small = s.rr <= 2;
+    const PrepPlan pp = w8a8_prep_plan(c.T, c.d, r, small);
     PrepArgs pa;
     std::memset(&pa, 0, sizeof(pa));
     pa.x = static_cast<const _Float16*>(c.x);
@@ -580,7 +590,7 @@ int run_w8a8(const Call& c, void* workspace, hipStream_t stream) {
     pa.xq = xq;
     pa.xscale = xscale;
     if (c.correct) {
-        if (c.T <= kW8SmallT || pp.ks > 1) {
+        if (small || pp.ks > 1) {
             pa.part = reinterpret_cast<float*>(base);
             base += w8_part_bytes(c.T, r, pp.ks);
         }
@@ -596,12 +606,11 @@ int run_w8a8(const Call& c, void* workspace, hipStream_t stream) {
     f.r = r;
     f.r_pad = rp;
     f.n_mod = c.m;
-    f.R = c.T <= kW8SmallT ? static_cast<void*>(pa.part) : static_cast<void*>(pa.R);
+    f.R = small ? static_cast<void*>(pa.part) : static_cast<void*>(pa.R);
     f.n_proj = pp.ks;  // fp32 K ranges of R (small calls)
     f.xq = xq;
     f.xscale = xscale;
     f.fmt = kFmtInt8;
-    const W8Shape s = choose_w8a8_shape(c);
     f.tile_tt = s.tt;
     f.tile_rr = s.rr;
     f.tile_ks = s.ks;
@@ -979,7 +988,11 @@ int glowq_repack_w8(const void* codes_dev, const float* scales_dev, int64_t n_ou
 size_t glowq_w8a8_workspace_bytes(int64_t T, int64_t d, int32_t r) {
     if (T <= 0 || T > kMaxT || d < kGroup || d % kGroup != 0 || d > kW8MaxD || r < 0 || r > GLOWQ_MAX_RANK) return 0;
     size_t n = round256((size_t)T * d) + round256((size_t)T * 4u);
-    if (r > 0) n += w8_part_bytes(T, r, w8a8_prep_plan(T, d, r).ks) + w8_r_bytes(T, r);
+    if (r > 0) {
+        const size_t small = T <= kW8SmallT ? w8_part_bytes(T, r, w8a8_prep_plan(T, d, r, true).ks) : 0;
+        const size_t tile = T > kW8TinyT ? w8_part_bytes(T, r, w8a8_prep_plan(T, d, r, false).ks) : 0;
+        n += std::max(small, tile) + w8_r_bytes(T, r);
+    }
     if (T > kW8SmallT) n += kW8PartBytes;
     return n;
 }

@@ -8,8 +8,8 @@ namespace glowq {
 constexpr int kFmtInt8 = 4;        // GLOWQ_FMT_INT8_CHANNEL
 constexpr int kW8Block = 2048;     // bytes of one 16-row x 128-input weight block
 constexpr int kW8Waves = 8;        // wavefronts that split the input groups of a small tile
-// Large tiles, as ForwardArgs::tile_rr row tiles per workgroup: 16 is 256 tokens x 256 rows on eight
-// wavefronts, 8 is 128 x 128 on four.
+// Tiles by ForwardArgs::tile_tt x tile_rr (16-token and 16-row tiles per workgroup): 8 x 16 and 8 x 8 on four
+// wavefronts, 4 x 8 on two; rr = 1, 2 is the small form, whose wavefronts split the input groups.
 constexpr int64_t kW8MaxD = 16384; // a token's row in the quantiser's registers; int32 sums exact
 
 // Launch shape of a call.
@@ -21,15 +21,14 @@ struct W8Shape {
 
 hipError_t launch_repack_w8(const int8_t* codes, const float* scales, int64_t n_out, int64_t k_in, uint8_t* q, float* sz,
                             int32_t* flag, hipStream_t stream);
-// Token codes and scales and, for r > 0, the projection, one launch.  Up to kW8SmallT tokens the K
-// ranges' fp32 sums [ks][T][rp] stay in `part` for the product to add; above, they are joined into the
+// Token codes and scales and, for r > 0, the projection, one launch.  For the small form the K ranges'
+// fp32 sums [ks][T][rp] stay in `part` for the product to add; for the tiles they are joined into the
 // fp16 R [T][rp] by a second launch (written directly with one range).
-constexpr int64_t kW8SmallT = 64;
 struct PrepPlan {
     int tt, nj;     // 16-token tiles and 16-column tiles of R per workgroup
     int range, ks;  // inputs per K range, ranges
 };
-PrepPlan w8a8_prep_plan(int64_t T, int64_t d, int32_t r);
+PrepPlan w8a8_prep_plan(int64_t T, int64_t d, int32_t r, bool small);
 struct PrepArgs {
     const _Float16* x;  // [T][d]
     const _Float16* b;  // [r][d]

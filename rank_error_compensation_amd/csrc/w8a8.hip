@@ -748,10 +748,10 @@ static void launch_prep_t(const PrepArgs& a, hipStream_t stream) {
     else launch_prep_n<TT, NJ, 256>(a, stream);
 }
 
-PrepPlan w8a8_prep_plan(int64_t T, int64_t d, int32_t r) {
-    PrepPlan p = {1, T <= kW8SmallT ? 1 : 4, (int)d, 1};
+PrepPlan w8a8_prep_plan(int64_t T, int64_t d, int32_t r, bool small) {
+    PrepPlan p = {1, small ? 1 : 4, (int)d, 1};
     if (r == 0) return p;
-    if (T <= kW8SmallT) {  // one batch of loads per wavefront
+    if (small) {  // one batch of loads per wavefront
         p.range = 32 * 8 * kPrepWaves;
     } else {
         p.tt = T >= 1024 ? 2 : 1;
@@ -793,7 +793,7 @@ static hipError_t launch_tile(const ForwardArgs& a, hipStream_t stream) {
 
 hipError_t launch_w8a8(const ForwardArgs& a, hipStream_t stream) {
     if (a.tile_rr == 16) return launch_tile<1, 4, 8>(a, stream);
-    if (a.tile_rr == 8) return launch_tile<2, 2, 4>(a, stream);
+    if (a.tile_rr == 8) return a.tile_tt == 8 ? launch_tile<2, 2, 4>(a, stream) : launch_tile<1, 2, 4>(a, stream);
     const dim3 grid((unsigned)a.n_tiles), block(64 * kW8Waves);
     switch (a.tile_tt * 4 + a.tile_rr) {
         case 4 + 1: hipLaunchKernelGGL((w8a8_split_kernel<1, 1>), grid, block, 0, stream, a); break;

@@ -58,7 +58,8 @@ SHAPES = [(1, 128, [16], 0), (1, 256, [1], 8), (1, 4096, [520, 17, 130], 64), (2
           (16, 1024, [520, 17], 64), (17, 512, [96, 64, 40], 32), (31, 640, [33] * 8, 16), (33, 640, [100], 24),
           (48, 2176, [300], 128), (64, 1024, [1024, 512, 512], 64), (65, 256, [48, 32], 16), (130, 384, [300, 200], 40),
           (300, 512, [2048, 2048], 128), (8, 2048, [64], 256), (257, 896, [1030, 515], 64), (513, 128, [770], 256),
-          (700, 1280, [2050], 8), (96, 14336, [272], 64), (5, 16384, [48], 64)]
+          (700, 1280, [2050], 8), (96, 14336, [272], 64), (5, 16384, [48], 64), (33, 512, [16400, 1], 24),
+          (64, 384, [8200, 8190], 64), (41, 128, [17000], 0)]
 
 
 @pytest.mark.parametrize("T,d,rows,r", SHAPES)
