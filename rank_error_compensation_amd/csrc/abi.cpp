@@ -524,8 +524,12 @@ constexpr int64_t kW8SmallT = 64;  // and, by the number of tiles, up to here
 // row stride of the projection: whole 64-column blocks, as the large tiles take them
 inline int64_t w8_r_pad(int32_t r) { return ceil_div(r, 64) * 64; }
 inline size_t w8_r_bytes(int64_t T, int32_t r) { return round256((size_t)T * (size_t)w8_r_pad(r) * 2u); }
-inline size_t w8_part_bytes(int64_t T, int32_t r, int ks) {
-    return round256((size_t)ks * (size_t)T * (size_t)w8_r_pad(r) * 4u);
+// fp32 K ranges of the projection.  Up to kW8TinyT tokens ranges of 2048 inputs, at most 8; above, at most
+// 512 / blocks ranges of (16 or 32)-token blocks, so ranges times tokens stay within max(T, 16384).  The
+// bound, not the plan's own number, is reserved: a workspace for T tokens serves fewer, too.
+inline size_t w8_part_bytes(int64_t T, int32_t r) {
+    const int64_t rows = T <= kW8TinyT ? 8 * T : std::max<int64_t>(T, 16384);
+    return round256((size_t)rows * (size_t)w8_r_pad(r) * 4u);
 }
 
 W8Shape choose_w8a8_shape(const Call& c) {
@@ -592,7 +596,8 @@ int run_w8a8(const Call& c, void* workspace, hipStream_t stream) {
     if (c.correct) {
         if (small || pp.ks > 1) {
             pa.part = reinterpret_cast<float*>(base);
-            base += w8_part_bytes(c.T, r, pp.ks);
+            if ((size_t)pp.ks * (size_t)c.T * (size_t)rp * 4u > w8_part_bytes(c.T, r)) return GLOWQ_ERR_WORKSPACE;
+            base += w8_part_bytes(c.T, r);
         }
         pa.R = reinterpret_cast<_Float16*>(base);
         base += w8_r_bytes(c.T, r);
@@ -988,11 +993,7 @@ int glowq_repack_w8(const void* codes_dev, const float* scales_dev, int64_t n_ou
 size_t glowq_w8a8_workspace_bytes(int64_t T, int64_t d, int32_t r) {
     if (T <= 0 || T > kMaxT || d < kGroup || d % kGroup != 0 || d > kW8MaxD || r < 0 || r > GLOWQ_MAX_RANK) return 0;
     size_t n = round256((size_t)T * d) + round256((size_t)T * 4u);
-    if (r > 0) {
-        const size_t small = T <= kW8SmallT ? w8_part_bytes(T, r, w8a8_prep_plan(T, d, r, true).ks) : 0;
-        const size_t tile = T > kW8TinyT ? w8_part_bytes(T, r, w8a8_prep_plan(T, d, r, false).ks) : 0;
-        n += std::max(small, tile) + w8_r_bytes(T, r);
-    }
+    if (r > 0) n += w8_part_bytes(T, r) + w8_r_bytes(T, r);
     if (T > kW8SmallT) n += kW8PartBytes;
     return n;
 }

@@ -32,6 +32,14 @@ def test_w8a8_workspace_bytes():
     for T, d, r in ((0, 256, 0), (-1, 256, 0), (3, 100, 0), (3, 16384 + 128, 0), (3, 256, -8), (3, 256, 264),
                     ((1 << 20) + 1, 128, 0)):
         assert f(T, d, r) == 0
+    # a workspace for the largest call serves every smaller one
+    Ts = [1, 2, 16, 31, 32, 33, 63, 64, 65, 100, 511, 512, 513, 1023, 1024, 1025, 2047, 2048, 2049, 3000, 8191, 8193, 65536]
+    for d in (128, 2048, 4096, 11008, 16384):
+        for r in (0, 8, 64, 72, 256):
+            n = [f(T, d, r) for T in Ts]
+            assert n == sorted(n), (d, r)
+            assert r == 256 or all(f(T, d, r) <= f(T, d, r + 8) for T in Ts)
+            assert d == 16384 or all(f(T, d, r) <= f(T, d + 128, r) for T in Ts)
 
 
 def w8(fmt=4, n_out=32, k_in=256, q=FAKE, sz=FAKE, reserved=0):
