@@ -602,7 +602,7 @@ int run_w8a8(const Call& c, void* workspace, hipStream_t stream) {
         pa.R = reinterpret_cast<_Float16*>(base);
         base += w8_r_bytes(c.T, r);
     }
-    if (launch_w8a8_prep(pa, pp, stream) != hipSuccess) return GLOWQ_ERR_HIP;
+    if (launch_w8a8_prep(pa, pp, s.ks == 1, stream) != hipSuccess) return GLOWQ_ERR_HIP;
     ForwardArgs f;
     std::memset(&f, 0, sizeof(f));
     f.T = (int32_t)c.T;
@@ -637,7 +637,7 @@ int run_w8a8(const Call& c, void* workspace, hipStream_t stream) {
     f.m_tiles = (int32_t)ceil_div(c.T, 16 * s.tt);
     // small tiles: work tiles of the launch; large ones: columns (row blocks x K ranges)
     f.n_tiles = (int32_t)(s.rr >= 8 ? tiles * s.ks : tiles * f.m_tiles);
-    return launch_w8a8(f, stream) == hipSuccess ? GLOWQ_OK : GLOWQ_ERR_HIP;
+    return launch_w8a8(f, pa, stream) == hipSuccess ? GLOWQ_OK : GLOWQ_ERR_HIP;
 }
 
 // Arguments shared by the calls that move routed rows.

@@ -39,7 +39,8 @@ struct PrepArgs {
     float* part;   // [ks][T][rp], nullptr for one range rounded directly
     _Float16* R;
 };
-hipError_t launch_w8a8_prep(const PrepArgs& a, const PrepPlan& p, hipStream_t stream);
-hipError_t launch_w8a8(const ForwardArgs& a, hipStream_t stream);
+// join: add the projection's ranges here (false where launch_w8a8 does, in a call whose K is split)
+hipError_t launch_w8a8_prep(const PrepArgs& a, const PrepPlan& p, bool join, hipStream_t stream);
+hipError_t launch_w8a8(const ForwardArgs& a, const PrepArgs& p, hipStream_t stream);
 
 }  // namespace glowq

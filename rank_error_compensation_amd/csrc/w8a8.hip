@@ -232,9 +232,9 @@ __global__ __launch_bounds__(kPrepThreads) void prep_kernel(const PrepArgs a, in
                          a.part != nullptr ? a.part + (size_t)k * a.T * a.rp : nullptr, red);
 }
 
-// R = the K ranges' sums added in order, rounded once to fp16.
-__global__ __launch_bounds__(256) void prep_join_kernel(const PrepArgs a) {
-    const size_t n = (size_t)a.T * a.rp / 4, i = (size_t)blockIdx.x * 256 + threadIdx.x;
+// R = the K ranges' sums added in order, rounded once to fp16; four values from value 4 i.
+__device__ __forceinline__ void join_ranges(const PrepArgs& a, size_t i) {
+    const size_t n = (size_t)a.T * a.rp / 4;
     if (i >= n) return;
     const f4* p = reinterpret_cast<const f4*>(a.part) + i;
     f4 v = p[0];
@@ -242,6 +242,10 @@ __global__ __launch_bounds__(256) void prep_join_kernel(const PrepArgs a) {
     for (int k = 1; k < a.ks; ++k) v += p[(size_t)k * n];
     const h2 lo = {(_Float16)v[0], (_Float16)v[1]}, hi = {(_Float16)v[2], (_Float16)v[3]};
     reinterpret_cast<u2*>(a.R)[i] = u2{as_u32(lo), as_u32(hi)};
+}
+
+__global__ __launch_bounds__(256) void prep_join_kernel(const PrepArgs a) {
+    join_ranges(a, (size_t)blockIdx.x * 256 + threadIdx.x);
 }
 
 // --------------------------------------------------------------------- product
@@ -370,9 +374,9 @@ using ic = std::integral_constant<int, I>;
 // Column of the launch (row block of a module and K range) and token block of a workgroup: XCD x
 // (workgroups b with b % 8 == x) takes the columns x, x + 8, ..., eight token blocks at a time, so
 // that a column's weights stay in one L2 and its workgroups run together.
-__device__ __forceinline__ bool w8_place(const ForwardArgs& args, int& mb, int& col) {
+__device__ __forceinline__ bool w8_place(const ForwardArgs& args, int block, int& mb, int& col) {
     const int cols = args.n_tiles, MT = args.m_tiles;
-    const int xcd = blockIdx.x & 7, local = blockIdx.x >> 3;
+    const int xcd = block & 7, local = block >> 3;
     const int mine = (cols - xcd + 7) >> 3;  // columns of this XCD
     if (mine <= 0) return false;
     const int per = 8 * mine;
@@ -389,7 +393,8 @@ __device__ __forceinline__ bool w8_place(const ForwardArgs& args, int& mb, int& 
 enum : int { kW8Plain = 0, kW8Correct = 1, kW8Split = 2 };  // what follows the integer sums
 
 template <int WM, int WN, int TT, int MODE>
-__global__ __launch_bounds__(64 * WM * WN, 2) void w8a8_tile_kernel(const ForwardArgs args) {
+__global__ __launch_bounds__(64 * WM * WN, 2) void w8a8_tile_kernel(const ForwardArgs args, const PrepArgs prep,
+                                                                   int join_blocks) {
     constexpr int RR = 4, NW = WM * WN, BM = 16 * TT * WM, SB = BM * 128;
     constexpr int NC = BM / 8 / NW;  // 1 KB code copies per wavefront and group
     static_assert(NC * 8 * NW == BM && NC + 3 * RR < 63 && BM % 64 == 0, "copies");
@@ -399,8 +404,16 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void w8a8_tile_kernel(const Forwar
     __shared__ __attribute__((aligned(16))) uint8_t st3[SB];
     __shared__ __attribute__((aligned(16))) float row_scale[NW * 64];
     __shared__ __attribute__((aligned(16))) float tok_scale[BM];
+    // With a K split the projection is only used by the launch after this one: the first workgroups (a
+    // multiple of 8) join its ranges instead of a launch of their own
+    if constexpr (MODE == kW8Split) {
+        if ((int)blockIdx.x < join_blocks) {
+            join_ranges(prep, (size_t)blockIdx.x * (64 * NW) + threadIdx.x);
+            return;
+        }
+    }
     int mb, col;
-    if (!w8_place(args, mb, col)) return;
+    if (!w8_place(args, (int)blockIdx.x - join_blocks, mb, col)) return;
     const int ks = MODE == kW8Split ? args.tile_ks : 1, nbl = col / ks, kr = col - nbl * ks;
     const ModuleArgs M = args.mod[module_of(args, nbl)];
     const int lane = threadIdx.x & 63;
@@ -764,26 +777,28 @@ PrepPlan w8a8_prep_plan(int64_t T, int64_t d, int32_t r, bool small) {
     return p;
 }
 
-hipError_t launch_w8a8_prep(const PrepArgs& a, const PrepPlan& p, hipStream_t stream) {
+hipError_t launch_w8a8_prep(const PrepArgs& a, const PrepPlan& p, bool join, hipStream_t stream) {
     if (a.d % kGroup != 0 || a.d > kPrepMaxD) return hipErrorInvalidValue;
     if (p.nj == 1) launch_prep_t<1, 1>(a, stream);
     else if (p.tt == 1) launch_prep_t<1, 4>(a, stream);
     else launch_prep_t<2, 4>(a, stream);
     hipError_t e = hipGetLastError();
-    if (e != hipSuccess || a.r == 0 || p.nj == 1 || a.part == nullptr) return e;
+    if (e != hipSuccess || a.r == 0 || p.nj == 1 || a.part == nullptr || !join) return e;
     hipLaunchKernelGGL(prep_join_kernel, dim3((unsigned)ceil_div((int64_t)a.T * a.rp / 4, 256)), dim3(256), 0, stream, a);
     return hipGetLastError();
 }
 
 template <int WM, int WN, int TT>
-static hipError_t launch_tile(const ForwardArgs& a, hipStream_t stream) {
+static hipError_t launch_tile(const ForwardArgs& a, const PrepArgs& p, hipStream_t stream) {
     // every XCD takes ceil(columns / 8) columns of every token block; those it has not return at once
-    const int64_t grid = 8 * ceil_div(a.n_tiles, 8) * a.m_tiles;
+    const int64_t join = a.tile_ks > 1 && a.r > 0 && p.part != nullptr
+                             ? ceil_div(ceil_div((int64_t)p.T * p.rp / 4, 64 * WM * WN), 8) * 8 : 0;
+    const int64_t grid = join + 8 * ceil_div(a.n_tiles, 8) * a.m_tiles;
     if (grid * 64 * WM * WN > (int64_t)UINT32_MAX) return hipErrorInvalidConfiguration;
     const dim3 g((unsigned)grid), block(64 * WM * WN);
-    if (a.tile_ks > 1) hipLaunchKernelGGL((w8a8_tile_kernel<WM, WN, TT, kW8Split>), g, block, 0, stream, a);
-    else if (a.r > 0) hipLaunchKernelGGL((w8a8_tile_kernel<WM, WN, TT, kW8Correct>), g, block, 0, stream, a);
-    else hipLaunchKernelGGL((w8a8_tile_kernel<WM, WN, TT, kW8Plain>), g, block, 0, stream, a);
+    if (a.tile_ks > 1) hipLaunchKernelGGL((w8a8_tile_kernel<WM, WN, TT, kW8Split>), g, block, 0, stream, a, p, (int)join);
+    else if (a.r > 0) hipLaunchKernelGGL((w8a8_tile_kernel<WM, WN, TT, kW8Correct>), g, block, 0, stream, a, p, (int)join);
+    else hipLaunchKernelGGL((w8a8_tile_kernel<WM, WN, TT, kW8Plain>), g, block, 0, stream, a, p, (int)join);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.tile_ks == 1) return e;
     const int pieces = a.m_tiles * (a.n_tiles / a.tile_ks) * WM * WN * TT;
@@ -791,9 +806,9 @@ static hipError_t launch_tile(const ForwardArgs& a, hipStream_t stream) {
     return hipGetLastError();
 }
 
-hipError_t launch_w8a8(const ForwardArgs& a, hipStream_t stream) {
-    if (a.tile_rr == 16) return launch_tile<1, 4, 8>(a, stream);
-    if (a.tile_rr == 8) return a.tile_tt == 8 ? launch_tile<2, 2, 4>(a, stream) : launch_tile<1, 2, 4>(a, stream);
+hipError_t launch_w8a8(const ForwardArgs& a, const PrepArgs& p, hipStream_t stream) {
+    if (a.tile_rr == 16) return launch_tile<1, 4, 8>(a, p, stream);
+    if (a.tile_rr == 8) return a.tile_tt == 8 ? launch_tile<2, 2, 4>(a, p, stream) : launch_tile<1, 2, 4>(a, p, stream);
     const dim3 grid((unsigned)a.n_tiles), block(64 * kW8Waves);
     switch (a.tile_tt * 4 + a.tile_rr) {
         case 4 + 1: hipLaunchKernelGGL((w8a8_split_kernel<1, 1>), grid, block, 0, stream, a); break;
