@@ -3,7 +3,8 @@
 // and its gradients  dg = dh u s (1 + g (1 - s)),  du = dh g s,  over n values of any shape.
 // With e = exp(-|g|) and q = 1 / (1 + e):  s = q and 1 - s = e q for g >= 0, s = e q and 1 - s = q
 // below -- no overflow and no cancellation at either end.  fp32 arithmetic, one rounding.
-// Bound by memory: 3 values moved per output value, 5 for the gradients.
+// Bound by memory: 3 values moved per output value, 5 for the gradients.  Tensors above kStreamBytes go past
+// the caches (the fp32 gradients of 16383 x 1408 values, cold: 75 us, 85 through them).
 #include <algorithm>
 
 #include "glowq.h"
@@ -27,19 +28,24 @@ __device__ __forceinline__ void sigmoid_pair(float g, float& s, float& one_minus
     one_minus_s = g >= 0.f ? eq : q;
 }
 
-template <typename S>
+template <typename S, bool NT>
 __device__ __forceinline__ Gate<S> load_gate(const S* p, int64_t i, int64_t n) {
-    if (i + Gate<S>::N <= n) return __builtin_bit_cast(Gate<S>, *reinterpret_cast<const u4*>(p + i));
+    if (i + Gate<S>::N <= n) {
+        const u4* q = reinterpret_cast<const u4*>(p + i);
+        return __builtin_bit_cast(Gate<S>, NT ? __builtin_nontemporal_load(q) : *q);
+    }
     Gate<S> r;
 #pragma unroll
     for (int k = 0; k < Gate<S>::N; ++k) r.v[k] = i + k < n ? p[i + k] : (S)0.f;
     return r;
 }
 
-template <typename S>
+template <typename S, bool NT>
 __device__ __forceinline__ void store_gate(S* p, int64_t i, int64_t n, const Gate<S>& r) {
     if (i + Gate<S>::N <= n) {
-        *reinterpret_cast<u4*>(p + i) = __builtin_bit_cast(u4, r);
+        u4* q = reinterpret_cast<u4*>(p + i);
+        if constexpr (NT) __builtin_nontemporal_store(__builtin_bit_cast(u4, r), q);
+        else *q = __builtin_bit_cast(u4, r);
         return;
     }
 #pragma unroll
@@ -47,11 +53,11 @@ __device__ __forceinline__ void store_gate(S* p, int64_t i, int64_t n, const Gat
         if (i + k < n) p[i + k] = r.v[k];
 }
 
-template <typename S>
+template <typename S, bool NT>
 __global__ __launch_bounds__(kGateThreads) void swiglu_kernel(const S* gate, const S* up, int64_t n, S* h) {
     const int64_t i = ((int64_t)blockIdx.x * kGateThreads + threadIdx.x) * Gate<S>::N;
     if (i >= n) return;
-    const Gate<S> g = load_gate(gate, i, n), u = load_gate(up, i, n);
+    const Gate<S> g = load_gate<S, NT>(gate, i, n), u = load_gate<S, NT>(up, i, n);
     Gate<S> r;
 #pragma unroll
     for (int k = 0; k < Gate<S>::N; ++k) {
@@ -59,15 +65,15 @@ __global__ __launch_bounds__(kGateThreads) void swiglu_kernel(const S* gate, con
         sigmoid_pair((float)g.v[k], s, t);
         r.v[k] = (S)((float)g.v[k] * s * (float)u.v[k]);
     }
-    store_gate(h, i, n, r);
+    store_gate<S, NT>(h, i, n, r);
 }
 
-template <typename S>
+template <typename S, bool NT>
 __global__ __launch_bounds__(kGateThreads) void swiglu_backward_kernel(const S* dh, const S* gate, const S* up, int64_t n,
                                                                        S* dgate, S* dup) {
     const int64_t i = ((int64_t)blockIdx.x * kGateThreads + threadIdx.x) * Gate<S>::N;
     if (i >= n) return;
-    const Gate<S> d = load_gate(dh, i, n), g = load_gate(gate, i, n), u = load_gate(up, i, n);
+    const Gate<S> d = load_gate<S, NT>(dh, i, n), g = load_gate<S, NT>(gate, i, n), u = load_gate<S, NT>(up, i, n);
     Gate<S> rg, ru;
 #pragma unroll
     for (int k = 0; k < Gate<S>::N; ++k) {
@@ -77,8 +83,8 @@ __global__ __launch_bounds__(kGateThreads) void swiglu_backward_kernel(const S* 
         rg.v[k] = (S)(df * (float)u.v[k] * s * fmaf(gf, t, 1.f));
         ru.v[k] = (S)(df * gf * s);
     }
-    store_gate(dgate, i, n, rg);
-    store_gate(dup, i, n, ru);
+    store_gate<S, NT>(dgate, i, n, rg);
+    store_gate<S, NT>(dup, i, n, ru);
 }
 
 template <typename S>
@@ -88,27 +94,40 @@ unsigned gate_grid(int64_t n) {
 
 }  // namespace
 
-hipError_t launch_swiglu(const void* gate, const void* up, int64_t n, int32_t dtype, void* h, hipStream_t stream) {
-    if (dtype == GLOWQ_DTYPE_F16)
-        hipLaunchKernelGGL((swiglu_kernel<_Float16>), dim3(gate_grid<_Float16>(n)), dim3(kGateThreads), 0, stream,
-                           static_cast<const _Float16*>(gate), static_cast<const _Float16*>(up), n, static_cast<_Float16*>(h));
+template <typename S>
+static hipError_t launch_swiglu_t(const void* gate, const void* up, int64_t n, void* h, hipStream_t stream) {
+    const dim3 grid(gate_grid<S>(n)), block(kGateThreads);
+    const S *g = static_cast<const S*>(gate), *u = static_cast<const S*>(up);
+    if (n * (int64_t)sizeof(S) > kStreamBytes)
+        hipLaunchKernelGGL((swiglu_kernel<S, true>), grid, block, 0, stream, g, u, n, static_cast<S*>(h));
     else
-        hipLaunchKernelGGL((swiglu_kernel<float>), dim3(gate_grid<float>(n)), dim3(kGateThreads), 0, stream,
-                           static_cast<const float*>(gate), static_cast<const float*>(up), n, static_cast<float*>(h));
+        hipLaunchKernelGGL((swiglu_kernel<S, false>), grid, block, 0, stream, g, u, n, static_cast<S*>(h));
+    return hipGetLastError();
+}
+
+hipError_t launch_swiglu(const void* gate, const void* up, int64_t n, int32_t dtype, void* h, hipStream_t stream) {
+    return dtype == GLOWQ_DTYPE_F16 ? launch_swiglu_t<_Float16>(gate, up, n, h, stream)
+                                    : launch_swiglu_t<float>(gate, up, n, h, stream);
+}
+
+template <typename S>
+static hipError_t launch_swiglu_backward_t(const void* dh, const void* gate, const void* up, int64_t n, void* dgate,
+                                           void* dup, hipStream_t stream) {
+    const dim3 grid(gate_grid<S>(n)), block(kGateThreads);
+    const S *d = static_cast<const S*>(dh), *g = static_cast<const S*>(gate), *u = static_cast<const S*>(up);
+    if (n * (int64_t)sizeof(S) > kStreamBytes)
+        hipLaunchKernelGGL((swiglu_backward_kernel<S, true>), grid, block, 0, stream, d, g, u, n, static_cast<S*>(dgate),
+                           static_cast<S*>(dup));
+    else
+        hipLaunchKernelGGL((swiglu_backward_kernel<S, false>), grid, block, 0, stream, d, g, u, n, static_cast<S*>(dgate),
+                           static_cast<S*>(dup));
     return hipGetLastError();
 }
 
 hipError_t launch_swiglu_backward(const void* dh, const void* gate, const void* up, int64_t n, int32_t dtype,
                                   void* dgate, void* dup, hipStream_t stream) {
-    if (dtype == GLOWQ_DTYPE_F16)
-        hipLaunchKernelGGL((swiglu_backward_kernel<_Float16>), dim3(gate_grid<_Float16>(n)), dim3(kGateThreads), 0, stream,
-                           static_cast<const _Float16*>(dh), static_cast<const _Float16*>(gate),
-                           static_cast<const _Float16*>(up), n, static_cast<_Float16*>(dgate), static_cast<_Float16*>(dup));
-    else
-        hipLaunchKernelGGL((swiglu_backward_kernel<float>), dim3(gate_grid<float>(n)), dim3(kGateThreads), 0, stream,
-                           static_cast<const float*>(dh), static_cast<const float*>(gate), static_cast<const float*>(up), n,
-                           static_cast<float*>(dgate), static_cast<float*>(dup));
-    return hipGetLastError();
+    return dtype == GLOWQ_DTYPE_F16 ? launch_swiglu_backward_t<_Float16>(dh, gate, up, n, dgate, dup, stream)
+                                    : launch_swiglu_backward_t<float>(dh, gate, up, n, dgate, dup, stream);
 }
 
 }  // namespace glowq

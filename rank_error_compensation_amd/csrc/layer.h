@@ -5,6 +5,9 @@
 
 namespace glowq {
 
+// Above this many bytes a tensor does not stay in the L2 caches (8 x 4 MB) for its next reader.
+constexpr int64_t kStreamBytes = (int64_t)32 << 20;
+
 constexpr int kMoeMaxTopK = 64;  // choices per token: one lane of a wavefront each
 
 // Routing lists.  n pairs (T top_k), buckets 0 .. n_exp - 1 for the experts and n_exp for pairs

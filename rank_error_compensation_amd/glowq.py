@@ -542,7 +542,11 @@ def group_forward_w8a8(x: torch.Tensor, weights: Sequence[QWeight], b: Optional[
     per output row and per token, the correction on the fp16 activations."""
     what = "group_forward_w8a8"
     a = a or ()
-    _same_place(what, x, b, workspace, *a, *(y or ()), *[w.q for w in weights], *[w.sz for w in weights])
+    _same_place(what, x, b, workspace, *a, *(y or ()))
+    dev = x.get_device()
+    for w in weights:
+        if w.q.get_device() != dev or w.sz.get_device() != dev:
+            raise GlowQError(ERR_INVALID_ARG, f"{what}: weights on the device of x")
     ctx = _elsewhere(x, stream)
     if ctx is not None:
         with ctx:

@@ -23,7 +23,8 @@ def values(shape, kind, seed, scale=3.0):
 
 
 @pytest.mark.parametrize("kind", ["f16", "f32"])
-@pytest.mark.parametrize("shape", [(1,), (3,), (8,), (9,), (4, 1408), (127, 33), (2, 3, 5, 7), (1000, 1001)])
+@pytest.mark.parametrize("shape", [(1,), (3,), (8,), (9,), (4, 1408), (127, 33), (2, 3, 5, 7), (1000, 1001),
+                                   (5003, 4001)])
 def test_swiglu_and_gradients(shape, kind):
     g = glowq()
     log(f"swiglu {shape} {kind}")

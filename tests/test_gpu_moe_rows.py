@@ -117,6 +117,29 @@ def test_rows_and_gradients(T, k, E, d, drop, kind):
     assert g.workspace_status(ws) == g.OK
 
 
+@pytest.mark.parametrize("kind,d", [("f16", 4096), ("f16", 4095), ("f32", 2052), ("f32", 2051)])
+def test_rows_that_outgrow_the_caches(kind, d):
+    """More than 32 MB of rows (read past the caches): every row of sampled tokens."""
+    g = glowq()
+    T, k = 2500, 2
+    tok, pr, n = lists(T, k, 12, 33, 0.05)
+    assert n * d * (2 if kind == "f16" else 4) > 32 << 20
+    ws = workspace()
+    rows, dy = randn((n, d), kind, 1), randn((T, d), kind, 2)
+    w = torch.rand(T, k).cuda()
+    some = torch.arange(0, T, 83)
+    y = g.moe_combine(rows, pr, w, add=dy, workspace=ws)
+    dr, dw = g.moe_combine_backward(dy, rows, pr, tok, w, workspace=ws)
+    dx = g.moe_dispatch_backward(rows, pr, workspace=ws)
+    prs, ws_ = pr.cpu()[some].numpy(), w.cpu()[some].double().numpy()
+    R.within(y[some], *R.combine(rows, prs, ws_, dy[some], kind), "combine")
+    R.within(dx[some], *R.combine(rows, prs, None, None, kind), "dispatch gradient")
+    ref, bound, rw, bw, named = R.combine_backward(dy[some], rows, prs, ws_, n, kind)
+    R.within(dr[torch.from_numpy(named).cuda()], ref[named], bound[named], "d_rows")
+    R.within(dw[some], rw, bw, "d_weights")
+    assert g.workspace_status(ws) == g.OK
+
+
 def test_gradients_against_differences():
     """<dy, combine(rows + h v) - combine(rows - h v)> / 2h against <d_rows, v>, and the same for weights:
     the operator is linear in each, so in fp32 only rounding is left (values of order 1, h = 1)."""
