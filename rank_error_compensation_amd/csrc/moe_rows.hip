@@ -291,7 +291,9 @@ __device__ void zero_free_rows(const RowsArgs& a, int64_t first) {
 // ones).  Lane j < top_k holds choice j: its row counts when it lies in range,
 // row_token names this token and no earlier choice of the token has it -- so that a row is written
 // by one wavefront once, whatever the lists hold; anything else but -1 raises the error word.
-template <typename S, int N, bool NT>
+// NT: 1 for rows that outgrow the caches, 2 where dy is read once too (it is read again for every
+// kChoices choices).
+template <typename S, int N, int NT>
 __global__ __launch_bounds__(kRowsThreads) void combine_backward_kernel(const RowsArgs a, int chunks, int token_blocks) {
     if ((int)blockIdx.x >= token_blocks) {
         zero_free_rows<S>(a, (int64_t)((int)blockIdx.x - token_blocks) * kRowsThreads);
@@ -335,12 +337,10 @@ __global__ __launch_bounds__(kRowsThreads) void combine_backward_kernel(const Ro
         for (int c = lane; c < chunks; c += 64) {
             const size_t col = (size_t)c * N;
             float g[N], v[kChoices][N];
-            // dy is read again for every kChoices choices
-            if (NT && k <= kChoices) load_f32<S, N, true>(dy + col, g);
-            else load_f32<S, N, false>(dy + col, g);
+            load_f32<S, N, NT == 2>(dy + col, g);
 #pragma unroll
             for (int u = 0; u < kChoices; ++u)
-                if (ok[u]) load_f32<S, N, NT>(src[u] + col, v[u]);
+                if (ok[u]) load_f32<S, N, (NT > 0)>(src[u] + col, v[u]);
 #pragma unroll
             for (int u = 0; u < kChoices; ++u)
                 if (ok[u]) {
@@ -421,12 +421,12 @@ template <typename S, int N>
 static hipError_t launch_combine_backward_n(const RowsArgs& a, hipStream_t stream) {
     const int blocks = (int)ceil_div(a.T, kRowsThreads / 64);
     const unsigned grid = (unsigned)(blocks + ceil_div(a.n_rows, kRowsThreads));
-    if (stream_rows<S>(a))
-        hipLaunchKernelGGL((combine_backward_kernel<S, N, true>), dim3(grid), dim3(kRowsThreads), 0, stream, a,
-                           (int)(a.d / N), blocks);
-    else
-        hipLaunchKernelGGL((combine_backward_kernel<S, N, false>), dim3(grid), dim3(kRowsThreads), 0, stream, a,
-                           (int)(a.d / N), blocks);
+    const dim3 g(grid), block(kRowsThreads);
+    const int chunks = (int)(a.d / N);
+    if (!stream_rows<S>(a)) hipLaunchKernelGGL((combine_backward_kernel<S, N, 0>), g, block, 0, stream, a, chunks, blocks);
+    else if (a.top_k > kChoices)
+        hipLaunchKernelGGL((combine_backward_kernel<S, N, 1>), g, block, 0, stream, a, chunks, blocks);
+    else hipLaunchKernelGGL((combine_backward_kernel<S, N, 2>), g, block, 0, stream, a, chunks, blocks);
     return hipGetLastError();
 }
 
