@@ -134,6 +134,7 @@ def test_rows_that_outgrow_the_caches(kind, d, T, k):
     prs, ws_ = pr.cpu()[some].numpy(), w.cpu()[some].double().numpy()
     R.within(y[some], *R.combine(rows, prs, ws_, dy[some], kind), "combine")
     R.within(dx[some], *R.combine(rows, prs, None, None, kind), "dispatch gradient")
+    assert torch.equal(g.moe_dispatch(dy, tok, workspace=ws), dy[tok.long()])
     ref, bound, rw, bw, named = R.combine_backward(dy[some], rows, prs, ws_, n, kind)
     R.within(dr[torch.from_numpy(named).cuda()], ref[named], bound[named], "d_rows")
     R.within(dw[some], rw, bw, "d_weights")
