@@ -55,6 +55,17 @@ def test_far_gates(kind):
     assert torch.isnan(h[0]) and torch.isnan(h[1]) and torch.isinf(h[2]) and torch.isfinite(h[3])
 
 
+def test_large_factors_meet_a_small_slope():
+    """dh u = 1e50 lies outside fp32, dh u s (1 + g (1 - s)) at these gates inside: below 1e37."""
+    g = glowq()
+    gate = torch.tensor([-75.0, -60.0, -50.0, -40.0, -35.0]).cuda()
+    up, dh = torch.full_like(gate, 1e25), torch.full_like(gate, -1e25)
+    (dg, bg), (du, bu) = R.swiglu_backward(dh, gate, up, "f32")
+    a, c = g.swiglu_backward(dh, gate, up)
+    R.within(a, dg, bg, "d_gate")
+    R.within(c, du, bu, "d_up")
+
+
 def test_gradients_against_differences():
     """Central differences in fp64 of the reference formula at step 1e-4: error below its third derivative's
     share, h^2 / 6 times at most 2 |dh u| (|g| + 3), plus the fp32 bound."""
