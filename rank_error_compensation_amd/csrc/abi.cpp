@@ -533,7 +533,7 @@ inline size_t w8_part_bytes(int64_t T, int32_t r) {
 }
 
 W8Shape choose_w8a8_shape(const Call& c) {
-    W8Shape s = {c.T <= 16 ? 1 : (c.T <= 32 ? 2 : 4), c.T <= 16 ? 1 : 2, 1, (int)(c.d / kGroup), 0};
+    W8Shape s = {c.T <= 16 ? 1 : (c.T <= 32 ? 2 : 4), c.T <= 16 ? 1 : 2, 1, (int)(c.d / kGroup)};
     auto tiles = [&](int tt, int rr) {
         int64_t n = 0;
         for (int i = 0; i < c.m; ++i) n += ceil_div(ceil_div(c.w[i].n_out, 16), rr);
@@ -561,11 +561,9 @@ W8Shape choose_w8a8_shape(const Call& c) {
     int64_t ks = std::min<int64_t>(256 / n, G / 8);
     if (G / 24 >= 512 / n) ks = std::max<int64_t>(ks, 512 / n);
     ks = std::max<int64_t>(ks, 1);
-    while (ks > 1 && (size_t)(n * ks) * 65536u > kW8PartBytes) --ks;
     s.gk = (int)ceil_div(G, ks);
     s.ks = (int)ceil_div(G, s.gk);
-    if (s.ks > 1) s.part = (size_t)(n * s.ks) * 65536u;
-    return s;
+    return s;  // n ks <= 512 tiles of 64 KB wherever ks > 1
 }
 
 // W8A8 form.  Workspace: codes int8 [T][d] | scales fp32 [T] | fp16 projection [T][r_pad]
@@ -579,6 +577,11 @@ int run_w8a8(const Call& c, void* workspace, hipStream_t stream) {
     base += round256((size_t)c.T * 4u);
     const int32_t r = c.correct ? c.r : 0, rp = c.correct ? (int32_t)w8_r_pad(r) : 0;
     const W8Shape s = choose_w8a8_shape(c);
+    if (s.ks > 1) {
+        int64_t n = 0;
+        for (int i = 0; i < c.m; ++i) n += ceil_div(c.w[i].n_out, 128);
+        if ((size_t)(n * ceil_div(c.T, 128) * s.ks) * 65536u > kW8PartBytes) return GLOWQ_ERR_WORKSPACE;
+    }
     const bool small = s.rr <= 2;
     const PrepPlan pp = w8a8_prep_plan(c.T, c.d, r, small);
     PrepArgs pa;

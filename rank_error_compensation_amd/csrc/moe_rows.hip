@@ -53,7 +53,7 @@ __device__ int bucket_scan(int v, int* wsum) {
     return base + incl - v;
 }
 
-// Counts of one chunk per bucket.
+// Counts of one chunk per bucket.  Launch-bound: 65536 pairs on 256 workgroups 2.6 us.
 __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(const SortArgs a) {
     __shared__ int hist[kBuckets];
     const int nb = a.n_exp + 1;
@@ -70,6 +70,8 @@ __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(const SortArgs
 // that rows of one expert keep the pairs' order: counters[wave][bucket] first count the piece, then
 // hold the next free row (expert start + earlier chunks + earlier wavefronts); 64 pairs at a time
 // take theirs, a lane's place among the lanes of its bucket found from ballots of the bucket's bits.
+// Bound by latency, not by its 12 bytes a pair: in one workgroup a token's four choices take 2.7 us; 65536
+// pairs over 60 experts on 256 workgroups, each of which adds up all workgroups' counts, 6.9 us.
 template <bool ONE>
 __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(const SortArgs a) {
     __shared__ int cnt[kSortWaves * kHistStride];
@@ -165,6 +167,8 @@ inline int row_threads(int64_t chunks, int most) {
     return t;
 }
 
+// Bound by memory: 8188 rows of 4 KB out of 2047 take 8.4 us warm (33.5 MB written, 8.4 MB read: 5.0 TB/s).
+// Two rows a thread keep enough loads in flight (one or eight: no faster).
 // V: the piece of a row that one thread moves at a time (16 bytes where rows are multiples of it).
 // NT: rows written past the caches (32764 rows of 4 KB, cold: 38 us, 43 through them; 8188 rows: 10.6, 11.1).
 template <typename V, bool NT>
@@ -231,7 +235,10 @@ __device__ __forceinline__ void store_f32(S* p, const float (&f)[N]) {
 
 constexpr int kChoices = 4;  // choices whose rows are loaded together
 
-// y[t] for kRowsThreads / tpr tokens per workgroup, columns in N-value pieces.
+// y[t] for kRowsThreads / tpr tokens per workgroup, columns in N-value pieces.  A thread adds up all choices of
+// its columns in registers, the rows of kChoices of them in flight: every row is read once and y written once.
+// Bound by memory: 16384 tokens x 4 choices x 2048 fp16 (402 MB with the added rows) 68 us, 5.9 TB/s (rows
+// partly in the caches of the call before); as the gradient of a dispatch, 4096 tokens x 4 x 2048 fp32, 28 us.
 template <typename S, int N, bool NT>
 __global__ __launch_bounds__(kRowsThreads) void combine_kernel(const RowsArgs a, int chunks, int tpr) {
     const int per = kRowsThreads / tpr, sub = threadIdx.x / tpr;
@@ -297,6 +304,8 @@ __device__ void zero_free_rows(const RowsArgs& a, int64_t first) {
 // by one wavefront once, whatever the lists hold; anything else but -1 raises the error word.
 // NT: 1 for rows that outgrow the caches, 2 where dy is read once too (it is read again for every
 // kChoices choices).
+// A wavefront holds its token's dy piece while it goes over the choices: dy once, the rows once read and once
+// written.  Bound by memory: 8191 tokens x 4 x 2048 fp16 (302 MB) 56 to 58 us, 5.2 TB/s.
 template <typename S, int N, int NT>
 __global__ __launch_bounds__(kRowsThreads) void combine_backward_kernel(const RowsArgs a, int chunks, int token_blocks) {
     if ((int)blockIdx.x >= token_blocks) {

@@ -16,7 +16,6 @@ constexpr int64_t kW8MaxD = 16384; // a token's row in the quantiser's registers
 struct W8Shape {
     int tt, rr;      // 16-token tiles and 16-row tiles per workgroup
     int ks, gk;      // K ranges over workgroups, input groups per range
-    size_t part;     // bytes of the ranges' int32 tiles
 };
 
 hipError_t launch_repack_w8(const int8_t* codes, const float* scales, int64_t n_out, int64_t k_in, uint8_t* q, float* sz,

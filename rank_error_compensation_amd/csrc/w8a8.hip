@@ -68,7 +68,11 @@ __global__ __launch_bounds__(256) void repack_w8_scales_kernel(const float* __re
 
 // --------------------------------------------------------------------- token codes and projection
 // One launch, two kinds of workgroups (both read X, neither needs the other): first those of the
-// projection R = X B^T, then one per token for its scale and codes.
+// projection R = X B^T, then those of the scales and codes (512 / TPT tokens each, a token's row in
+// registers between its maximum and its codes, so that X is read once for them).
+// What bounds it: up to some 40 tokens the launch and one load's latency (d = 4096, r = 64: 4.9 us for one token,
+// 6.4 us for 37); then memory (T = 2048: 16.8 MB of X and 8.9 MB of codes, scales and sums, 14.8 us; X again by the
+// projection's workgroups, out of the caches).
 constexpr int kPrepThreads = 512;
 constexpr int kPrepWaves = kPrepThreads / 64;
 constexpr int kPrepChunks = 8;  // 8-input chunks per thread at most
@@ -232,7 +236,8 @@ __global__ __launch_bounds__(kPrepThreads) void prep_kernel(const PrepArgs a, in
                          a.part != nullptr ? a.part + (size_t)k * a.T * a.rp : nullptr, red);
 }
 
-// R = the K ranges' sums added in order, rounded once to fp16; four values from value 4 i.
+// R = the K ranges' sums added in order, rounded once to fp16; four values from value 4 i.  A few MB out of
+// the caches (T = 2048, r = 64, 8 ranges: 4.2 MB, 4.9 us): bound by its launch.
 __device__ __forceinline__ void join_ranges(const PrepArgs& a, size_t i) {
     const size_t n = (size_t)a.T * a.rp / 4;
     if (i >= n) return;
@@ -252,6 +257,10 @@ __global__ __launch_bounds__(256) void prep_join_kernel(const PrepArgs a) {
 // 16 TT tokens x 16 RR rows per workgroup; its NW wavefronts take the input groups in turn (group g
 // to wavefront g % NW), operands straight from memory, and add their exact int32 tiles through LDS.
 // Wavefront w then finishes tile w (w < TT RR): scales, correction steps, one rounding to fp16.
+// Few tokens: the weights are the traffic and each call a few microseconds, so K is split inside the workgroup
+// to have all its loads in flight at once; one row tile a workgroup up to 16 tokens, for workgroups enough.
+// Bound by the latency of that one round of loads: one token, 4096 + 2 x 1024 rows <- 4096 (25 MB), warm in the
+// caches 5.6 us, waits 0.84 of the wavefronts' time; 37 tokens, 2 x 1408 <- 2048 7.4 us.
 template <int TT, int RR>
 __global__ __launch_bounds__(64 * kW8Waves) void w8a8_split_kernel(const ForwardArgs args) {
     constexpr int NW = kW8Waves, NT = TT * RR;
@@ -359,14 +368,20 @@ __global__ __launch_bounds__(64 * kW8Waves) void w8a8_split_kernel(const Forward
 // --------------------------------------------------------------------- large tiles
 // 16 TT WM tokens x 64 WN rows per workgroup: WM x WN wavefronts, each 16 TT tokens x 4 row tiles.
 // The token codes of an input group (128 bytes a token) go HBM/L2 -> LDS by the load unit into a ring
-// of four stages; a wavefront's weight operands come straight into registers, one group ahead (the WM
-// wavefronts that share rows find them in the L1 cache), so that LDS carries only the codes: a code
+// of four stages; a wavefront's weight operands come straight into registers, up to three groups ahead (the
+// WM wavefronts that share rows find them in the L1 cache), so that LDS carries only the codes: a code
 // byte read feeds 4 matrix-core steps.  In a stage, row r keeps its 16-byte piece c at position
 // c ^ f(r), f(r) = (r % 8) ^ ((r / 8) % 2): the 16 rows of an operand read fall in distinct banks.
 // Tokens past T read token T - 1 and row tiles past the module its last tile; neither is stored.
 //
 // With args.tile_ks > 1 the input groups are split over workgroups: each writes its exact int32
 // tile to the workspace, and w8a8_join_kernel adds them and finishes.
+//
+// Measured (r = 64): 128 x 256, T = 2048, 2 x 11008 rows <- 4096: 185 to 191 us, 2.0 Pop/s of int8 (a plain int8
+// product of 8192^3 by the vendor's library: 2.07).  Matrix cores busy 0.47 of the time, operand returns from the
+// L1/LDS path 0.70 (2.4 GB from the L2 caches, 13 TB/s; 0.39 GB from behind them): bound by feeding operands.  256 x 256
+// on 4 or 8 wavefronts and 128 x 512 on 8 (half the weight traffic, one workgroup a CU) took 200 to 212 us.
+// 128 x 128 in four K ranges, T = 512, 4096 rows <- 14336: 40 us, 1.5 Pop/s, matrix cores busy 0.28.
 typedef __attribute__((address_space(3))) void lds_void;
 template <int I>
 using ic = std::integral_constant<int, I>;
@@ -677,18 +692,20 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void w8a8_tile_kernel(const Forwar
 }
 
 // Sums of the K ranges of one 16-token x 64-row piece per wavefront (pieces numbered as the tile
-// kernel stores them), scales, correction, one rounding to fp16.
-__global__ __launch_bounds__(256) void w8a8_join_kernel(const ForwardArgs args, int wm_n, int wn_n, int tt_n, int pieces) {
-    constexpr int RR = 4;
+// kernel stores them), scales, correction, one rounding to fp16.  Memory-bound: T = 512, 4096 rows, four
+// ranges: 33.5 MB of sums (from the caches) in 11 us, 3.4 TB/s with the 4.2 MB of y.
+template <int WM, int WN, int TT>
+__global__ __launch_bounds__(256) void w8a8_join_kernel(const ForwardArgs args, int pieces) {
+    constexpr int RR = 4, NW = WM * WN;
     const int lane = threadIdx.x & 63;
     const int piece = (int)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     if (piece >= pieces) return;
-    const int nw = wm_n * wn_n, ks = args.tile_ks, cols = args.n_tiles / ks;
-    const int tt = piece % tt_n, wave = piece / tt_n % nw, tile = piece / tt_n / nw;
+    const int ks = args.tile_ks, cols = args.n_tiles / ks;
+    const int tt = piece % TT, wave = piece / TT % NW, tile = piece / TT / NW;
     const int mb = tile / cols, nbl = tile - mb * cols;
     const ModuleArgs M = args.mod[module_of(args, nbl)];
-    const int rt0 = (nbl - M.tile_begin) * RR * wn_n + (wave / wm_n) * RR;
-    const int t = (mb * wm_n + wave % wm_n) * 16 * tt_n + 16 * tt + (lane & 15);
+    const int rt0 = (nbl - M.tile_begin) * RR * WN + (wave / WM) * RR;
+    const int t = (mb * WM + wave % WM) * 16 * TT + 16 * tt + (lane & 15);
     if (rt0 >= M.n_tiles16) return;
     const bool ok = t < args.T;
     const i4v* part = reinterpret_cast<const i4v*>(args.ypart);
@@ -696,7 +713,7 @@ __global__ __launch_bounds__(256) void w8a8_join_kernel(const ForwardArgs args, 
 #pragma unroll
     for (int rr = 0; rr < RR; ++rr) sum[rr] = i4v{0, 0, 0, 0};
     for (int k = 0; k < ks; ++k) {
-        const i4v* p = part + ((((size_t)tile * ks + k) * nw + wave) * tt_n + tt) * (RR * 64) + lane;
+        const i4v* p = part + ((((size_t)tile * ks + k) * NW + wave) * TT + tt) * (RR * 64) + lane;
 #pragma unroll
         for (int rr = 0; rr < RR; ++rr) sum[rr] += p[rr * 64];
     }
@@ -754,11 +771,16 @@ static void launch_prep_n(const PrepArgs& a, hipStream_t stream) {
 // Few tokens: a workgroup for each.  Many: as few threads per token as hold its row (64 values each).
 template <int TT, int NJ>
 static void launch_prep_t(const PrepArgs& a, hipStream_t stream) {
-    if constexpr (NJ == 1) launch_prep_n<TT, NJ, kPrepThreads>(a, stream);
-    else if (a.T <= 256) launch_prep_n<TT, NJ, kPrepThreads>(a, stream);
-    else if (a.d <= 64 * 64) launch_prep_n<TT, NJ, 64>(a, stream);
-    else if (a.d <= 128 * 64) launch_prep_n<TT, NJ, 128>(a, stream);
-    else launch_prep_n<TT, NJ, 256>(a, stream);
+    if constexpr (NJ == 1) {
+        launch_prep_n<TT, NJ, kPrepThreads>(a, stream);
+    } else {
+        if constexpr (TT == 1) {
+            if (a.T <= 256) return launch_prep_n<TT, NJ, kPrepThreads>(a, stream);
+        }
+        if (a.d <= 64 * 64) launch_prep_n<TT, NJ, 64>(a, stream);
+        else if (a.d <= 128 * 64) launch_prep_n<TT, NJ, 128>(a, stream);
+        else launch_prep_n<TT, NJ, 256>(a, stream);
+    }
 }
 
 PrepPlan w8a8_prep_plan(int64_t T, int64_t d, int32_t r, bool small) {
@@ -788,7 +810,8 @@ hipError_t launch_w8a8_prep(const PrepArgs& a, const PrepPlan& p, bool join, hip
     return hipGetLastError();
 }
 
-template <int WM, int WN, int TT>
+// SPLIT: the tile takes K ranges (only 128 x 128 does).
+template <int WM, int WN, int TT, bool SPLIT>
 static hipError_t launch_tile(const ForwardArgs& a, const PrepArgs& p, hipStream_t stream) {
     // every XCD takes ceil(columns / 8) columns of every token block; those it has not return at once
     const int64_t join = a.tile_ks > 1 && a.r > 0 && p.part != nullptr
@@ -796,23 +819,29 @@ static hipError_t launch_tile(const ForwardArgs& a, const PrepArgs& p, hipStream
     const int64_t grid = join + 8 * ceil_div(a.n_tiles, 8) * a.m_tiles;
     if (grid * 64 * WM * WN > (int64_t)UINT32_MAX) return hipErrorInvalidConfiguration;
     const dim3 g((unsigned)grid), block(64 * WM * WN);
-    if (a.tile_ks > 1) hipLaunchKernelGGL((w8a8_tile_kernel<WM, WN, TT, kW8Split>), g, block, 0, stream, a, p, (int)join);
-    else if (a.r > 0) hipLaunchKernelGGL((w8a8_tile_kernel<WM, WN, TT, kW8Correct>), g, block, 0, stream, a, p, (int)join);
+    if constexpr (SPLIT) {
+        if (a.tile_ks > 1) {
+            hipLaunchKernelGGL((w8a8_tile_kernel<WM, WN, TT, kW8Split>), g, block, 0, stream, a, p, (int)join);
+            const hipError_t e = hipGetLastError();
+            if (e != hipSuccess) return e;
+            const int pieces = a.m_tiles * (a.n_tiles / a.tile_ks) * WM * WN * TT;
+            hipLaunchKernelGGL((w8a8_join_kernel<WM, WN, TT>), dim3((unsigned)ceil_div(pieces, 4)), dim3(256), 0, stream, a,
+                               pieces);
+            return hipGetLastError();
+        }
+    }
+    if (a.tile_ks > 1) return hipErrorInvalidValue;
+    if (a.r > 0) hipLaunchKernelGGL((w8a8_tile_kernel<WM, WN, TT, kW8Correct>), g, block, 0, stream, a, p, (int)join);
     else hipLaunchKernelGGL((w8a8_tile_kernel<WM, WN, TT, kW8Plain>), g, block, 0, stream, a, p, (int)join);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || a.tile_ks == 1) return e;
-    const int pieces = a.m_tiles * (a.n_tiles / a.tile_ks) * WM * WN * TT;
-    hipLaunchKernelGGL(w8a8_join_kernel, dim3((unsigned)ceil_div(pieces, 4)), dim3(256), 0, stream, a, WM, WN, TT, pieces);
     return hipGetLastError();
 }
 
 hipError_t launch_w8a8(const ForwardArgs& a, const PrepArgs& p, hipStream_t stream) {
-    if (a.tile_rr == 16) return launch_tile<1, 4, 8>(a, p, stream);
-    if (a.tile_rr == 8) return a.tile_tt == 8 ? launch_tile<2, 2, 4>(a, p, stream) : launch_tile<1, 2, 4>(a, p, stream);
+    if (a.tile_rr == 16) return launch_tile<1, 4, 8, false>(a, p, stream);
+    if (a.tile_rr == 8) return a.tile_tt == 8 ? launch_tile<2, 2, 4, true>(a, p, stream) : launch_tile<1, 2, 4, false>(a, p, stream);
     const dim3 grid((unsigned)a.n_tiles), block(64 * kW8Waves);
     switch (a.tile_tt * 4 + a.tile_rr) {
         case 4 + 1: hipLaunchKernelGGL((w8a8_split_kernel<1, 1>), grid, block, 0, stream, a); break;
-        case 8 + 1: hipLaunchKernelGGL((w8a8_split_kernel<2, 1>), grid, block, 0, stream, a); break;
         case 8 + 2: hipLaunchKernelGGL((w8a8_split_kernel<2, 2>), grid, block, 0, stream, a); break;
         case 16 + 2: hipLaunchKernelGGL((w8a8_split_kernel<4, 2>), grid, block, 0, stream, a); break;
         default: return hipErrorInvalidValue;
