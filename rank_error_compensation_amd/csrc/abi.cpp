@@ -516,9 +516,9 @@ int run_w4a8(const Call& c, void* workspace, hipStream_t stream) {
     return (c.mx8 ? launch_mx8(f, stream) : launch_w4a8(f, stream)) == hipSuccess ? GLOWQ_OK : GLOWQ_ERR_HIP;
 }
 
-// K ranges' int32 tiles of a call of more than 64 tokens: bounded by the workspace that
-// glowq_w8a8_workspace_bytes reserves for them.
-constexpr size_t kW8PartBytes = (size_t)32 << 20;
+// K ranges' int32 tiles of a call of more than 32 tokens: at most 256 of 64 KB, which
+// glowq_w8a8_workspace_bytes reserves.
+constexpr size_t kW8PartBytes = (size_t)16 << 20;
 constexpr int64_t kW8TinyT = 32;   // the small form alone up to here
 constexpr int64_t kW8SmallT = 64;  // and, by the number of tiles, up to here
 // row stride of the projection: whole 64-column blocks, as the large tiles take them
@@ -533,17 +533,27 @@ inline size_t w8_part_bytes(int64_t T, int32_t r) {
 }
 
 W8Shape choose_w8a8_shape(const Call& c) {
-    W8Shape s = {c.T <= 16 ? 1 : (c.T <= 32 ? 2 : 4), c.T <= 16 ? 1 : 2, 1, (int)(c.d / kGroup)};
+    W8Shape s = {c.T <= 16 ? 1 : (c.T <= 32 ? 2 : 4), c.T <= 16 ? 1 : 2, 1, 1, (int)(c.d / kGroup)};
     auto tiles = [&](int tt, int rr) {
         int64_t n = 0;
         for (int i = 0; i < c.m; ++i) n += ceil_div(ceil_div(c.w[i].n_out, 16), rr);
         return n * ceil_div(c.T, 16 * tt);
     };
-    // Up to 64 tokens the small form, but past 32 tokens 64 x 128 tiles where they are many: the small form reads
-    // the codes anew for every 32 rows (2 x 11008 <- 4096 at T = 64, 172 tiles: 33 us, the small form 45; at
-    // T = 40: 32 and 36; Q/K/V 4096 + 2 x 1024, 48 tiles: 31 and 21)
+    const int64_t G = c.d / kGroup;
+    // Up to 64 tokens the small form.  Past 32 tokens one of its workgroups fills a CU and reads the token block's codes
+    // anew for its 32 rows, so 64 x 128 tiles (four teams of wavefronts each) where it has more workgroups than
+    // CUs or where a block's codes are many (r = 64, T = 64: 2 x 11008 <- 4096, 172 tiles, 32 us, the small form 45;
+    // 12288 <- 4096, 96 tiles, 28 and 33; 4096 <- 8192, 27 and 30; 4096 <- 14336, 32 and 44; but 8192 <- 6144, 64
+    // tiles, 30 and 25; 4096 <- 8192 at T = 40, 26 and 24), with K ranges of at least 24 groups up to a tile a CU
+    // (4096 <- 14336, 32 tiles: 32 us in four ranges, 38 in two; 2 x 8192 <- 4096: 32 in two, 29 in one)
     if (c.T <= kW8SmallT) {
-        if (c.T > kW8TinyT && tiles(4, 8) >= 128) s.tt = 4, s.rr = 8;
+        if (c.T <= kW8TinyT) return s;
+        const int64_t n = tiles(4, 8);
+        if (n <= 64 && c.T * c.d < ((int64_t)1 << 19)) return s;
+        s.tt = 4, s.rr = 8, s.kh = 4;
+        const int64_t ks = std::max<int64_t>(1, std::min<int64_t>(256 / n, G / 24));
+        s.gk = (int)ceil_div(G, ks);
+        s.ks = (int)ceil_div(G, s.gk);
         return s;
     }
     // 128 x 256 tiles for more than one a CU (measured at d = 4096, r = 64: QKV 4096 + 2 x 1024 at T = 2048, 384 of
@@ -552,18 +562,19 @@ W8Shape choose_w8a8_shape(const Call& c) {
     s.tt = 8;
     s.rr = 16;
     if (tiles(8, 16) > 256) return s;
-    // Fewer: 128 x 128 tiles, K split until every CU has one, with ranges of at least 8 groups (4096 <- 4096 at
-    // T = 200, 64 tiles: 31 us in four ranges, 35 in two); two a CU only with ranges of 24 (4096 <- 14336 at
-    // T = 512, 128 tiles: 66 us in four ranges, 71 in two, 97 in one; 4096 <- 4096: 40, 37 and 39;
-    // 2 x 11008 <- 4096 at T = 128, 172 tiles: 46 in two, 39 in one)
+    // Fewer: 128 x 128 tiles; up to one a CU on two teams of wavefronts, which halve the input groups, where those are
+    // at least 16 (2 x 11008 <- 4096 at T = 128, 172 tiles: 36.5 us, 39 with one team; 2816 <- 14336 at T = 1000, 176
+    // tiles: 110 and 120; but 24576 <- 1024 at T = 128: 22 and 21; 2 x 11008 <- 4096 at T = 256, 344 tiles: 61 and 52),
+    // K split up to a tile a CU, with ranges of at least 8 groups (4096 <- 4096 at T = 200, 64 tiles: 29 us in four
+    // ranges, 31 in two, 36 in one, 40 in eight of 4 groups; 4096 <- 14336 at T = 512, 128 tiles: 64 in two, 79 in four)
     s.rr = 8;
-    const int64_t n = tiles(8, 8), G = c.d / kGroup;
-    int64_t ks = std::min<int64_t>(256 / n, G / 8);
-    if (G / 24 >= 512 / n) ks = std::max<int64_t>(ks, 512 / n);
-    ks = std::max<int64_t>(ks, 1);
+    const int64_t n = tiles(8, 8);
+    if (n > 256 || G < 16) return s;
+    s.kh = 2;
+    const int64_t ks = std::max<int64_t>(1, std::min<int64_t>(256 / n, G / 8));
     s.gk = (int)ceil_div(G, ks);
     s.ks = (int)ceil_div(G, s.gk);
-    return s;  // n ks <= 512 tiles of 64 KB wherever ks > 1
+    return s;  // n ks <= 256 int32 tiles of at most 64 KB wherever ks > 1
 }
 
 // W8A8 form.  Workspace: codes int8 [T][d] | scales fp32 [T] | fp16 projection [T][r_pad]
@@ -580,9 +591,10 @@ int run_w8a8(const Call& c, void* workspace, hipStream_t stream) {
     if (s.ks > 1) {
         int64_t n = 0;
         for (int i = 0; i < c.m; ++i) n += ceil_div(c.w[i].n_out, 128);
-        if ((size_t)(n * ceil_div(c.T, 128) * s.ks) * 65536u > kW8PartBytes) return GLOWQ_ERR_WORKSPACE;
+        if ((size_t)(n * ceil_div(c.T, 16 * s.tt) * s.ks * s.tt) * 8192u > kW8PartBytes) return GLOWQ_ERR_WORKSPACE;
     }
     const bool small = s.rr <= 2;
+    const bool ranges = small || (s.kh > 1 && s.ks == 1);  // the product adds up the projection's K ranges itself
     const PrepPlan pp = w8a8_prep_plan(c.T, c.d, r, small);
     PrepArgs pa;
     std::memset(&pa, 0, sizeof(pa));
@@ -597,7 +609,7 @@ int run_w8a8(const Call& c, void* workspace, hipStream_t stream) {
     pa.xq = xq;
     pa.xscale = xscale;
     if (c.correct) {
-        if (small || pp.ks > 1) {
+        if (ranges || pp.ks > 1) {
             pa.part = reinterpret_cast<float*>(base);
             if ((size_t)pp.ks * (size_t)c.T * (size_t)rp * 4u > w8_part_bytes(c.T, r)) return GLOWQ_ERR_WORKSPACE;
             base += w8_part_bytes(c.T, r);
@@ -605,7 +617,7 @@ int run_w8a8(const Call& c, void* workspace, hipStream_t stream) {
         pa.R = reinterpret_cast<_Float16*>(base);
         base += w8_r_bytes(c.T, r);
     }
-    if (launch_w8a8_prep(pa, pp, s.ks == 1, stream) != hipSuccess) return GLOWQ_ERR_HIP;
+    if (launch_w8a8_prep(pa, pp, !ranges && s.ks == 1, stream) != hipSuccess) return GLOWQ_ERR_HIP;
     ForwardArgs f;
     std::memset(&f, 0, sizeof(f));
     f.T = (int32_t)c.T;
@@ -614,14 +626,15 @@ int run_w8a8(const Call& c, void* workspace, hipStream_t stream) {
     f.r = r;
     f.r_pad = rp;
     f.n_mod = c.m;
-    f.R = small ? static_cast<void*>(pa.part) : static_cast<void*>(pa.R);
-    f.n_proj = pp.ks;  // fp32 K ranges of R (small calls)
+    f.R = ranges ? static_cast<void*>(pa.part) : static_cast<void*>(pa.R);
+    f.n_proj = pp.ks;  // fp32 K ranges of R, where the product adds them up
     f.xq = xq;
     f.xscale = xscale;
     f.fmt = kFmtInt8;
     f.tile_tt = s.tt;
     f.tile_rr = s.rr;
     f.tile_ks = s.ks;
+    f.dec_ks = s.kh;
     f.dec_gk = s.gk;
     f.ypart = reinterpret_cast<float*>(base);
     int64_t tiles = 0;
@@ -997,7 +1010,7 @@ size_t glowq_w8a8_workspace_bytes(int64_t T, int64_t d, int32_t r) {
     if (T <= 0 || T > kMaxT || d < kGroup || d % kGroup != 0 || d > kW8MaxD || r < 0 || r > GLOWQ_MAX_RANK) return 0;
     size_t n = round256((size_t)T * d) + round256((size_t)T * 4u);
     if (r > 0) n += w8_part_bytes(T, r) + w8_r_bytes(T, r);
-    if (T > kW8SmallT) n += kW8PartBytes;
+    if (T > kW8TinyT) n += kW8PartBytes;
     return n;
 }
 

@@ -237,7 +237,7 @@ __global__ __launch_bounds__(kPrepThreads) void prep_kernel(const PrepArgs a, in
 }
 
 // R = the K ranges' sums added in order, rounded once to fp16; four values from value 4 i.  A few MB out of
-// the caches (T = 2048, r = 64, 8 ranges: 4.2 MB, 4.9 us): bound by its launch.
+// the caches (T = 2048, r = 64, 4 ranges: 2.1 MB, 4.9 us): bound by its launch.
 __device__ __forceinline__ void join_ranges(const PrepArgs& a, size_t i) {
     const size_t n = (size_t)a.T * a.rp / 4;
     if (i >= n) return;
@@ -374,14 +374,19 @@ __global__ __launch_bounds__(64 * kW8Waves) void w8a8_split_kernel(const Forward
 // c ^ f(r), f(r) = (r % 8) ^ ((r / 8) % 2): the 16 rows of an operand read fall in distinct banks.
 // Tokens past T read token T - 1 and row tiles past the module its last tile; neither is stored.
 //
-// With args.tile_ks > 1 the input groups are split over workgroups: each writes its exact int32
-// tile to the workspace, and w8a8_join_kernel adds them and finishes.
+// Where the tiles do not fill the GPU, KH such teams of WM x WN wavefronts share a workgroup: each takes a part
+// of the input groups through a ring of its own, the exact int32 sums meet in LDS, and a team finishes
+// TT / KH of the token tiles -- a full CU from one workgroup at a KH-th of the partial tiles that a split over
+// workgroups writes.  With args.tile_ks > 1 the input groups are split over workgroups too: each writes its exact
+// int32 tile to the workspace, and w8a8_join_kernel adds them and finishes.
 //
 // Measured (r = 64): 128 x 256, T = 2048, 2 x 11008 rows <- 4096: 185 to 191 us, 2.0 Pop/s of int8 (a plain int8
 // product of 8192^3 by the vendor's library: 2.07).  Matrix cores busy 0.47 of the time, operand returns from the
 // L1/LDS path 0.70 (2.4 GB from the L2 caches, 13 TB/s; 0.39 GB from behind them): bound by feeding operands.  256 x 256
 // on 4 or 8 wavefronts and 128 x 512 on 8 (half the weight traffic, one workgroup a CU) took 200 to 212 us.
-// 128 x 128 in four K ranges, T = 512, 4096 rows <- 14336: 40 us, 1.5 Pop/s, matrix cores busy 0.28.
+// 128 x 128 with two teams in two K ranges, T = 512, 4096 rows <- 14336: 45 us, 1.3 Pop/s; unsplit, T = 128,
+// 2 x 11008 <- 4096: 28 us (90 MB of weights from the last-level cache: 3.3 TB/s).  64 x 128 with four teams, T = 64,
+// the same rows: 23 us (3.9 TB/s).
 typedef __attribute__((address_space(3))) void lds_void;
 template <int I>
 using ic = std::integral_constant<int, I>;
@@ -407,23 +412,25 @@ __device__ __forceinline__ bool w8_place(const ForwardArgs& args, int block, int
 
 enum : int { kW8Plain = 0, kW8Correct = 1, kW8Split = 2 };  // what follows the integer sums
 
-template <int WM, int WN, int TT, int MODE>
-__global__ __launch_bounds__(64 * WM * WN, 2) void w8a8_tile_kernel(const ForwardArgs args, const PrepArgs prep,
-                                                                   int join_blocks) {
+template <int WM, int WN, int TT, int KH, int MODE>
+__global__ __launch_bounds__(64 * WM * WN * KH, 2) void w8a8_tile_kernel(const ForwardArgs args, const PrepArgs prep,
+                                                                        int join_blocks) {
     constexpr int RR = 4, NW = WM * WN, BM = 16 * TT * WM, SB = BM * 128;
-    constexpr int NC = BM / 8 / NW;  // 1 KB code copies per wavefront and group
-    static_assert(NC * 8 * NW == BM && NC + 3 * RR < 63 && BM % 64 == 0, "copies");
-    __shared__ __attribute__((aligned(16))) uint8_t st0[SB];
-    __shared__ __attribute__((aligned(16))) uint8_t st1[SB];
-    __shared__ __attribute__((aligned(16))) uint8_t st2[SB];
-    __shared__ __attribute__((aligned(16))) uint8_t st3[SB];
-    __shared__ __attribute__((aligned(16))) float row_scale[NW * 64];
+    constexpr int NC = BM / 8 / NW;        // 1 KB code copies per wavefront and group
+    constexpr int TE = TT / KH;            // token tiles that a wavefront finishes
+    constexpr int NE = BM / 8 / (NW * KH); // copies per wavefront of a stage that all fill
+    static_assert(NC * 8 * NW == BM && NC + 3 * RR < 63 && BM % 64 == 0 && NE > 0 && TE * KH == TT, "copies");
+    __shared__ __attribute__((aligned(16))) uint8_t st0[KH * SB];
+    __shared__ __attribute__((aligned(16))) uint8_t st1[KH * SB];
+    __shared__ __attribute__((aligned(16))) uint8_t st2[KH * SB];
+    __shared__ __attribute__((aligned(16))) uint8_t st3[KH * SB];
+    __shared__ __attribute__((aligned(16))) float row_scale[NW * KH * 64];
     __shared__ __attribute__((aligned(16))) float tok_scale[BM];
     // With a K split the projection is only used by the launch after this one: the first workgroups (a
     // multiple of 8) join its ranges instead of a launch of their own
     if constexpr (MODE == kW8Split) {
         if ((int)blockIdx.x < join_blocks) {
-            join_ranges(prep, (size_t)blockIdx.x * (64 * NW) + threadIdx.x);
+            join_ranges(prep, (size_t)blockIdx.x * (64 * NW * KH) + threadIdx.x);
             return;
         }
     }
@@ -432,11 +439,15 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void w8a8_tile_kernel(const Forwar
     const int ks = MODE == kW8Split ? args.tile_ks : 1, nbl = col / ks, kr = col - nbl * ks;
     const ModuleArgs M = args.mod[module_of(args, nbl)];
     const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int wave_all = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int kh = KH > 1 ? wave_all / NW : 0, wave = KH > 1 ? wave_all % NW : wave_all;  // team, wavefront of it
     const int wm = wave % WM, wn = wave / WM;
     const int T = args.T, d = args.d, NT = M.n_tiles16;
     const int m0 = mb * BM, rt0 = (nbl - M.tile_begin) * RR * WN + wn * RR;
-    const int g_begin = kr * args.dec_gk, n_g = min(args.dec_gk, args.G - g_begin);
+    // groups of the workgroup, and the KH-th part of them that this team takes (the last may be shorter, or none)
+    const int n_all = min(args.dec_gk, args.G - kr * args.dec_gk), n_turn = (n_all + KH - 1) / KH;
+    const int g_begin = kr * args.dec_gk + kh * n_turn, n_g = max(0, min(n_turn, n_all - kh * n_turn));
+    const int g_last = min(g_begin + n_g, args.G) - 1;  // steps past the part repeat its last group
     // copy i of wave w fills rows 8 (NC w + i) .. + 7 of the stage; lane l lands at row + l / 8,
     // position l % 8, holding the row's piece (l % 8) ^ f(row)
     uint32_t xoff[NC];
@@ -454,11 +465,11 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void w8a8_tile_kernel(const Forwar
     const uint32_t lofs = lane * 16;
 
     auto copy = [&](int v, uint8_t* stg) {
-        const int8_t* base = args.xq + (size_t)(g_begin + min(v, n_g - 1)) * kGroup;
+        const int8_t* base = args.xq + (size_t)min(g_begin + v, g_last) * kGroup;
 #pragma unroll
         for (int i = 0; i < NC; ++i)
-            __builtin_amdgcn_global_load_lds((const void*)(base + xoff[i]), (lds_void*)(stg + 8 * (NC * wave + i) * 128), 16, 0,
-                                             0);
+            __builtin_amdgcn_global_load_lds((const void*)(base + xoff[i]), (lds_void*)(stg + kh * SB + 8 * (NC * wave + i) * 128),
+                                             16, 0, 0);
     };
     // Operands in flight: where registers allow (TT = 4), whole groups three ahead, group v in slot v % 4;
     // else halves, half h = 2 v + m in slot h % 4, three halves ahead.
@@ -466,7 +477,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void w8a8_tile_kernel(const Forwar
     constexpr int kAhead = kDeep ? 3 : 2;  // groups the code copies are ahead
     i4v w[kDeep ? 8 : 4][RR];
     auto wload = [&](int v, int m, int slot) {
-        const size_t g = (size_t)(g_begin + min(v, n_g - 1)) * NT;
+        const size_t g = (size_t)min(g_begin + v, g_last) * NT;
 #pragma unroll
         for (int rr = 0; rr < RR; ++rr)
             w[slot][rr] = *reinterpret_cast<const i4v*>(M.q + (g + rts[rr]) * kW8Block + 1024 * m + lofs);
@@ -479,9 +490,9 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void w8a8_tile_kernel(const Forwar
 
     {
         const uint32_t rt = (uint32_t)min(rt0 + (lane >> 4), NT - 1);
-        __builtin_amdgcn_global_load_lds((const void*)(M.sz + (rt * 64 + (lane & 15) * 4)), (lds_void*)(row_scale + wave * 64),
+        __builtin_amdgcn_global_load_lds((const void*)(M.sz + (rt * 64 + (lane & 15) * 4)), (lds_void*)(row_scale + wave_all * 64),
                                          4, 0, 0);
-        const int t0 = 64 * (wave % (BM / 64));
+        const int t0 = 64 * (wave_all % (BM / 64));
         __builtin_amdgcn_global_load_lds((const void*)(args.xscale + min(m0 + t0 + lane, T - 1)),
                                          (lds_void*)(tok_scale + t0), 4, 0, 0);
     }
@@ -505,7 +516,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void w8a8_tile_kernel(const Forwar
         constexpr int N = kDeep ? 2 * NC + 6 * RR : NC + 3 * RR;
         static_assert(N < 64, "vmcnt");
         uint8_t* const st[4] = {st0, st1, st2, st3};
-        uint8_t* cur = st[S];
+        const uint8_t* cur = st[S] + kh * SB;
         uint8_t* nxt = st[(S + kAhead) & 3];
         __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | ((N >> 4) << 14));  // vmcnt(N)
         __builtin_amdgcn_s_barrier();
@@ -555,23 +566,55 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void w8a8_tile_kernel(const Forwar
     };
     // whole turns of the ring; steps past the range only keep time (a tail of its own made the
     // compiler move and spill accumulators)
-    for (int v = 0; v < n_g; v += 4) {
+    for (int v = 0; v < n_turn; v += 4) {
         step(v, ic<0>{});
         step(v + 1, ic<1>{});
         step(v + 2, ic<2>{});
         step(v + 3, ic<3>{});
     }
-    if constexpr (MODE == kW8Split) {
-        __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): no copy may land in LDS after the workgroup ends
-        i4v* part = reinterpret_cast<i4v*>(args.ypart) + ((((size_t)mb * (args.n_tiles / ks) + nbl) * ks + kr) * NW + wave) * (TT * RR * 64);
+    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): no copy may land in LDS after this
+    __builtin_amdgcn_s_barrier();
+    // Team kh finishes token tiles TE kh .. + TE - 1: the others' sums of them come through LDS, past the
+    // first SB bytes of the stages (those are R's).
+    if constexpr (KH > 1) {
+        constexpr int kPiece = TE * RR * 1024, kStage = (KH - 1) * SB / kPiece;
+        static_assert(kStage * kPiece == (KH - 1) * SB && 4 * kStage == KH * NW * (KH - 1), "sums fill the stages");
+        auto piece_at = [&](int to, int from) {
+            const int q = (to * NW + wave) * (KH - 1) + (from - to + KH) % KH - 1, at = q / kStage;
+            return (at == 0 ? st0 : (at == 1 ? st1 : (at == 2 ? st2 : st3))) + SB + (q % kStage) * kPiece + 16 * lane;
+        };
 #pragma unroll
-        for (int tt = 0; tt < TT; ++tt)
+        for (int to = 0; to < KH; ++to)
+            if (to != kh) {
+                uint8_t* dst = piece_at(to, kh);
+#pragma unroll
+                for (int i = 0; i < TE * RR; ++i)
+                    *reinterpret_cast<i4v*>(dst + 1024 * i) = acc[to * TE + i / RR][i % RR];
+            }
+#pragma unroll
+        for (int to = 1; to < KH; ++to)
+            if (to == kh) {
+#pragma unroll
+                for (int i = 0; i < TE * RR; ++i) acc[i / RR][i % RR] = acc[to * TE + i / RR][i % RR];
+            }
+        __syncthreads();
+#pragma unroll
+        for (int k = 1; k < KH; ++k) {
+            const uint8_t* src = piece_at(kh, (kh + k) % KH);
+#pragma unroll
+            for (int i = 0; i < TE * RR; ++i) acc[i / RR][i % RR] += *reinterpret_cast<const i4v*>(src + 1024 * i);
+        }
+    }
+    if constexpr (MODE == kW8Split) {
+        i4v* part = reinterpret_cast<i4v*>(args.ypart) +
+                    ((((size_t)mb * (args.n_tiles / ks) + nbl) * ks + kr) * NW + wave) * (TT * RR * 64) + kh * (TE * RR * 64);
+#pragma unroll
+        for (int tt = 0; tt < TE; ++tt)
 #pragma unroll
             for (int rr = 0; rr < RR; ++rr) part[(tt * RR + rr) * 64 + lane] = acc[tt][rr];
         return;
     }
-    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): no copy may land in LDS after this
-    __builtin_amdgcn_s_barrier();
+    const int te0 = TT * wm + TE * kh;  // first of the wavefront's token tiles
     // The correction: R's columns 64 j .. + 63 (128 bytes a token, as a group of codes) go to stage j (r <= 256),
     // A's operands to registers, while the sums are scaled.  Rows of A past the module and tokens past T
     // repeat the last one (their results are not stored); columns of A past r are taken as zero, R's are
@@ -579,12 +622,33 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void w8a8_tile_kernel(const Forwar
     const int r = args.r, rp = args.r_pad;
     auto rcopy = [&](int j, uint8_t* stg) {
         if (64 * j >= rp) return;
+        if constexpr (KH > 1) {  // R as the K ranges' fp32 sums: added in order, rounded once to fp16 here
+            for (int i = threadIdx.x; i < BM * 8; i += 64 * NW * KH) {
+                const int row = i >> 3, c = i & 7;
+                const float* p = static_cast<const float*>(args.R) + (size_t)min(m0 + row, T - 1) * rp + (64 * j + 8 * c);
+                f4 lo = *reinterpret_cast<const f4*>(p), hi = *reinterpret_cast<const f4*>(p + 4);
+                for (int k = 1; k < args.n_proj; ++k) {
+                    p += (size_t)T * rp;
+                    lo += *reinterpret_cast<const f4*>(p);
+                    hi += *reinterpret_cast<const f4*>(p + 4);
+                }
+                h8 v;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    v[e] = (_Float16)lo[e];
+                    v[4 + e] = (_Float16)hi[e];
+                }
+                *reinterpret_cast<h8*>(stg + row * 128 + 16 * (c ^ (row & 7) ^ ((row >> 3) & 1))) = v;
+            }
+            return;
+        }
         const uint8_t* base = reinterpret_cast<const uint8_t*>(args.R) + 128 * j;
 #pragma unroll
-        for (int i = 0; i < NC; ++i) {
-            const uint32_t t = (uint32_t)min(m0 + 8 * (NC * wave + i) + (lane >> 3), T - 1);
-            __builtin_amdgcn_global_load_lds((const void*)(base + (t * (uint32_t)rp * 2u + (piece ^ (16 * (i & 1))))),
-                                             (lds_void*)(stg + 8 * (NC * wave + i) * 128), 16, 0, 0);
+        for (int i = 0; i < NE; ++i) {
+            const int row = NE * wave_all + i;  // of eight tokens
+            const uint32_t t = (uint32_t)min(m0 + 8 * row + (lane >> 3), T - 1);
+            __builtin_amdgcn_global_load_lds((const void*)(base + (t * (uint32_t)rp * 2u + (piece ^ (16 * (row & 1))))),
+                                             (lds_void*)(stg + 8 * row * 128), 16, 0, 0);
         }
     };
     const uint8_t* Ab = reinterpret_cast<const uint8_t*>(M.a) + (size_t)rts[0] * 32 * r;
@@ -612,10 +676,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void w8a8_tile_kernel(const Forwar
         f4 sw[RR];
 #pragma unroll
         for (int rr = 0; rr < RR; ++rr)
-            sw[rr] = *reinterpret_cast<const f4*>(row_scale + wave * 64 + 16 * rr + 4 * (lane >> 4));
+            sw[rr] = *reinterpret_cast<const f4*>(row_scale + wave_all * 64 + 16 * rr + 4 * (lane >> 4));
 #pragma unroll
-        for (int tt = 0; tt < TT; ++tt) {
-            float st = tok_scale[16 * (TT * wm + tt) + (lane & 15)];
+        for (int tt = 0; tt < TE; ++tt) {
+            float st = tok_scale[16 * (te0 + tt) + (lane & 15)];
             asm volatile("" : "+v"(st));
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -631,7 +695,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void w8a8_tile_kernel(const Forwar
     }
     if constexpr (MODE == kW8Correct) {
         __builtin_amdgcn_s_waitcnt(0x0F70);
-        __builtin_amdgcn_s_barrier();
+        __syncthreads();
         int j = 0;
 #pragma unroll 1
         do {
@@ -647,8 +711,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void w8a8_tile_kernel(const Forwar
 #pragma unroll
                 for (int rr = 0; rr < RR; ++rr) av[rr] = __builtin_bit_cast(h8, in ? w[m][rr] : i4v{0, 0, 0, 0});
 #pragma unroll
-                for (int tt = 0; tt < TT; ++tt) {
-                    const h8 xv = *reinterpret_cast<const h8*>(cur + (m == 0 ? rofs0 : rofs1) + tt * 2048);
+                for (int tt = 0; tt < TE; ++tt) {
+                    const h8 xv = *reinterpret_cast<const h8*>(cur + (m == 0 ? rofs0 : rofs1) + (TE * kh + tt) * 2048);
 #pragma unroll
                     for (int rr = 0; rr < RR; ++rr)
                         acc[tt][rr] = __builtin_bit_cast(i4v, mfma16(av[rr], xv, __builtin_bit_cast(f4, acc[tt][rr])));
@@ -660,12 +724,12 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void w8a8_tile_kernel(const Forwar
     // To memory through the wavefront's own part of the (finished) ring: [16 TT tokens][64 rows] fp16,
     // a token's eight 16-byte pieces p at p ^ (token % 8), then whole 128-byte lines.
     __builtin_amdgcn_s_barrier();
-    constexpr int kPart = 16 * TT * 128, kPer = SB / kPart;
-    static_assert(NW * kPart <= 4 * SB && SB % kPart == 0, "a part per wavefront");
-    const int sel = wave / kPer;
-    uint8_t* out = (sel == 0 ? st0 : (sel == 1 ? st1 : (sel == 2 ? st2 : st3))) + (wave % kPer) * kPart;
+    constexpr int kPart = 16 * TE * 128, kPer = SB / kPart;
+    static_assert(NW * KH * kPart <= 4 * SB && SB % kPart == 0, "a part per wavefront");
+    const int sel = wave_all / kPer;
+    uint8_t* out = (sel == 0 ? st0 : (sel == 1 ? st1 : (sel == 2 ? st2 : st3))) + (wave_all % kPer) * kPart;
 #pragma unroll
-    for (int tt = 0; tt < TT; ++tt)
+    for (int tt = 0; tt < TE; ++tt)
 #pragma unroll
         for (int rr = 0; rr < RR; ++rr) {
             const f4 v = __builtin_bit_cast(f4, acc[tt][rr]);
@@ -678,8 +742,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void w8a8_tile_kernel(const Forwar
     const int row0 = rt0 * 16 + 8 * (lane & 7);
     const bool vec = (M.n_out & 7) == 0 && row0 + 7 < M.n_out;
 #pragma unroll 4
-    for (int i = 0; i < 2 * TT; ++i) {
-        const int tl = 8 * i + (lane >> 3), t = m0 + 16 * TT * wm + tl;
+    for (int i = 0; i < 2 * TE; ++i) {
+        const int tl = 8 * i + (lane >> 3), t = m0 + 16 * te0 + tl;
         const uint8_t* piece = out + tl * 128 + 16 * ((lane & 7) ^ (tl & 7));
         if (t >= T) continue;
         _Float16* y = M.y + (size_t)t * M.n_out + row0;
@@ -692,8 +756,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void w8a8_tile_kernel(const Forwar
 }
 
 // Sums of the K ranges of one 16-token x 64-row piece per wavefront (pieces numbered as the tile
-// kernel stores them), scales, correction, one rounding to fp16.  Memory-bound: T = 512, 4096 rows, four
-// ranges: 33.5 MB of sums (from the caches) in 11 us, 3.4 TB/s with the 4.2 MB of y.
+// kernel stores them), scales, correction, one rounding to fp16.  Memory- and launch-bound: T = 512, 4096 rows, two
+// ranges, 16.8 MB of sums and 4.2 MB of y: 9.7 us.
 template <int WM, int WN, int TT>
 __global__ __launch_bounds__(256) void w8a8_join_kernel(const ForwardArgs args, int pieces) {
     constexpr int RR = 4, NW = WM * WN;
@@ -811,17 +875,17 @@ hipError_t launch_w8a8_prep(const PrepArgs& a, const PrepPlan& p, bool join, hip
 }
 
 // SPLIT: the tile takes K ranges (only 128 x 128 does).
-template <int WM, int WN, int TT, bool SPLIT>
+template <int WM, int WN, int TT, int KH, bool SPLIT>
 static hipError_t launch_tile(const ForwardArgs& a, const PrepArgs& p, hipStream_t stream) {
     // every XCD takes ceil(columns / 8) columns of every token block; those it has not return at once
     const int64_t join = a.tile_ks > 1 && a.r > 0 && p.part != nullptr
-                             ? ceil_div(ceil_div((int64_t)p.T * p.rp / 4, 64 * WM * WN), 8) * 8 : 0;
+                             ? ceil_div(ceil_div((int64_t)p.T * p.rp / 4, 64 * WM * WN * KH), 8) * 8 : 0;
     const int64_t grid = join + 8 * ceil_div(a.n_tiles, 8) * a.m_tiles;
-    if (grid * 64 * WM * WN > (int64_t)UINT32_MAX) return hipErrorInvalidConfiguration;
-    const dim3 g((unsigned)grid), block(64 * WM * WN);
+    if (grid * 64 * WM * WN * KH > (int64_t)UINT32_MAX) return hipErrorInvalidConfiguration;
+    const dim3 g((unsigned)grid), block(64 * WM * WN * KH);
     if constexpr (SPLIT) {
         if (a.tile_ks > 1) {
-            hipLaunchKernelGGL((w8a8_tile_kernel<WM, WN, TT, kW8Split>), g, block, 0, stream, a, p, (int)join);
+            hipLaunchKernelGGL((w8a8_tile_kernel<WM, WN, TT, KH, kW8Split>), g, block, 0, stream, a, p, (int)join);
             const hipError_t e = hipGetLastError();
             if (e != hipSuccess) return e;
             const int pieces = a.m_tiles * (a.n_tiles / a.tile_ks) * WM * WN * TT;
@@ -831,14 +895,16 @@ static hipError_t launch_tile(const ForwardArgs& a, const PrepArgs& p, hipStream
         }
     }
     if (a.tile_ks > 1) return hipErrorInvalidValue;
-    if (a.r > 0) hipLaunchKernelGGL((w8a8_tile_kernel<WM, WN, TT, kW8Correct>), g, block, 0, stream, a, p, (int)join);
-    else hipLaunchKernelGGL((w8a8_tile_kernel<WM, WN, TT, kW8Plain>), g, block, 0, stream, a, p, (int)join);
+    if (a.r > 0) hipLaunchKernelGGL((w8a8_tile_kernel<WM, WN, TT, KH, kW8Correct>), g, block, 0, stream, a, p, (int)join);
+    else hipLaunchKernelGGL((w8a8_tile_kernel<WM, WN, TT, KH, kW8Plain>), g, block, 0, stream, a, p, (int)join);
     return hipGetLastError();
 }
 
 hipError_t launch_w8a8(const ForwardArgs& a, const PrepArgs& p, hipStream_t stream) {
-    if (a.tile_rr == 16) return launch_tile<1, 4, 8, false>(a, p, stream);
-    if (a.tile_rr == 8) return a.tile_tt == 8 ? launch_tile<2, 2, 4, true>(a, p, stream) : launch_tile<1, 2, 4, false>(a, p, stream);
+    if (a.tile_rr == 16) return launch_tile<1, 4, 8, 1, false>(a, p, stream);
+    if (a.tile_rr == 8 && a.tile_tt == 8)
+        return a.dec_ks == 2 ? launch_tile<2, 2, 4, 2, true>(a, p, stream) : launch_tile<2, 2, 4, 1, false>(a, p, stream);
+    if (a.tile_rr == 8) return launch_tile<1, 2, 4, 4, true>(a, p, stream);
     const dim3 grid((unsigned)a.n_tiles), block(64 * kW8Waves);
     switch (a.tile_tt * 4 + a.tile_rr) {
         case 4 + 1: hipLaunchKernelGGL((w8a8_split_kernel<1, 1>), grid, block, 0, stream, a); break;

@@ -80,6 +80,17 @@ def test_w8a8_matches_reference(T, d, rows, r):
         u.check(ys, restore, f"restore={restore}")
 
 
+# input groups shared out unevenly: over K ranges (103 in 26 26 26 25, 17 in 9 8, 25 in 9 9 7) and over the teams
+# of wavefronts inside a workgroup (26 in 7 7 7 5, 17 in 9 8), projections in several ranges, r up to 256
+@pytest.mark.parametrize("T,d,rows,r", [(40, 13184, [130, 5], 24), (64, 16384, [272], 256), (33, 16384, [1024, 8], 0),
+                                        (128, 2176, [17000], 40), (66, 2048, [16500, 3], 200), (300, 2176, [5000], 64),
+                                        (200, 3200, [600, 30], 200), (500, 16384, [140], 8), (60, 4224, [9000], 72)])
+def test_w8a8_uneven_splits(T, d, rows, r):
+    u = Unit(T, d, rows, r, 3000 + T + d)
+    log(f"w8a8 uneven T={T} d={d} rows={rows} r={r}")
+    u.check(u.run(r > 0), r > 0, "uneven")
+
+
 @pytest.mark.parametrize("T,d,rows,r", [(2048, 512, [4096, 1000], 64), (2043, 384, [4096, 4090], 24),
                                         (1500, 256, [9000, 3001], 0), (1100, 640, [16400], 128)])
 def test_w8a8_large_grid(T, d, rows, r):
