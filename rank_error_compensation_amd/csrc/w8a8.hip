@@ -573,7 +573,7 @@ __global__ __launch_bounds__(64 * WM * WN * KH, 2) void w8a8_tile_kernel(const F
         step(v + 3, ic<3>{});
     }
     __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): no copy may land in LDS after this
-    __builtin_amdgcn_s_barrier();
+    __syncthreads();
     // Team kh finishes token tiles TE kh .. + TE - 1: the others' sums of them come through LDS, past the
     // first SB bytes of the stages (those are R's).
     if constexpr (KH > 1) {
@@ -723,7 +723,7 @@ __global__ __launch_bounds__(64 * WM * WN * KH, 2) void w8a8_tile_kernel(const F
     }
     // To memory through the wavefront's own part of the (finished) ring: [16 TT tokens][64 rows] fp16,
     // a token's eight 16-byte pieces p at p ^ (token % 8), then whole 128-byte lines.
-    __builtin_amdgcn_s_barrier();
+    __syncthreads();
     constexpr int kPart = 16 * TE * 128, kPer = SB / kPart;
     static_assert(NW * KH * kPart <= 4 * SB && SB % kPart == 0, "a part per wavefront");
     const int sel = wave_all / kPer;
