@@ -670,6 +670,14 @@ int validate_moe_workspace(const void* workspace, size_t bytes, size_t need) {
     return aligned(workspace, 256) ? GLOWQ_OK : GLOWQ_ERR_ALIGN;
 }
 
+// Whether two ranges of device memory share a byte.
+inline bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a != nullptr && b != nullptr && na > 0 && nb > 0 && x < y + nb && y < x + na;
+}
+
+inline size_t dtype_bytes(int32_t dtype) { return dtype == GLOWQ_DTYPE_F16 ? 2u : 4u; }
+
 inline int32_t* error_word(void* workspace) { return static_cast<int32_t*>(workspace) + kSyncError; }
 
 // Workgroups and pairs per workgroup of a routing-list call.
@@ -853,6 +861,11 @@ int glowq_moe_sort(const int32_t* expert_ids_dev, int64_t T, int64_t top_k, int3
         return GLOWQ_ERR_ALIGN;
     const int w = validate_moe_workspace(workspace, workspace_bytes, glowq_moe_sort_workspace_bytes(T, top_k, n_exp));
     if (w != GLOWQ_OK) return w;
+    const void* list[4] = {expert_ids_dev, row_token_dev, pair_row_dev, offsets_dev};
+    for (int i = 0; i < 4; ++i)
+        for (int j = i + 1; j < 4; ++j)
+            if (overlap(list[i], (size_t)(T * top_k) * 4u, list[j], j == 3 ? (size_t)(n_exp + 1) * 4u : (size_t)(T * top_k) * 4u))
+                return GLOWQ_ERR_INVALID_ARG;
     int64_t blocks, chunk;
     sort_plan(T * top_k, blocks, chunk);
     SortArgs a;
@@ -875,11 +888,12 @@ int glowq_moe_dispatch(const void* x, int64_t T, int64_t d, int32_t dtype, const
     const int v = validate_rows(T, 1, n_rows, d, dtype);
     if (v != GLOWQ_OK) return v;
     if (n_rows == 0) return GLOWQ_OK;
-    if (T < 1) return GLOWQ_ERR_SHAPE;
-    if (x == nullptr || row_token_dev == nullptr || rows == nullptr) return GLOWQ_ERR_INVALID_ARG;
+    if ((T > 0 && x == nullptr) || row_token_dev == nullptr || rows == nullptr) return GLOWQ_ERR_INVALID_ARG;
     if (!aligned(x, 16) || !aligned(row_token_dev, 4) || !aligned(rows, 16)) return GLOWQ_ERR_ALIGN;
     const int w = validate_moe_workspace(workspace, workspace_bytes, kWsHeader);
     if (w != GLOWQ_OK) return w;
+    const size_t row_bytes = (size_t)d * dtype_bytes(dtype);
+    if (overlap(rows, n_rows * row_bytes, x, T * row_bytes)) return GLOWQ_ERR_INVALID_ARG;
     RowsArgs a;
     std::memset(&a, 0, sizeof(a));
     a.x = x;
@@ -905,6 +919,9 @@ int glowq_moe_combine(const void* rows, int64_t n_rows, const int32_t* pair_row_
         return GLOWQ_ERR_ALIGN;
     const int w = validate_moe_workspace(workspace, workspace_bytes, kWsHeader);
     if (w != GLOWQ_OK) return w;
+    const size_t row_bytes = (size_t)d * dtype_bytes(dtype);
+    if (overlap(y, T * row_bytes, rows, n_rows * row_bytes) || (add != y && overlap(y, T * row_bytes, add, T * row_bytes)))
+        return GLOWQ_ERR_INVALID_ARG;
     RowsArgs a;
     std::memset(&a, 0, sizeof(a));
     a.x = rows;
@@ -927,8 +944,8 @@ int glowq_moe_combine_backward(const void* dy, const void* rows, int64_t n_rows,
                                hipStream_t stream) {
     const int v = validate_rows(T, top_k, n_rows, d, dtype);
     if (v != GLOWQ_OK) return v;
-    if (T == 0) return GLOWQ_OK;
-    if (dy == nullptr || pair_row_dev == nullptr || d_weights_dev == nullptr ||
+    if (T == 0 && n_rows == 0) return GLOWQ_OK;
+    if ((T > 0 && (dy == nullptr || pair_row_dev == nullptr || d_weights_dev == nullptr)) ||
         (n_rows > 0 && (rows == nullptr || row_token_dev == nullptr || d_rows == nullptr)))
         return GLOWQ_ERR_INVALID_ARG;
     if (!aligned(dy, 16) || !aligned(rows, 16) || !aligned(pair_row_dev, 4) || !aligned(row_token_dev, 4) ||
@@ -936,6 +953,10 @@ int glowq_moe_combine_backward(const void* dy, const void* rows, int64_t n_rows,
         return GLOWQ_ERR_ALIGN;
     const int w = validate_moe_workspace(workspace, workspace_bytes, kWsHeader);
     if (w != GLOWQ_OK) return w;
+    const size_t row_bytes = (size_t)d * dtype_bytes(dtype);
+    if (overlap(d_rows, n_rows * row_bytes, dy, T * row_bytes) ||
+        (d_rows != rows && overlap(d_rows, n_rows * row_bytes, rows, n_rows * row_bytes)))
+        return GLOWQ_ERR_INVALID_ARG;
     RowsArgs a;
     std::memset(&a, 0, sizeof(a));
     a.x = dy;
@@ -961,6 +982,9 @@ int glowq_swiglu(const void* gate, const void* up, int64_t n, int32_t dtype, voi
     if (n == 0) return GLOWQ_OK;
     if (gate == nullptr || up == nullptr || h == nullptr) return GLOWQ_ERR_INVALID_ARG;
     if (!aligned(gate, 16) || !aligned(up, 16) || !aligned(h, 16)) return GLOWQ_ERR_ALIGN;
+    const size_t bytes = (size_t)n * dtype_bytes(dtype);
+    for (const void* in : {gate, up})
+        if (in != h && overlap(h, bytes, in, bytes)) return GLOWQ_ERR_INVALID_ARG;
     return launch_swiglu(gate, up, n, dtype, h, stream) == hipSuccess ? GLOWQ_OK : GLOWQ_ERR_HIP;
 }
 
@@ -974,6 +998,11 @@ int glowq_swiglu_backward(const void* dh, const void* gate, const void* up, int6
         return GLOWQ_ERR_INVALID_ARG;
     if (!aligned(dh, 16) || !aligned(gate, 16) || !aligned(up, 16) || !aligned(d_gate, 16) || !aligned(d_up, 16))
         return GLOWQ_ERR_ALIGN;
+    const size_t bytes = (size_t)n * dtype_bytes(dtype);
+    if (overlap(d_gate, bytes, d_up, bytes)) return GLOWQ_ERR_INVALID_ARG;
+    for (const void* in : {dh, gate, up})
+        if ((in != d_gate && overlap(d_gate, bytes, in, bytes)) || (in != d_up && overlap(d_up, bytes, in, bytes)))
+            return GLOWQ_ERR_INVALID_ARG;
     return launch_swiglu_backward(dh, gate, up, n, dtype, d_gate, d_up, stream) == hipSuccess ? GLOWQ_OK : GLOWQ_ERR_HIP;
 }
 

@@ -81,6 +81,19 @@ def test_gradients_against_differences():
     assert bool(((c.double() - num).abs() <= (D * G).abs() * 2 * R.GATE + 1e-10).all())
 
 
+@pytest.mark.parametrize("kind", ["f16", "f32"])
+def test_in_place(kind):
+    g = glowq()
+    gate, up, dh = (values((33, 21), kind, i) for i in range(3))
+    want, (dg, du) = g.swiglu(gate, up), g.swiglu_backward(dh, gate, up)
+    for i in range(2):
+        t = [gate.clone(), up.clone()]
+        assert torch.equal(g.swiglu(*t, out=t[i]), want)
+    t = [dh.clone(), gate.clone(), up.clone()]
+    a, b = g.swiglu_backward(*t, out=(t[1], t[2]))
+    assert torch.equal(a, dg) and torch.equal(b, du)
+
+
 def test_empty_streams_and_graph():
     g = glowq()
     e = torch.empty(0, 5, dtype=torch.float16, device="cuda")

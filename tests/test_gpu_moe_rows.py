@@ -186,6 +186,36 @@ def test_tail_rows_and_unnamed_rows():
     assert g.workspace_status(ws) == g.OK
 
 
+def test_no_tokens_but_rows():
+    """Padded row lists of a batch without tokens: every row zero, forward and backward."""
+    g = glowq()
+    ws = workspace()
+    tok = torch.full((300,), -1, dtype=torch.int32, device="cuda")
+    none, rows = torch.empty(0, 24, device="cuda"), torch.full((300, 24), 5.0, device="cuda")
+    got = g.moe_dispatch(none, tok, workspace=ws, out=rows.clone())
+    assert got.shape == (300, 24) and not got.any()
+    pr = torch.empty(0, 3, dtype=torch.int32, device="cuda")
+    dr, dw = g.moe_combine_backward(none, rows, pr, tok, None, workspace=ws, out=(rows.clone(), torch.empty(0, 3, device="cuda")))
+    assert not dr.any() and dw.shape == (0, 3)
+    assert g.workspace_status(ws) == g.OK
+
+
+@pytest.mark.parametrize("kind", ["f16", "f32"])
+def test_in_place(kind):
+    """y in add, d_rows in rows."""
+    g = glowq()
+    tok, pr, n = lists(40, 6, 9, 3)
+    ws = workspace()
+    rows, dy, w = randn((n, 50), kind, 1), randn((40, 50), kind, 2), torch.rand(40, 6).cuda()
+    want = g.moe_combine(rows, pr, w, add=dy, workspace=ws)
+    y = dy.clone()
+    assert torch.equal(g.moe_combine(rows, pr, w, add=y, workspace=ws, out=y), want)
+    dr, dw = g.moe_combine_backward(dy, rows, pr, tok, w, workspace=ws)
+    r = rows.clone()
+    a, b = g.moe_combine_backward(dy, r, pr, tok, w, workspace=ws, out=(r, torch.empty(40, 6, device="cuda")))
+    assert torch.equal(a, dr) and torch.equal(b, dw) and g.workspace_status(ws) == g.OK
+
+
 def test_bad_list_entries_are_skipped_and_reported():
     g = glowq()
     T, k, E, d = 30, 2, 5, 40

@@ -133,7 +133,7 @@ def rows_args(kw):
     return a
 
 
-@pytest.mark.parametrize("kw,status", ROWS + [(dict(T=0), g.ERR_SHAPE), (dict(n_rows=0, x=None), g.OK)])
+@pytest.mark.parametrize("kw,status", ROWS + [(dict(T=0, lst=None), g.ERR_INVALID_ARG), (dict(n_rows=0, x=None), g.OK)])
 def test_moe_dispatch_refusals(kw, status):
     a = rows_args(kw)
     assert g.lib().glowq_moe_dispatch(a["x"], a["T"], a["d"], a["dtype"], a["lst"], a["n_rows"], a["out"], a["ws"],
@@ -149,8 +149,8 @@ def test_moe_combine_refusals(kw, status):
                                      a["out"], a["ws"], a["n"], None) == status
 
 
-@pytest.mark.parametrize("kw,status", ROWS + [(dict(T=0, x=None), g.OK), (dict(k=0), g.ERR_SHAPE),
-                                              (dict(tok=None), g.ERR_INVALID_ARG), (dict(rows=None), g.ERR_INVALID_ARG),
+@pytest.mark.parametrize("kw,status", ROWS + [(dict(T=0, n_rows=0, x=None), g.OK), (dict(k=0), g.ERR_SHAPE),
+                                              (dict(T=0, out=None), g.ERR_INVALID_ARG), (dict(tok=None), g.ERR_INVALID_ARG), (dict(rows=None), g.ERR_INVALID_ARG),
                                               (dict(dw=None), g.ERR_INVALID_ARG), (dict(dw=FAKE + 2), g.ERR_ALIGN),
                                               (dict(rows=FAKE + 8), g.ERR_ALIGN)])
 def test_moe_combine_backward_refusals(kw, status):
@@ -172,6 +172,26 @@ def test_swiglu_refusals(kw, status):
     if a["n"]:
         assert L.glowq_swiglu_backward(None, FAKE, FAKE, 8, 1, FAKE, FAKE, None) == g.ERR_INVALID_ARG
         assert L.glowq_swiglu_backward(FAKE, FAKE, FAKE, 8, 1, FAKE, None, None) == g.ERR_INVALID_ARG
+
+
+FAR = [FAKE + (i << 20) for i in range(8)]  # addresses with room between them
+
+
+def test_overlapping_tensors_are_refused():
+    L, bad = g.lib(), g.ERR_INVALID_ARG
+    a, b, c, o, tok, ws, w, e = FAR
+    row = 16 * 2  # fp16 rows of 16 values
+    for x in (o, o + 7 * row, o - 3 * row):
+        assert L.glowq_moe_dispatch(x, 4, 16, 1, tok, 8, o, ws, HDR, None) == bad
+    for rows, add in ((o, None), (o - 7 * row, b), (a, o + row), (a, o - 3 * row)):
+        assert L.glowq_moe_combine(rows, 8, c, w, add, 4, 2, 16, 1, o, ws, HDR, None) == bad
+    for dy, rows in ((o, a), (o + 7 * row, a), (a, o + row), (a, o - row)):
+        assert L.glowq_moe_combine_backward(dy, rows, 8, c, tok, w, 4, 2, 16, 1, o, e, ws, HDR, None) == bad
+    for ids, off, t, p in ((a, b, a, o), (a, b, c, a + 28), (a, a + 28, c, o), (a, b, c, c + 16), (a, o + 4, c, o)):
+        assert L.glowq_moe_sort(ids, 4, 2, 3, off, t, p, ws, HDR, None) == bad
+    assert L.glowq_swiglu(a, b, 64, 1, a + 16, None) == bad and L.glowq_swiglu(a, b, 64, 1, b - 112, None) == bad
+    for dg, du in ((a + 16, o), (o, b + 16), (c - 112, o), (o, o), (o, o + 16)):
+        assert L.glowq_swiglu_backward(a, b, c, 64, 1, dg, du, None) == bad
 
 
 def test_python_checks_refuse_host_tensors():
