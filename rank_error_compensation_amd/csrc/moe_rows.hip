@@ -53,7 +53,7 @@ __device__ int bucket_scan(int v, int* wsum) {
     return base + incl - v;
 }
 
-// Counts of one chunk per bucket.  Launch-bound: 65536 pairs on 256 workgroups 2.6 us.
+// Counts of one chunk per bucket.  Launch-bound: 262144 pairs on 256 workgroups 2.6 us.
 __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(const SortArgs a) {
     __shared__ int hist[kBuckets];
     const int nb = a.n_exp + 1;
@@ -70,8 +70,9 @@ __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(const SortArgs
 // that rows of one expert keep the pairs' order: counters[wave][bucket] first count the piece, then
 // hold the next free row (expert start + earlier chunks + earlier wavefronts); 64 pairs at a time
 // take theirs, a lane's place among the lanes of its bucket found from ballots of the bucket's bits.
-// Bound by latency, not by its 12 bytes a pair: in one workgroup a token's four choices take 2.7 us; 65536
-// pairs over 60 experts on 256 workgroups, each of which adds up all workgroups' counts, 6.9 us.
+// Bound by latency, not by its 12 bytes a pair: in one workgroup a token's four choices take 2.6 us; 262144
+// pairs over 60 experts on 256 workgroups, each of which adds up all workgroups' counts, 6.8 us
+// (all of a thread's counts loaded at once: 0.4 us less there, 0.8 more at 16384 pairs).
 template <bool ONE>
 __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(const SortArgs a) {
     __shared__ int cnt[kSortWaves * kHistStride];
