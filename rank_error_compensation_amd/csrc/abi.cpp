@@ -525,10 +525,10 @@ constexpr int64_t kW8SmallT = 64;  // and, by the number of tiles, up to here
 inline int64_t w8_r_pad(int32_t r) { return ceil_div(r, 64) * 64; }
 inline size_t w8_r_bytes(int64_t T, int32_t r) { return round256((size_t)T * (size_t)w8_r_pad(r) * 2u); }
 // fp32 K ranges of the projection.  Up to kW8TinyT tokens ranges of 2048 inputs, at most 8; above, at most
-// 512 / blocks ranges of (16 or 32)-token blocks, so ranges times tokens stay within max(T, 16384).  The
+// 256 / blocks ranges of (16 or 32)-token blocks, so ranges times tokens stay within max(T, 8192).  The
 // bound, not the plan's own number, is reserved: a workspace for T tokens serves fewer, too.
 inline size_t w8_part_bytes(int64_t T, int32_t r) {
-    const int64_t rows = T <= kW8TinyT ? 8 * T : std::max<int64_t>(T, 16384);
+    const int64_t rows = T <= kW8TinyT ? 8 * T : std::max<int64_t>(T, 8192);
     return round256((size_t)rows * (size_t)w8_r_pad(r) * 4u);
 }
 

@@ -853,9 +853,13 @@ PrepPlan w8a8_prep_plan(int64_t T, int64_t d, int32_t r, bool small) {
     if (small) {  // one batch of loads per wavefront
         p.range = 32 * 8 * kPrepWaves;
     } else {
-        p.tt = T >= 1024 ? 2 : 1;
+        // 32-token blocks (half the reads of B) where 16-token ones are more than the GPU holds at once: the call on
+        // 128 rows at T = 512, d = 14336 33.2 us, 34.6 with 16; T = 1000, d = 8192 31.9 and 33.2; but T = 512, d = 4096
+        // 25.5 and 24.4, T = 300, d = 14336 32.1 and 31.3.  K ranges up to 256 workgroups (one a CU, the codes'
+        // beside them; 384: 38 us at T = 512, d = 14336, 512: 36).
+        p.tt = T >= 512 && T * d >= ((int64_t)1 << 22) ? 2 : 1;
         const int64_t blocks = ceil_div(T, 16 * p.tt) * ceil_div((int64_t)r, 64);
-        const int64_t want = std::max<int64_t>(1, 512 / blocks);
+        const int64_t want = std::max<int64_t>(1, 256 / blocks);
         p.range = (int)std::max<int64_t>(32 * 4 * kPrepWaves, ceil_div(ceil_div(d, want), 32) * 32);
     }
     p.range = std::min<int>(p.range, (int)d);
