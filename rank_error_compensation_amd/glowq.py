@@ -269,13 +269,14 @@ class QWeight:
                  "from_int8: int8 codes [n_out][k_in], fp32 scales [n_out]")
         _require(tuple(scales.shape) == (codes.shape[0],), ERR_SHAPE, "from_int8: one scale per row")
         n_out, k_in = (int(n) for n in codes.shape)
-        c, s = codes.to(device).contiguous(), scales.to(device).contiguous()
         L = lib()
         qb, zb = L.glowq_w8_q_bytes(n_out, k_in), L.glowq_w8_sz_bytes(n_out)
         if qb == 0 or zb == 0:
             raise GlowQError(ERR_SHAPE, "glowq_w8_q_bytes")
-        _require(c.is_cuda, ERR_INVALID_ARG, "from_int8: a GPU device")
-        with torch.cuda.device(c.device):
+        _require(torch.device(device).type == "cuda", ERR_INVALID_ARG, "from_int8: a GPU device")
+        # copies, allocations and the repack all on the one stream
+        with torch.cuda.device(device) if stream is None else torch.cuda.stream(stream):
+            c, s = codes.to(device).contiguous(), scales.to(device).contiguous()
             q_dev = torch.empty(qb, dtype=torch.uint8, device=c.device)
             sz_dev = torch.empty(zb, dtype=torch.uint8, device=c.device)
             flag = torch.empty(1, dtype=torch.int32, device=c.device)

@@ -92,7 +92,8 @@ def test_w8a8_uneven_splits(T, d, rows, r):
 
 
 @pytest.mark.parametrize("T,d,rows,r", [(2048, 512, [4096, 1000], 64), (2043, 384, [4096, 4090], 24),
-                                        (1500, 256, [9000, 3001], 0), (1100, 640, [16400], 128)])
+                                        (1500, 256, [9000, 3001], 0), (1100, 640, [16400], 128),
+                                        (70001, 128, [520], 8), (66000, 256, [20], 64)])
 def test_w8a8_large_grid(T, d, rows, r):
     """Grids of the large tiles, every token block: tokens sampled from each 64 against the reference."""
     u = Unit(T, d, rows, r, 7 + T)
@@ -102,6 +103,25 @@ def test_w8a8_large_grid(T, d, rows, r):
     sub.__dict__.update(u.__dict__)
     sub.x = u.x[some]
     sub.check([y[some.cuda()] for y in ys], r > 0, f"large T={T}")
+
+
+@pytest.mark.parametrize("T", [2, 40, 70])
+def test_w8a8_weights_past_four_gigabytes(T):
+    """270000 x 16384 codes: byte offsets of the last rows' blocks need more than 32 bits."""
+    g = glowq()
+    n, d, r = 270000, 16384, 8
+    gen = torch.Generator("cuda").manual_seed(T)
+    codes = torch.randint(-128, 128, (n, d), generator=gen, dtype=torch.int8, device="cuda")
+    scales = 0.001 + 0.002 * torch.rand(n, generator=gen, device="cuda")
+    x = torch.randn(T, d, generator=gen, device="cuda").half()
+    b = (torch.randn(r, d, generator=gen, device="cuda") / d ** 0.5).half()
+    a = (0.3 * torch.randn(n, r, generator=gen, device="cuda")).half()
+    w = g.QWeight.from_int8(codes, scales)
+    log(f"w8a8 past 4 GB T={T}")
+    y, = g.group_forward_w8a8(x, [w], b, [a], r)
+    some = torch.tensor([0, 1, 131071, 131072, 262143, 262144, 262159, 269990, n - 1], device="cuda")
+    ref, bound = R.w8a8(x.cpu(), [codes[some].cpu()], [scales[some].cpu()], b.cpu(), [a[some].cpu()], True)
+    R.within(y[:, some], ref[0], bound[0], "far rows")
 
 
 def test_w8a8_largest_sums_are_exact():
@@ -164,6 +184,19 @@ def test_w8a8_tokens_do_not_depend_on_the_batch(T):
     full = u.run(False)[0]
     part = u.run(False, x=u.x.cuda()[:T].contiguous())[0]
     assert torch.equal(part, full[:T])
+
+
+def test_w8a8_repack_on_another_stream():
+    """Transposed codes: their dense copy and the repack both on the given stream."""
+    g = glowq()
+    u = Unit(3, 4096, [2048], 0, 21)
+    s = torch.cuda.Stream()
+    codes, scales = u.codes[0].t().contiguous().cuda().t(), u.scales[0].cuda()
+    s.wait_stream(torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    for _ in range(3):
+        w = g.QWeight.from_int8(codes, scales, stream=s)
+        assert torch.equal(w.q, u.w[0].q) and torch.equal(w.sz[: 4 * 2048], u.w[0].sz[: 4 * 2048])
 
 
 def test_w8a8_repack_rejects_non_finite_scales():
