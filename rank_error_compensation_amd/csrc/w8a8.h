@@ -9,7 +9,8 @@ constexpr int kFmtInt8 = 4;        // GLOWQ_FMT_INT8_CHANNEL
 constexpr int kW8Block = 2048;     // bytes of one 16-row x 128-input weight block
 constexpr int kW8Waves = 8;        // wavefronts that split the input groups of a small tile
 // Tiles by ForwardArgs::tile_tt x tile_rr (16-token and 16-row tiles per workgroup): 8 x 16 and 8 x 8 on four
-// wavefronts, 4 x 8 on two, times ForwardArgs::dec_ks teams; rr = 1, 2 is the small form, whose wavefronts split the input groups.
+// wavefronts, 4 x 8 on two, times ForwardArgs::dec_ks teams; rr = 1, 2 is the small form, whose wavefronts split the
+// input groups.
 constexpr int64_t kW8MaxD = 16384; // a token's row in the quantiser's registers; int32 sums exact
 
 // Launch shape of a call.
