@@ -588,7 +588,8 @@ def group_forward_w8a8(x: torch.Tensor, weights: Sequence[QWeight], b: Optional[
 @dataclass
 class MoeModule:
     """One module (gate, up or down) of every expert, stacked: expert e's device layout at
-    e * q_bytes / e * sz_bytes, its left factor a[e] fp16 [n_out][r]."""
+    e * q_bytes / e * sz_bytes, its left factor a[e] fp16 [n_out][r].  INT4 weights of one shape:
+    the experts' product knows no other layout, and takes expert e's place from these sizes."""
     q: torch.Tensor
     sz: torch.Tensor
     a: Optional[torch.Tensor]   # fp16 [n_exp][n_out][r]
@@ -597,6 +598,11 @@ class MoeModule:
 
     @staticmethod
     def stack(weights: Sequence[QWeight], a: Optional[Sequence[torch.Tensor]]) -> "MoeModule":
+        _require(len(weights) > 0, ERR_SHAPE, "MoeModule.stack: a weight per expert")
+        for w in weights:
+            _require(w.fmt == FMT_INT4_G128, ERR_UNSUPPORTED, "MoeModule.stack: INT4 weights")
+            _require((w.n_out, w.k_in) == (weights[0].n_out, weights[0].k_in), ERR_SHAPE,
+                     "MoeModule.stack: weights of one shape")
         q = torch.cat([w.q for w in weights]).contiguous()
         sz = torch.cat([w.sz for w in weights]).contiguous()
         a_st = torch.stack(list(a)).contiguous() if a is not None else None
@@ -612,6 +618,11 @@ def moe_forward(x: torch.Tensor, n_exp: int, modules: Sequence[MoeModule], b: Op
                 workspace: Optional[torch.Tensor] = None, y: Optional[List[torch.Tensor]] = None,
                 stream=None) -> List[torch.Tensor]:
     """glowq_moe_forward: outputs y_i fp16 [n_rows][n_out_i] in routed-row order."""
+    L = lib()
+    for mm in modules:
+        _require(_bytes(mm.q) >= n_exp * L.glowq_q_bytes(mm.n_out, mm.k_in) and
+                 _bytes(mm.sz) >= n_exp * L.glowq_sz_bytes(mm.n_out, mm.k_in), ERR_SHAPE,
+                 "moe_forward: INT4 modules of n_exp experts")
     if y is None:
         y = [torch.empty(n_rows, mm.n_out, dtype=torch.float16, device=x.device) for mm in modules]
     if workspace is None:
@@ -620,9 +631,9 @@ def moe_forward(x: torch.Tensor, n_exp: int, modules: Sequence[MoeModule], b: Op
     mc = _arr(MoeModuleC, [MoeModuleC(mm.q.data_ptr(), mm.sz.data_ptr(),
                                       None if mm.a is None else mm.a.data_ptr(), yy.data_ptr(), mm.n_out, mm.k_in)
                            for mm, yy in zip(modules, y)])
-    check(lib().glowq_moe_forward(_ptr(x), x.shape[0], x.shape[1], n_exp, len(modules), mc, _ptr(b), share, r,
-                                  int(bool(restore)), _ptr(row_token), _ptr(offsets), n_rows, _ptr(workspace),
-                                  workspace.numel(), _stream(stream)), "glowq_moe_forward")
+    check(L.glowq_moe_forward(_ptr(x), x.shape[0], x.shape[1], n_exp, len(modules), mc, _ptr(b), share, r,
+                              int(bool(restore)), _ptr(row_token), _ptr(offsets), n_rows, _ptr(workspace),
+                              workspace.numel(), _stream(stream)), "glowq_moe_forward")
     return y
 
 

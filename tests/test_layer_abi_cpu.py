@@ -84,6 +84,66 @@ def test_other_forwards_refuse_int8_weights():
     assert L.glowq_dequant(ctypes.byref(wc[0]), FAKE, 0, None) == g.ERR_INVALID_ARG
 
 
+def test_every_other_entry_point_refuses_int8_weights():
+    L, big = g.lib(), 1 << 30
+    wc = (g.QWeightC * 1)(w8())
+    p = (ctypes.c_void_p * 1)(FAKE)
+    unit = (g.UnitC * 1)(g.UnitC(1, 1, FAKE, 4, 256, wc, FAKE, p, 8, 1, p))
+    for r in (0, 8):
+        assert L.glowq_solo_forward(FAKE, 4, 256, wc, FAKE, FAKE, r, 1, FAKE, big, FAKE, None) == g.ERR_INVALID_ARG
+        assert L.glowq_group_forward_static(FAKE, 4, 256, 1, wc, FAKE, p, r, 1, p, None) == g.ERR_INVALID_ARG
+        for f in (L.glowq_group_forward_w4a8, L.glowq_group_forward_mx8):
+            assert f(FAKE, 4, 256, 1, wc, FAKE, p, r, 1, FAKE, big, p, None) == g.ERR_INVALID_ARG
+        assert L.glowq_layerwise_forward(FAKE, 4, 256, 1, wc, p, p, r, 1, FAKE, big, p, None) == g.ERR_INVALID_ARG
+    assert L.glowq_path_forward(unit, 1, FAKE, big, None) == g.ERR_INVALID_ARG
+    assert L.glowq_ner_sums(FAKE, wc, FAKE, big, FAKE, None) == g.ERR_UNSUPPORTED
+    wp = ctypes.cast(p, ctypes.POINTER(ctypes.c_void_p))
+    assert L.glowq_ner_sums_batch(1, wp, wc, FAKE, big, FAKE, None) == g.ERR_UNSUPPORTED
+
+
+def host_weight(fmt, n_out=32, k_in=256):
+    """A weight with buffers of its format's sizes (the experts' product takes INT4 alone)."""
+    L = g.lib()
+    if fmt == g.FMT_INT8_CHANNEL:
+        q, z = L.glowq_w8_q_bytes(n_out, k_in), L.glowq_w8_sz_bytes(n_out)
+    else:
+        q, z = L.glowq_q_bytes(n_out, k_in), L.glowq_sz_bytes(n_out, k_in)
+    return g.QWeight(torch.zeros(q, dtype=torch.uint8), torch.zeros(z, dtype=torch.uint8), n_out, k_in, fmt)
+
+
+@pytest.mark.parametrize("fmts", [[g.FMT_INT8_CHANNEL] * 2, [g.FMT_INT4_G128, g.FMT_INT8_CHANNEL],
+                                  [g.FMT_MXFP4] * 2, [g.FMT_MXFP6_E2M3], [g.FMT_INT4_G128, g.FMT_MXFP6_E3M2]])
+def test_stacked_experts_refuse_other_formats(fmts):
+    with pytest.raises(g.GlowQError) as e:
+        g.MoeModule.stack([host_weight(f) for f in fmts], None)
+    assert e.value.status == g.ERR_UNSUPPORTED
+
+
+def test_stacked_experts_refuse_mixed_shapes_and_none():
+    for ws in ([], [host_weight(0), host_weight(0, 48)], [host_weight(0), host_weight(0, 32, 384)]):
+        with pytest.raises(g.GlowQError) as e:
+            g.MoeModule.stack(ws, None)
+        assert e.value.status == g.ERR_SHAPE
+    m = g.MoeModule.stack([host_weight(0), host_weight(0)], None)
+    assert m.n_out == 32 and m.k_in == 256 and m.q.numel() == 2 * g.lib().glowq_q_bytes(32, 256)
+
+
+@pytest.mark.parametrize("case", ["int8 scales", "short codes", "fewer experts"])
+def test_moe_forward_refuses_modules_smaller_than_their_experts(case):
+    """Buffers that do not hold n_exp INT4 modules are never handed to the kernels."""
+    m = g.MoeModule.stack([host_weight(0), host_weight(0)], None)
+    if case == "int8 scales":
+        w = host_weight(g.FMT_INT8_CHANNEL)
+        m = g.MoeModule(torch.cat([w.q, w.q]), torch.cat([w.sz, w.sz]), None, 32, 256)
+    elif case == "short codes":
+        m = g.MoeModule(m.q[:-1], m.sz, None, 32, 256)
+    x, off = torch.zeros(2, 256, dtype=torch.float16), torch.zeros(4, dtype=torch.int32)
+    with pytest.raises(g.GlowQError) as e:
+        g.moe_forward(x, 3 if case == "fewer experts" else 2, [m], None, g.MOE_SHARE_EXPERT, 0, False, None, off, 2,
+                      workspace=torch.zeros(HDR, dtype=torch.uint8), stream=type("S", (), {"cuda_stream": 0}))
+    assert e.value.status == g.ERR_SHAPE
+
+
 @pytest.mark.parametrize("kw,status", [
     (dict(codes=None), g.ERR_INVALID_ARG), (dict(scales=None), g.ERR_INVALID_ARG), (dict(flag=None), g.ERR_INVALID_ARG),
     (dict(n=0), g.ERR_SHAPE), (dict(k=100), g.ERR_SHAPE), (dict(k=16512), g.ERR_UNSUPPORTED),
