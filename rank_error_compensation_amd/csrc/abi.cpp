@@ -688,6 +688,45 @@ void sort_plan(int64_t n, int64_t& blocks, int64_t& chunk) {
     blocks = ceil_div(n, chunk);
 }
 
+// glowq_moe_combine_backward, and with `whole` glowq_moe_combine_backward_whole.
+int combine_backward(const void* dy, const void* rows, int64_t n_rows, const int32_t* pair_row_dev,
+                     const int32_t* row_token_dev, const float* weights_dev, int64_t T, int64_t top_k, int64_t d,
+                     int32_t dtype, void* d_rows, float* d_weights_dev, void* workspace, size_t workspace_bytes,
+                     bool whole, hipStream_t stream) {
+    const int v = validate_rows(T, top_k, n_rows, d, dtype);
+    if (v != GLOWQ_OK) return v;
+    if (T == 0 && n_rows == 0) return GLOWQ_OK;
+    if ((T > 0 && (dy == nullptr || pair_row_dev == nullptr || d_weights_dev == nullptr)) ||
+        (n_rows > 0 && (rows == nullptr || row_token_dev == nullptr || d_rows == nullptr)))
+        return GLOWQ_ERR_INVALID_ARG;
+    if (!aligned(dy, 16) || !aligned(rows, 16) || !aligned(pair_row_dev, 4) || !aligned(row_token_dev, 4) ||
+        !aligned(weights_dev, 4) || !aligned(d_rows, 16) || !aligned(d_weights_dev, 4))
+        return GLOWQ_ERR_ALIGN;
+    const int w = validate_moe_workspace(workspace, workspace_bytes, kWsHeader);
+    if (w != GLOWQ_OK) return w;
+    const size_t row_bytes = (size_t)d * dtype_bytes(dtype);
+    if (overlap(d_rows, n_rows * row_bytes, dy, T * row_bytes) ||
+        (d_rows != rows && overlap(d_rows, n_rows * row_bytes, rows, n_rows * row_bytes)))
+        return GLOWQ_ERR_INVALID_ARG;
+    RowsArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.x = dy;
+    a.rows = rows;
+    a.row_token = row_token_dev;
+    a.pair_row = pair_row_dev;
+    a.w = weights_dev;
+    a.out = d_rows;
+    a.dw = d_weights_dev;
+    a.T = (int32_t)T;
+    a.top_k = (int32_t)top_k;
+    a.n_rows = (int32_t)n_rows;
+    a.d = d;
+    a.dtype = dtype;
+    a.whole = whole ? 1 : 0;
+    a.err = error_word(workspace);
+    return launch_moe_combine_backward(a, stream) == hipSuccess ? GLOWQ_OK : GLOWQ_ERR_HIP;
+}
+
 }  // namespace
 
 extern "C" {
@@ -942,37 +981,16 @@ int glowq_moe_combine_backward(const void* dy, const void* rows, int64_t n_rows,
                                const int32_t* row_token_dev, const float* weights_dev, int64_t T, int64_t top_k, int64_t d,
                                int32_t dtype, void* d_rows, float* d_weights_dev, void* workspace, size_t workspace_bytes,
                                hipStream_t stream) {
-    const int v = validate_rows(T, top_k, n_rows, d, dtype);
-    if (v != GLOWQ_OK) return v;
-    if (T == 0 && n_rows == 0) return GLOWQ_OK;
-    if ((T > 0 && (dy == nullptr || pair_row_dev == nullptr || d_weights_dev == nullptr)) ||
-        (n_rows > 0 && (rows == nullptr || row_token_dev == nullptr || d_rows == nullptr)))
-        return GLOWQ_ERR_INVALID_ARG;
-    if (!aligned(dy, 16) || !aligned(rows, 16) || !aligned(pair_row_dev, 4) || !aligned(row_token_dev, 4) ||
-        !aligned(weights_dev, 4) || !aligned(d_rows, 16) || !aligned(d_weights_dev, 4))
-        return GLOWQ_ERR_ALIGN;
-    const int w = validate_moe_workspace(workspace, workspace_bytes, kWsHeader);
-    if (w != GLOWQ_OK) return w;
-    const size_t row_bytes = (size_t)d * dtype_bytes(dtype);
-    if (overlap(d_rows, n_rows * row_bytes, dy, T * row_bytes) ||
-        (d_rows != rows && overlap(d_rows, n_rows * row_bytes, rows, n_rows * row_bytes)))
-        return GLOWQ_ERR_INVALID_ARG;
-    RowsArgs a;
-    std::memset(&a, 0, sizeof(a));
-    a.x = dy;
-    a.rows = rows;
-    a.row_token = row_token_dev;
-    a.pair_row = pair_row_dev;
-    a.w = weights_dev;
-    a.out = d_rows;
-    a.dw = d_weights_dev;
-    a.T = (int32_t)T;
-    a.top_k = (int32_t)top_k;
-    a.n_rows = (int32_t)n_rows;
-    a.d = d;
-    a.dtype = dtype;
-    a.err = error_word(workspace);
-    return launch_moe_combine_backward(a, stream) == hipSuccess ? GLOWQ_OK : GLOWQ_ERR_HIP;
+    return combine_backward(dy, rows, n_rows, pair_row_dev, row_token_dev, weights_dev, T, top_k, d, dtype, d_rows,
+                            d_weights_dev, workspace, workspace_bytes, false, stream);
+}
+
+int glowq_moe_combine_backward_whole(const void* dy, const void* rows, int64_t n_rows, const int32_t* pair_row_dev,
+                                     const int32_t* row_token_dev, const float* weights_dev, int64_t T, int64_t top_k, int64_t d,
+                                     int32_t dtype, void* d_rows, float* d_weights_dev, void* workspace, size_t workspace_bytes,
+                                     hipStream_t stream) {
+    return combine_backward(dy, rows, n_rows, pair_row_dev, row_token_dev, weights_dev, T, top_k, d, dtype, d_rows,
+                            d_weights_dev, workspace, workspace_bytes, true, stream);
 }
 
 int glowq_swiglu(const void* gate, const void* up, int64_t n, int32_t dtype, void* h, hipStream_t stream) {

@@ -40,6 +40,7 @@ struct RowsArgs {
     int32_t T, top_k, n_rows;
     int64_t d;
     int32_t dtype;             // GLOWQ_DTYPE_*
+    int32_t whole;             // gradient: rows that no pair takes are zeroed
     int32_t* err;
 };
 hipError_t launch_moe_dispatch(const RowsArgs& a, hipStream_t stream);

@@ -285,13 +285,20 @@ __global__ __launch_bounds__(kRowsThreads) void combine_kernel(const RowsArgs a,
 }
 
 // Rows of token -1 (behind the last expert's) belong to no pair: their gradient is zero.  A token out of
-// range is reported here, since no pair need point at its row.
+// range is reported here, since no pair need point at its row.  With a.whole the rows that no choice of
+// their token takes are zeroed, too -- those that no wavefront of a token writes.
 template <typename S>
 __device__ void zero_free_rows(const RowsArgs& a, int64_t first) {
     const int64_t row = first + threadIdx.x;
     const int t = row < a.n_rows ? a.row_token[row] : 0;
-    if (row < a.n_rows && t != -1 && (t < 0 || t >= a.T)) raise_routing(a.err);
-    unsigned long long free_rows = __ballot(row < a.n_rows && t == -1);
+    const bool far = t < 0 || t >= a.T;
+    if (row < a.n_rows && far && t != -1) raise_routing(a.err);
+    bool unowned = t == -1;
+    if (a.whole && row < a.n_rows) {
+        unowned = true;
+        for (int j = 0; j < a.top_k; ++j) unowned &= far || a.pair_row[(int64_t)t * a.top_k + j] != row;
+    }
+    unsigned long long free_rows = __ballot(row < a.n_rows && unowned);
     const int lane = threadIdx.x & 63;
     const int64_t row0 = first + (threadIdx.x & ~63);
     while (free_rows != 0) {

@@ -98,6 +98,8 @@ EXPORTS = {
     "glowq_moe_combine": (ctypes.c_int, [_vp, _i64, _vp, _vp, _vp, _i64, _i64, _i64, _i32, _vp, _vp, _sz, _vp]),
     "glowq_moe_combine_backward": (ctypes.c_int, [_vp, _vp, _i64, _vp, _vp, _vp, _i64, _i64, _i64, _i32, _vp, _vp, _vp,
                                                   _sz, _vp]),
+    "glowq_moe_combine_backward_whole": (ctypes.c_int, [_vp, _vp, _i64, _vp, _vp, _vp, _i64, _i64, _i64, _i32, _vp, _vp,
+                                                        _vp, _sz, _vp]),
     "glowq_swiglu": (ctypes.c_int, [_vp, _vp, _i64, _i32, _vp, _vp]),
     "glowq_swiglu_backward": (ctypes.c_int, [_vp, _vp, _vp, _i64, _i32, _vp, _vp, _vp]),
     "glowq_moe_workspace_bytes": (_sz, [_i64, _i64, _i32, _i32]),
@@ -759,8 +761,10 @@ def moe_dispatch_backward(d_rows: torch.Tensor, pair_row: torch.Tensor, workspac
 def moe_combine_backward(dy: torch.Tensor, rows: torch.Tensor, pair_row: torch.Tensor, row_token: torch.Tensor,
                          weights: Optional[torch.Tensor], workspace: Optional[torch.Tensor] = None, out=None,
                          stream=None):
-    """glowq_moe_combine_backward: (d_rows [n_rows][d], d_weights fp32 [T][top_k]) for dy [T][d]; rows of
-    token -1 get zeros, rows that no pair takes are left as they were (`out` may hold the two tensors)."""
+    """Gradients of moe_combine: (d_rows [n_rows][d], d_weights fp32 [T][top_k]) for dy [T][d].  Every row of
+    fresh memory is written: rows of token -1 and rows that no pair takes get zeros
+    (glowq_moe_combine_backward_whole).  In the two tensors of `out` the latter are left as they were
+    (glowq_moe_combine_backward)."""
     what = "moe_combine_backward"
     dt = _row_dtype(what, rows)
     T, k = _pairs(what, pair_row, weights)
@@ -776,12 +780,12 @@ def moe_combine_backward(dy: torch.Tensor, rows: torch.Tensor, pair_row: torch.T
         raise GlowQError(ERR_INVALID_ARG, f"{what}: int32 list [n_rows]")
     _require(row_token.shape[0] == n, ERR_SHAPE, f"{what}: row_token [n_rows]")
     d_rows, d_w = out if out is not None else (None, None)
+    f = lib().glowq_moe_combine_backward_whole if d_rows is None else lib().glowq_moe_combine_backward
     d_rows = _new(d_rows, (n, d), rows.dtype, rows, what)
     d_w = _new(d_w, (T, k), torch.float32, rows, what)
     ws = _moe_ws(workspace, rows, _MOE_HEADER)
-    st = lib().glowq_moe_combine_backward(dy.data_ptr(), rows.data_ptr(), n, pair_row.data_ptr(), row_token.data_ptr(),
-                                          _addr(weights), T, k, d, dt, d_rows.data_ptr(), d_w.data_ptr(), ws.data_ptr(),
-                                          _bytes(ws), _current(rows))
+    st = f(dy.data_ptr(), rows.data_ptr(), n, pair_row.data_ptr(), row_token.data_ptr(), _addr(weights), T, k, d, dt,
+           d_rows.data_ptr(), d_w.data_ptr(), ws.data_ptr(), _bytes(ws), _current(rows))
     if st != OK:
         check(st, "glowq_moe_combine_backward")
     return d_rows, d_w

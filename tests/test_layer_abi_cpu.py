@@ -219,6 +219,17 @@ def test_moe_combine_backward_refusals(kw, status):
                                               a["d"], a["dtype"], a["out"], a["dw"], a["ws"], a["n"], None) == status
 
 
+@pytest.mark.parametrize("kw,status", ROWS + [(dict(T=0, n_rows=0, x=None), g.OK), (dict(k=0), g.ERR_SHAPE),
+                                              (dict(T=0, out=None), g.ERR_INVALID_ARG), (dict(tok=None), g.ERR_INVALID_ARG), (dict(rows=None), g.ERR_INVALID_ARG),
+                                              (dict(dw=None), g.ERR_INVALID_ARG), (dict(dw=FAKE + 2), g.ERR_ALIGN),
+                                              (dict(x=FAKE + 32, out=FAKE), g.ERR_INVALID_ARG)])
+def test_moe_combine_backward_whole_refusals(kw, status):
+    a = rows_args(kw)
+    assert g.lib().glowq_moe_combine_backward_whole(a["x"], a["rows"], a["n_rows"], a["lst"], a["tok"], a["w"], a["T"],
+                                                    a["k"], a["d"], a["dtype"], a["out"], a["dw"], a["ws"], a["n"],
+                                                    None) == status
+
+
 @pytest.mark.parametrize("kw,status", [
     (dict(dtype=2), g.ERR_INVALID_ARG), (dict(n=-1), g.ERR_SHAPE), (dict(n=(1 << 33) + 1), g.ERR_UNSUPPORTED),
     (dict(gate=None), g.ERR_INVALID_ARG), (dict(up=None), g.ERR_INVALID_ARG), (dict(h=None), g.ERR_INVALID_ARG),
