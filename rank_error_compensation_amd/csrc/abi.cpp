@@ -742,6 +742,7 @@ const char* glowq_status_string(int status) {
         case GLOWQ_ERR_HIP: return "GLOWQ_ERR_HIP: HIP runtime or launch failure";
         case GLOWQ_ERR_RANGE: return "GLOWQ_ERR_RANGE: value out of range (zero point, scale, or a matrix that is not positive semidefinite)";
         case GLOWQ_ERR_HANDOFF: return "GLOWQ_ERR_HANDOFF: a bounded wait for the projection expired; outputs since the last check are invalid";
+        case GLOWQ_ERR_ROUTING: return "GLOWQ_ERR_ROUTING: routing data out of range; the entries were clamped or skipped";
         default: return "GLOWQ_ERR_UNKNOWN";
     }
 }

@@ -422,7 +422,7 @@ def init_workspace(ws: torch.Tensor, stream=None) -> torch.Tensor:
 
 
 def workspace_status(ws: torch.Tensor, stream=None) -> int:
-    """glowq_workspace_status: synchronises, returns OK or ERR_HANDOFF and clears the word."""
+    """glowq_workspace_status: synchronises, returns OK, ERR_HANDOFF or ERR_ROUTING and clears the word."""
     st = int(lib().glowq_workspace_status(_ptr(ws), ws.numel(), _stream(stream)))
     if st not in (OK, ERR_HANDOFF, ERR_ROUTING):
         check(st, "glowq_workspace_status")

@@ -291,3 +291,8 @@ def test_python_checks_refuse_types_and_shapes(f):
     with pytest.raises(g.GlowQError) as e:
         f(torch.zeros(2, 16), torch.zeros(2, 2, dtype=torch.int32))
     assert e.value.status in (g.ERR_INVALID_ARG, g.ERR_SHAPE)
+
+
+def test_routing_status_has_its_name():
+    assert g.lib().glowq_status_string(g.ERR_ROUTING).startswith(b"GLOWQ_ERR_ROUTING")
+    assert "GLOWQ_ERR_ROUTING" in str(g.GlowQError(g.ERR_ROUTING, "glowq_moe_sort"))
