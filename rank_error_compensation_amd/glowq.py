@@ -640,15 +640,28 @@ def moe_forward(x: torch.Tensor, n_exp: int, modules: Sequence[MoeModule], b: Op
 
 
 # --------------------------------------------------------------------------- routed rows
+# Calls with a workspace are asynchronous and report list entries out of range through workspace_status; without
+# one they look themselves: they synchronise, raise ERR_ROUTING, and are refused under capture.
 def _bytes(ws: Optional[torch.Tensor]) -> int:
     return 0 if ws is None else ws.numel() * ws.element_size()
 
 
 def _moe_ws(workspace: Optional[torch.Tensor], like: torch.Tensor, n: int) -> torch.Tensor:
-    """The caller's workspace, or a fresh zero-filled one (its error word is then not looked at)."""
+    """The caller's workspace, or a fresh zero-filled one, whose error word _moe_done reads.  A captured call
+    has to bring its own: nothing but the program that replays it can look at the word."""
     if workspace is None:
+        _require(not torch.cuda.is_current_stream_capturing(), ERR_WORKSPACE, "a captured call takes a workspace")
         workspace = init_workspace(torch.empty(n, dtype=torch.uint8, device=like.device))
     return workspace
+
+
+def _moe_done(status: int, workspace: Optional[torch.Tensor], ws: torch.Tensor, what: str) -> None:
+    """Raises the call's status and, where it made its own workspace, list entries out of range
+    (synchronises the stream); with the caller's they wait for workspace_status."""
+    if status != OK:
+        check(status, what)
+    if workspace is None:
+        check(workspace_status(ws), what)
 
 
 def _new(out: Optional[torch.Tensor], shape, dtype, like: torch.Tensor, what: str) -> torch.Tensor:
@@ -686,7 +699,9 @@ def moe_sort_workspace_bytes(T: int, top_k: int, n_exp: int) -> int:
 
 def moe_sort(expert_ids: torch.Tensor, n_exp: int, workspace: Optional[torch.Tensor] = None, out=None, stream=None):
     """glowq_moe_sort: expert ids int32 [T][top_k] (-1: no expert) -> (offsets int32 [n_exp + 1], row_token
-    int32 [T top_k], pair_row int32 [T][top_k]); `out` may hold the three."""
+    int32 [T top_k], pair_row int32 [T][top_k]); `out` may hold the three.  Here and in the calls below
+    `workspace` None means a fresh one: the call then synchronises, raises ERR_ROUTING itself and cannot be
+    captured."""
     T, k = _pairs("moe_sort", expert_ids, None)
     _same_place("moe_sort", expert_ids, workspace, *(out or ()))
     ctx = _elsewhere(expert_ids, stream)
@@ -702,8 +717,7 @@ def moe_sort(expert_ids: torch.Tensor, n_exp: int, workspace: Optional[torch.Ten
         ws = _moe_ws(None, expert_ids, max(moe_sort_workspace_bytes(T, k, n_exp), _MOE_HEADER))
     st = lib().glowq_moe_sort(expert_ids.data_ptr(), T, k, n_exp, off.data_ptr(), tok.data_ptr(), pr.data_ptr(),
                               ws.data_ptr(), _bytes(ws), _current(expert_ids))
-    if st != OK:
-        check(st, "glowq_moe_sort")
+    _moe_done(st, workspace, ws, "glowq_moe_sort")
     return off, tok, pr
 
 
@@ -724,8 +738,7 @@ def moe_dispatch(x: torch.Tensor, row_token: torch.Tensor, workspace: Optional[t
     ws = _moe_ws(workspace, x, _MOE_HEADER)
     st = lib().glowq_moe_dispatch(x.data_ptr(), T, d, dt, row_token.data_ptr(), n, out.data_ptr(), ws.data_ptr(),
                                   _bytes(ws), _current(x))
-    if st != OK:
-        check(st, "glowq_moe_dispatch")
+    _moe_done(st, workspace, ws, "glowq_moe_dispatch")
     return out
 
 
@@ -747,8 +760,7 @@ def moe_combine(rows: torch.Tensor, pair_row: torch.Tensor, weights: Optional[to
     ws = _moe_ws(workspace, rows, _MOE_HEADER)
     st = lib().glowq_moe_combine(rows.data_ptr(), n, pair_row.data_ptr(), _addr(weights), _addr(add), T, k, d, dt,
                                  out.data_ptr(), ws.data_ptr(), _bytes(ws), _current(rows))
-    if st != OK:
-        check(st, "glowq_moe_combine")
+    _moe_done(st, workspace, ws, "glowq_moe_combine")
     return out
 
 
@@ -786,8 +798,7 @@ def moe_combine_backward(dy: torch.Tensor, rows: torch.Tensor, pair_row: torch.T
     ws = _moe_ws(workspace, rows, _MOE_HEADER)
     st = f(dy.data_ptr(), rows.data_ptr(), n, pair_row.data_ptr(), row_token.data_ptr(), _addr(weights), T, k, d, dt,
            d_rows.data_ptr(), d_w.data_ptr(), ws.data_ptr(), _bytes(ws), _current(rows))
-    if st != OK:
-        check(st, "glowq_moe_combine_backward")
+    _moe_done(st, workspace, ws, "glowq_moe_combine_backward")
     return d_rows, d_w
 
 

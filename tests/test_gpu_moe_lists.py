@@ -121,3 +121,70 @@ def test_combine_gradient_whole_in_place_and_captured():
     assert st == g.OK
     assert torch.equal(r2, want[0]) and torch.equal(dw, want[1])
     assert g.workspace_status(ws) == g.OK
+
+
+def far_lists():
+    """Calls without a workspace on lists with one entry out of range each, by name."""
+    g = glowq()
+    T, k, E, d = 30, 2, 5, 40
+    tok, pr, n = lists(T, k, E, 5)
+    ids = routing(T, k, E, 5).cuda()
+    x, rows, dy, w = randn((T, d), "f16", 1), randn((n, d), "f16", 2), randn((T, d), "f16", 3), torch.rand(T, k).cuda()
+    i2, t2, p2 = ids.clone(), tok.clone(), pr.clone()
+    i2[3, 1], t2[4], p2[5, 0] = E, T, n
+    return {"sort": lambda bad: g.moe_sort(i2 if bad else ids, E),
+            "dispatch": lambda bad: g.moe_dispatch(x, t2 if bad else tok),
+            "dispatch gradient": lambda bad: g.moe_dispatch_backward(rows, p2 if bad else pr),
+            "combine": lambda bad: g.moe_combine(rows, p2 if bad else pr, w),
+            "combine gradient": lambda bad: g.moe_combine_backward(dy, rows, p2 if bad else pr, tok, w)}
+
+
+def status_of(f):
+    """Status of a call.  The exception dies here: kept beside a graph (pytest.raises(...) as e) it would keep
+    the frame, and so the graph, until the collector runs -- perhaps within another test's capture, where a
+    graph must not be destroyed."""
+    g = glowq()
+    try:
+        f()
+    except g.GlowQError as err:
+        return err.status
+    return g.OK
+
+
+NAMES = ["sort", "dispatch", "dispatch gradient", "combine", "combine gradient"]
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_without_workspace_list_errors_are_raised(name):
+    """A call that makes its own workspace is the only one that can look at its error word."""
+    g = glowq()
+    f = far_lists()[name]
+    log(f"no workspace: {name}")
+    f(False)
+    assert status_of(lambda: f(True)) == g.ERR_ROUTING
+    f(False)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        assert status_of(lambda: f(True)) == g.ERR_ROUTING
+    torch.cuda.current_stream().wait_stream(s)
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_captured_calls_need_a_workspace(name):
+    """Under capture nobody could look at it: refused before anything is recorded, the capture goes on."""
+    g = glowq()
+    f = far_lists()[name]
+    one = torch.ones(8, device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(s):
+        with torch.cuda.graph(graph, stream=s):
+            status = status_of(lambda: f(False))
+            two = one + one
+    torch.cuda.current_stream().wait_stream(s)
+    assert status == g.ERR_WORKSPACE
+    graph.replay()
+    torch.cuda.synchronize()
+    assert bool((two == 2).all())
