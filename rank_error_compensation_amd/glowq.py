@@ -266,7 +266,7 @@ class QWeight:
     def from_int8(codes: torch.Tensor, scales: torch.Tensor, device=None, stream=None) -> "QWeight":
         """Repack 8-bit integer codes (int8 [n_out][k_in]) and per-row scales (fp32 [n_out]) into the
         device layout of group_forward_w8a8 (glowq_repack_w8; synchronises the stream)."""
-        device = device or torch.device("cuda")
+        device = torch.device("cuda" if device is None else device)
         _require(codes.dim() == 2 and codes.dtype == torch.int8 and scales.dtype == torch.float32, ERR_INVALID_ARG,
                  "from_int8: int8 codes [n_out][k_in], fp32 scales [n_out]")
         _require(tuple(scales.shape) == (codes.shape[0],), ERR_SHAPE, "from_int8: one scale per row")
@@ -275,7 +275,9 @@ class QWeight:
         qb, zb = L.glowq_w8_q_bytes(n_out, k_in), L.glowq_w8_sz_bytes(n_out)
         if qb == 0 or zb == 0:
             raise GlowQError(ERR_SHAPE, "glowq_w8_q_bytes")
-        _require(torch.device(device).type == "cuda", ERR_INVALID_ARG, "from_int8: a GPU device")
+        _require(device.type == "cuda", ERR_INVALID_ARG, "from_int8: a GPU device")
+        _require(stream is None or device.index is None or stream.device == device, ERR_INVALID_ARG,
+                 "from_int8: stream of another device")
         # copies, allocations and the repack all on the one stream
         with torch.cuda.device(device) if stream is None else torch.cuda.stream(stream):
             c, s = codes.to(device).contiguous(), scales.to(device).contiguous()

@@ -296,3 +296,13 @@ def test_python_checks_refuse_types_and_shapes(f):
 def test_routing_status_has_its_name():
     assert g.lib().glowq_status_string(g.ERR_ROUTING).startswith(b"GLOWQ_ERR_ROUTING")
     assert "GLOWQ_ERR_ROUTING" in str(g.GlowQError(g.ERR_ROUTING, "glowq_moe_sort"))
+
+
+def test_from_int8_refuses_a_stream_of_another_device():
+    """The repack would run on one device with the other's memory."""
+    stream = type("S", (), {"device": torch.device("cuda:1"), "cuda_stream": 0})
+    codes, scales = torch.zeros(16, 128, dtype=torch.int8), torch.ones(16)
+    for device in ("cuda:0", torch.device("cuda", 0)):
+        with pytest.raises(g.GlowQError) as e:
+            g.QWeight.from_int8(codes, scales, device=device, stream=stream)
+        assert e.value.status == g.ERR_INVALID_ARG
