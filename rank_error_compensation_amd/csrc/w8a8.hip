@@ -496,17 +496,25 @@ __global__ __launch_bounds__(64 * WM * WN * KH, 2) void w8a8_tile_kernel(const F
         __builtin_amdgcn_global_load_lds((const void*)(args.xscale + min(m0 + t0 + lane, T - 1)),
                                          (lds_void*)(tok_scale + t0), 4, 0, 0);
     }
+    // The waits of the ring count the loads behind a copy, so that no operand load may move in front of one
+    // (or a copy behind the operands of its group): the barriers keep the order under any scheduling.
     copy(0, st0);
+    __builtin_amdgcn_sched_barrier(0);
     wload(0, 0, 0);
     wload(0, 1, 1);
+    __builtin_amdgcn_sched_barrier(0);
     copy(1, st1);
+    __builtin_amdgcn_sched_barrier(0);
     wload(1, 0, 2);
     if constexpr (kDeep) {
         wload(1, 1, 3);
+        __builtin_amdgcn_sched_barrier(0);
         copy(2, st2);
+        __builtin_amdgcn_sched_barrier(0);
         wload(2, 0, 4);
         wload(2, 1, 5);
     }
+    __builtin_amdgcn_sched_barrier(0);
 
     // Group v in stage S = v % 4.  At the barrier its copies have landed: after them at most those of the
     // kAhead - 1 groups behind it and the operands in flight were issued.  The copies of v + kAhead go to a
@@ -522,6 +530,7 @@ __global__ __launch_bounds__(64 * WM * WN * KH, 2) void w8a8_tile_kernel(const F
         __builtin_amdgcn_s_barrier();
         if constexpr (kDeep) {
             copy(v + 3, nxt);
+            __builtin_amdgcn_sched_barrier(0);
             wload(v + 3, 0, (2 * S + 6) & 7);
             wload(v + 3, 1, (2 * S + 7) & 7);
             __builtin_amdgcn_sched_barrier(0);
@@ -546,7 +555,10 @@ __global__ __launch_bounds__(64 * WM * WN * KH, 2) void w8a8_tile_kernel(const F
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
             wload(v + 1 + m, 1 - m, (2 * S + m + 3) & 3);
-            if (m == 0) copy(v + 2, nxt);
+            if (m == 0) {
+                __builtin_amdgcn_sched_barrier(0);
+                copy(v + 2, nxt);
+            }
             __builtin_amdgcn_sched_barrier(0);
             if (v >= n_g) continue;
             const int at = m == 0 ? rofs0 : rofs1;
