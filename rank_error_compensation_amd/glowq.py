@@ -622,11 +622,10 @@ def moe_forward(x: torch.Tensor, n_exp: int, modules: Sequence[MoeModule], b: Op
                 workspace: Optional[torch.Tensor] = None, y: Optional[List[torch.Tensor]] = None,
                 stream=None) -> List[torch.Tensor]:
     """glowq_moe_forward: outputs y_i fp16 [n_rows][n_out_i] in routed-row order."""
-    L = lib()
     for mm in modules:
-        _require(_bytes(mm.q) >= n_exp * L.glowq_q_bytes(mm.n_out, mm.k_in) and
-                 _bytes(mm.sz) >= n_exp * L.glowq_sz_bytes(mm.n_out, mm.k_in), ERR_SHAPE,
-                 "moe_forward: INT4 modules of n_exp experts")
+        blocks = n_exp * (-(-mm.n_out // 16) * (mm.k_in // 128))  # 16 x 128 weights: 1024 bytes of codes, 64 of scales
+        if mm.q.nbytes < 1024 * blocks or mm.sz.nbytes < 64 * blocks:
+            raise GlowQError(ERR_SHAPE, "moe_forward: INT4 modules of n_exp experts")
     if y is None:
         y = [torch.empty(n_rows, mm.n_out, dtype=torch.float16, device=x.device) for mm in modules]
     if workspace is None:
@@ -635,9 +634,9 @@ def moe_forward(x: torch.Tensor, n_exp: int, modules: Sequence[MoeModule], b: Op
     mc = _arr(MoeModuleC, [MoeModuleC(mm.q.data_ptr(), mm.sz.data_ptr(),
                                       None if mm.a is None else mm.a.data_ptr(), yy.data_ptr(), mm.n_out, mm.k_in)
                            for mm, yy in zip(modules, y)])
-    check(L.glowq_moe_forward(_ptr(x), x.shape[0], x.shape[1], n_exp, len(modules), mc, _ptr(b), share, r,
-                              int(bool(restore)), _ptr(row_token), _ptr(offsets), n_rows, _ptr(workspace),
-                              workspace.numel(), _stream(stream)), "glowq_moe_forward")
+    check(lib().glowq_moe_forward(_ptr(x), x.shape[0], x.shape[1], n_exp, len(modules), mc, _ptr(b), share, r,
+                                  int(bool(restore)), _ptr(row_token), _ptr(offsets), n_rows, _ptr(workspace),
+                                  workspace.numel(), _stream(stream)), "glowq_moe_forward")
     return y
 
 

@@ -128,6 +128,16 @@ def test_stacked_experts_refuse_mixed_shapes_and_none():
     assert m.n_out == 32 and m.k_in == 256 and m.q.numel() == 2 * g.lib().glowq_q_bytes(32, 256)
 
 
+@pytest.mark.parametrize("n_out,k_in,n_exp", [(1, 128, 1), (17, 256, 3), (1408, 2048, 2)])
+def test_moe_forward_takes_modules_of_exactly_their_experts(n_out, k_in, n_exp):
+    """Buffers of the library's own sizes pass (a call without rows: nothing is launched)."""
+    m = g.MoeModule.stack([host_weight(0, n_out, k_in)] * n_exp, None)
+    x, off = torch.zeros(0, k_in, dtype=torch.float16), torch.zeros(n_exp + 1, dtype=torch.int32)
+    ys = g.moe_forward(x, n_exp, [m], None, g.MOE_SHARE_EXPERT, 0, False, None, off, 0,
+                       workspace=torch.zeros(HDR, dtype=torch.uint8), stream=type("S", (), {"cuda_stream": 0}))
+    assert ys[0].shape == (0, n_out)
+
+
 @pytest.mark.parametrize("case", ["int8 scales", "short codes", "fewer experts"])
 def test_moe_forward_refuses_modules_smaller_than_their_experts(case):
     """Buffers that do not hold n_exp INT4 modules are never handed to the kernels."""
