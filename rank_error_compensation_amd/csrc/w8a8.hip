@@ -865,11 +865,14 @@ PrepPlan w8a8_prep_plan(int64_t T, int64_t d, int32_t r, bool small) {
     if (small) {  // one batch of loads per wavefront
         p.range = 32 * 8 * kPrepWaves;
     } else {
-        // 32-token blocks (half the reads of B) where 16-token ones are more than the GPU holds at once: the call on
-        // 128 rows at T = 512, d = 14336 33.2 us, 34.6 with 16; T = 1000, d = 8192 31.9 and 33.2; but T = 512, d = 4096
-        // 25.5 and 24.4, T = 300, d = 14336 32.1 and 31.3.  K ranges up to 256 workgroups (one a CU, the codes'
-        // beside them; 384: 38 us at T = 512, d = 14336, 512: 36).
-        p.tt = T >= 512 && T * d >= ((int64_t)1 << 22) ? 2 : 1;
+        // 32-token blocks halve the reads of B: where 16-token ones would read 24 MB of it or more (T / 16 blocks of d r
+        // fp16 values) past the 128 tokens up to which a workgroup for each token's codes, which only the 16-token form
+        // has, weighs more.  The call on 128 rows, 32- and 16-token blocks, r = 64: T = 300, d = 14336 31.8 us and 31.6;
+        // T = 384, d = 8192 26.3 and 27.4; T = 768, d = 4096 26.0 and 26.9; T = 512, d = 14336 34.0 and 35.0, d = 4096
+        // 24.7 and 23.6; T = 300, d = 8192 25.6 and 24.5.  r = 256: T = 300, d = 4096 28.7 and 31.9; T = 384, d = 14336
+        // 47 and 61; T = 256, d = 4096 28.3 and 27.3; T = 128, d = 14336 37.1 and 35.2.  K ranges up to 256 workgroups
+        // (one a CU, the codes' beside them; 384: 38 us at T = 512, d = 14336, 512: 36).
+        p.tt = T > 128 && T * d * ceil_div((int64_t)r, 64) >= ((int64_t)3 << 20) ? 2 : 1;
         const int64_t blocks = ceil_div(T, 16 * p.tt) * ceil_div((int64_t)r, 64);
         const int64_t want = std::max<int64_t>(1, 256 / blocks);
         p.range = (int)std::max<int64_t>(32 * 4 * kPrepWaves, ceil_div(ceil_div(d, want), 32) * 32);
@@ -890,7 +893,7 @@ hipError_t launch_w8a8_prep(const PrepArgs& a, const PrepPlan& p, bool join, hip
     return hipGetLastError();
 }
 
-// SPLIT: the tile takes K ranges (only 128 x 128 does).
+// SPLIT: the tile takes K ranges (128 x 128 with two teams and 64 x 128 do).
 template <int WM, int WN, int TT, int KH, bool SPLIT>
 static hipError_t launch_tile(const ForwardArgs& a, const PrepArgs& p, hipStream_t stream) {
     // every XCD takes ceil(columns / 8) columns of every token block; those it has not return at once

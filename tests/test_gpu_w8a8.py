@@ -91,6 +91,16 @@ def test_w8a8_uneven_splits(T, d, rows, r):
     u.check(u.run(r > 0), r > 0, "uneven")
 
 
+# the projection's blocks of 16 and 32 tokens: both sides of the rule that chooses them, ragged tokens and ranks
+@pytest.mark.parametrize("T,d,rows,r", [(128, 16384, [48], 256), (129, 8192, [48], 256), (145, 16384, [33], 200),
+                                        (200, 15744, [40], 64), (199, 15744, [40], 64), (300, 10496, [16, 7], 8),
+                                        (299, 10496, [16, 7], 8), (640, 1280, [17], 256), (1537, 2048, [130], 72)])
+def test_w8a8_projection_blocks(T, d, rows, r):
+    u = Unit(T, d, rows, r, 5000 + T + d)
+    log(f"w8a8 projection blocks T={T} d={d} rows={rows} r={r}")
+    u.check(u.run(), True, "blocks")
+
+
 @pytest.mark.parametrize("T,d,rows,r", [(2048, 512, [4096, 1000], 64), (2043, 384, [4096, 4090], 24),
                                         (1500, 256, [9000, 3001], 0), (1100, 640, [16400], 128),
                                         (70001, 128, [520], 8), (66000, 256, [20], 64)])
