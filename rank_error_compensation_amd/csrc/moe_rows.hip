@@ -53,7 +53,7 @@ __device__ int bucket_scan(int v, int* wsum) {
     return base + incl - v;
 }
 
-// Counts of one chunk per bucket.  Launch-bound: 262144 pairs on 256 workgroups 2.6 us.
+// Counts of one chunk per bucket.  Launch-bound: 262144 pairs on 256 workgroups 2.5 us.
 __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(const SortArgs a) {
     __shared__ int hist[kBuckets];
     const int nb = a.n_exp + 1;
@@ -70,8 +70,8 @@ __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(const SortArgs
 // that rows of one expert keep the pairs' order: counters[wave][bucket] first count the piece, then
 // hold the next free row (expert start + earlier chunks + earlier wavefronts); 64 pairs at a time
 // take theirs, a lane's place among the lanes of its bucket found from ballots of the bucket's bits.
-// Bound by latency, not by its 12 bytes a pair: in one workgroup a token's four choices take 2.6 us; 262144
-// pairs over 60 experts on 256 workgroups, each of which adds up all workgroups' counts, 6.8 us
+// Bound by latency, not by its 12 bytes a pair: in one workgroup a token's four choices take 2.5 us; 262144
+// pairs over 60 experts on 256 workgroups, each of which adds up all workgroups' counts, 6.9 us
 // (all of a thread's counts loaded at once: 0.4 us less there, 0.8 more at 16384 pairs).
 template <bool ONE>
 __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(const SortArgs a) {
@@ -202,8 +202,10 @@ __global__ __launch_bounds__(kRowsThreads) void dispatch_kernel(const RowsArgs a
     }
 }
 
-// N values of type S as fp32: one 16-byte load (N S's to 16 bytes) or one value.  NT: past the caches,
-// for rows that outgrow them (kStreamBytes): cold, combine of 65536 x 2048 fp16 rows takes 69 us against
+// N values of type S as fp32: one 16-byte load (N S's to 16 bytes), or one value (N = 1) where rows are not
+// multiples of 16 bytes -- 2 or 4 bytes a lane, far from the memory's rate: combine of 4096 tokens x 4 x 2050
+// fp16 79 us, of 2048 columns 22; its gradients 79 and 30; fp32 72 and 37, 78 and 53.  NT: past the caches,
+// for 16-byte pieces of rows that outgrow them (kStreamBytes): cold, combine of 65536 x 2048 fp16 rows takes 69 us against
 // 77, its gradients for 8191 tokens (rows read so, written as usual) 58 against 71, the fp32 dispatch
 // gradient of 16384 rows 30 against 34.
 template <typename S, int N>
@@ -212,6 +214,7 @@ struct Pack {
 };
 template <typename S, int N, bool NT>
 __device__ __forceinline__ void load_f32(const S* p, float (&f)[N]) {
+    static_assert(N > 1 || !NT, "single values go through the caches");
     if constexpr (N > 1) {
         const u4 raw = NT ? __builtin_nontemporal_load(reinterpret_cast<const u4*>(p)) : *reinterpret_cast<const u4*>(p);
         const Pack<S, N> q = __builtin_bit_cast(Pack<S, N>, raw);
@@ -286,7 +289,9 @@ __global__ __launch_bounds__(kRowsThreads) void combine_kernel(const RowsArgs a,
 
 // Rows of token -1 (behind the last expert's) belong to no pair: their gradient is zero.  A token out of
 // range is reported here, since no pair need point at its row.  With a.whole the rows that no choice of
-// their token takes are zeroed, too -- those that no wavefront of a token writes.
+// their token takes are zeroed, too -- those that no wavefront of a token writes.  A wavefront clears its rows
+// one after another, a value a lane: with one in 16 of 32764 pairs dropped and the lists left at T top_k rows
+// of 2048 fp16 values the call takes 100 us, 60 with the lists cut to the rows in use.
 template <typename S>
 __device__ void zero_free_rows(const RowsArgs& a, int64_t first) {
     const int64_t row = first + threadIdx.x;
@@ -430,10 +435,13 @@ static hipError_t launch_combine_n(const RowsArgs& a, hipStream_t stream) {
     // few tokens: a token's columns over several workgroups
     const int64_t ny = blocks >= 256 ? 1 : std::min<int64_t>(ceil_div(chunks, tpr), 16);
     const dim3 grid((unsigned)blocks, (unsigned)ny);
-    if (stream_rows<S>(a))
-        hipLaunchKernelGGL((combine_kernel<S, N, true>), grid, dim3(kRowsThreads), 0, stream, a, (int)chunks, tpr);
-    else
-        hipLaunchKernelGGL((combine_kernel<S, N, false>), grid, dim3(kRowsThreads), 0, stream, a, (int)chunks, tpr);
+    if constexpr (N > 1) {
+        if (stream_rows<S>(a)) {
+            hipLaunchKernelGGL((combine_kernel<S, N, true>), grid, dim3(kRowsThreads), 0, stream, a, (int)chunks, tpr);
+            return hipGetLastError();
+        }
+    }
+    hipLaunchKernelGGL((combine_kernel<S, N, false>), grid, dim3(kRowsThreads), 0, stream, a, (int)chunks, tpr);
     return hipGetLastError();
 }
 
@@ -449,10 +457,15 @@ static hipError_t launch_combine_backward_n(const RowsArgs& a, hipStream_t strea
     const unsigned grid = (unsigned)(blocks + ceil_div(a.n_rows, kRowsThreads));
     const dim3 g(grid), block(kRowsThreads);
     const int chunks = (int)(a.d / N);
-    if (!stream_rows<S>(a)) hipLaunchKernelGGL((combine_backward_kernel<S, N, 0>), g, block, 0, stream, a, chunks, blocks);
-    else if (a.top_k > kChoices)
-        hipLaunchKernelGGL((combine_backward_kernel<S, N, 1>), g, block, 0, stream, a, chunks, blocks);
-    else hipLaunchKernelGGL((combine_backward_kernel<S, N, 2>), g, block, 0, stream, a, chunks, blocks);
+    if constexpr (N > 1) {
+        if (stream_rows<S>(a)) {
+            if (a.top_k > kChoices)
+                hipLaunchKernelGGL((combine_backward_kernel<S, N, 1>), g, block, 0, stream, a, chunks, blocks);
+            else hipLaunchKernelGGL((combine_backward_kernel<S, N, 2>), g, block, 0, stream, a, chunks, blocks);
+            return hipGetLastError();
+        }
+    }
+    hipLaunchKernelGGL((combine_backward_kernel<S, N, 0>), g, block, 0, stream, a, chunks, blocks);
     return hipGetLastError();
 }
 
