@@ -71,7 +71,7 @@ __global__ __launch_bounds__(256) void repack_w8_scales_kernel(const float* __re
 // projection R = X B^T, then those of the scales and codes (512 / TPT tokens each, a token's row in
 // registers between its maximum and its codes, so that X is read once for them).
 // What bounds it: up to some 40 tokens the launch and one load's latency (d = 4096, r = 64: 4.9 us for one token,
-// 6.4 us for 37); then memory (T = 2048: 16.8 MB of X and 8.9 MB of codes, scales and sums, 14.8 us; X again by the
+// 6.4 us for 37); then memory (T = 2048: 16.8 MB of X and 8.9 MB of codes, scales and sums, 15.2 us; X again by the
 // projection's workgroups, out of the caches).
 constexpr int kPrepThreads = 512;
 constexpr int kPrepWaves = kPrepThreads / 64;
@@ -260,7 +260,7 @@ __global__ __launch_bounds__(256) void prep_join_kernel(const PrepArgs a) {
 // Few tokens: the weights are the traffic and each call a few microseconds, so K is split inside the workgroup
 // to have all its loads in flight at once; one row tile a workgroup up to 16 tokens, for workgroups enough.
 // Bound by the latency of that one round of loads: one token, 4096 + 2 x 1024 rows <- 4096 (25 MB), warm in the
-// caches 5.6 us, waits 0.84 of the wavefronts' time; 37 tokens, 2 x 1408 <- 2048 7.4 us.
+// caches 5.7 us, waits 0.84 of the wavefronts' time; 37 tokens, 2 x 1408 <- 2048 7.3 us.
 template <int TT, int RR>
 __global__ __launch_bounds__(64 * kW8Waves) void w8a8_split_kernel(const ForwardArgs args) {
     constexpr int NW = kW8Waves, NT = TT * RR;
@@ -368,10 +368,15 @@ __global__ __launch_bounds__(64 * kW8Waves) void w8a8_split_kernel(const Forward
 // --------------------------------------------------------------------- large tiles
 // 16 TT WM tokens x 64 WN rows per workgroup: WM x WN wavefronts, each 16 TT tokens x 4 row tiles.
 // The token codes of an input group (128 bytes a token) go HBM/L2 -> LDS by the load unit into a ring
-// of four stages; a wavefront's weight operands come straight into registers, up to three groups ahead (the
-// WM wavefronts that share rows find them in the L1 cache), so that LDS carries only the codes: a code
-// byte read feeds 4 matrix-core steps.  In a stage, row r keeps its 16-byte piece c at position
-// c ^ f(r), f(r) = (r % 8) ^ ((r / 8) % 2): the 16 rows of an operand read fall in distinct banks.
+// of four stages; a wavefront's weight operands come straight into registers (the WM wavefronts that share
+// rows find them in the L1 cache), so that LDS carries only the codes: a code byte read feeds 4 matrix-core
+// steps.  Both are requested two or three groups ahead, but seldom stay in flight that long: where the paths
+// around a team's last, shorter turn meet, the compiler cannot count the operand loads and waits for all of
+// them, once in four groups with TT = 4, four times with TT = 8.
+// In a stage, row r keeps its 16-byte piece c at position c ^ f(r), f(r) = (r % 8) ^ ((r / 8) % 2).  That is
+// not free of bank conflicts: LDS serves a 16-byte read 16 lanes at a time, eight of one piece and eight of
+// the next, and rows 12 to 15 of a piece meet rows 4 to 7 of the next one, rows 0 to 3 its rows 8 to 11 --
+// two lanes a bank, conflicts for 0.47 to 0.49 of the access cycles.
 // Tokens past T read token T - 1 and row tiles past the module its last tile; neither is stored.
 //
 // Where the tiles do not fill the GPU, KH such teams of WM x WN wavefronts share a workgroup: each takes a part
@@ -380,11 +385,12 @@ __global__ __launch_bounds__(64 * kW8Waves) void w8a8_split_kernel(const Forward
 // workgroups writes.  With args.tile_ks > 1 the input groups are split over workgroups too: each writes its exact
 // int32 tile to the workspace, and w8a8_join_kernel adds them and finishes.
 //
-// Measured (r = 64): 128 x 256, T = 2048, 2 x 11008 rows <- 4096: 185 to 191 us, 2.0 Pop/s of int8 (a plain int8
-// product of 8192^3 by the vendor's library: 2.07).  Matrix cores busy 0.47 of the time, operand returns from the
-// L1/LDS path 0.70 (2.4 GB from the L2 caches, 13 TB/s; 0.39 GB from behind them): bound by feeding operands.  256 x 256
+// Measured (r = 64): 128 x 256, T = 2048, 2 x 11008 rows <- 4096: 175 to 193 us, 1.9 to 2.1 Pop/s of int8 (a plain
+// int8 product of 8192^3 by the vendor's library: 2.07).  Matrix cores busy 0.47 of the time, operand returns from the
+// L1/LDS path 0.70 (2.4 GB from the L2 caches, 13 TB/s; 0.40 GB from behind them).  Bound by the operands and the
+// waits for them: a timing copy without the loads took 139 us of the 190, one without LDS reads too 131.  256 x 256
 // on 4 or 8 wavefronts and 128 x 512 on 8 (half the weight traffic, one workgroup a CU) took 200 to 212 us.
-// 128 x 128 with two teams in two K ranges, T = 512, 4096 rows <- 14336: 45 us, 1.3 Pop/s; unsplit, T = 128,
+// 128 x 128 with two teams in two K ranges, T = 512, 4096 rows <- 14336: 42 us, 1.4 Pop/s; unsplit, T = 128,
 // 2 x 11008 <- 4096: 28 us (90 MB of weights from the last-level cache: 3.3 TB/s).  64 x 128 with four teams, T = 64,
 // the same rows: 23 us (3.9 TB/s).
 typedef __attribute__((address_space(3))) void lds_void;
@@ -471,7 +477,7 @@ __global__ __launch_bounds__(64 * WM * WN * KH, 2) void w8a8_tile_kernel(const F
             __builtin_amdgcn_global_load_lds((const void*)(base + xoff[i]), (lds_void*)(stg + kh * SB + 8 * (NC * wave + i) * 128),
                                              16, 0, 0);
     };
-    // Operands in flight: where registers allow (TT = 4), whole groups three ahead, group v in slot v % 4;
+    // Operands requested: where registers allow (TT = 4), whole groups three ahead, group v in slot v % 4;
     // else halves, half h = 2 v + m in slot h % 4, three halves ahead.
     constexpr bool kDeep = TT <= 4;
     constexpr int kAhead = kDeep ? 3 : 2;  // groups the code copies are ahead
