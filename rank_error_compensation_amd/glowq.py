@@ -656,13 +656,11 @@ def _moe_ws(workspace: Optional[torch.Tensor], like: torch.Tensor, n: int) -> to
     return workspace
 
 
-def _moe_done(status: int, workspace: Optional[torch.Tensor], ws: torch.Tensor, what: str) -> None:
-    """Raises the call's status and, where it made its own workspace, list entries out of range
-    (synchronises the stream); with the caller's they wait for workspace_status."""
-    if status != OK:
-        check(status, what)
-    if workspace is None:
-        check(workspace_status(ws), what)
+def _moe_done(status: int, ws: torch.Tensor, what: str) -> None:
+    """Raises a call's status or, after one with its own workspace, list entries out of range (synchronises
+    the stream); with the caller's workspace they wait for workspace_status."""
+    check(status, what)
+    check(workspace_status(ws), what)
 
 
 def _new(out: Optional[torch.Tensor], shape, dtype, like: torch.Tensor, what: str) -> torch.Tensor:
@@ -718,7 +716,8 @@ def moe_sort(expert_ids: torch.Tensor, n_exp: int, workspace: Optional[torch.Ten
         ws = _moe_ws(None, expert_ids, max(moe_sort_workspace_bytes(T, k, n_exp), _MOE_HEADER))
     st = lib().glowq_moe_sort(expert_ids.data_ptr(), T, k, n_exp, off.data_ptr(), tok.data_ptr(), pr.data_ptr(),
                               ws.data_ptr(), _bytes(ws), _current(expert_ids))
-    _moe_done(st, workspace, ws, "glowq_moe_sort")
+    if st != OK or workspace is None:
+        _moe_done(st, ws, "glowq_moe_sort")
     return off, tok, pr
 
 
@@ -739,7 +738,8 @@ def moe_dispatch(x: torch.Tensor, row_token: torch.Tensor, workspace: Optional[t
     ws = _moe_ws(workspace, x, _MOE_HEADER)
     st = lib().glowq_moe_dispatch(x.data_ptr(), T, d, dt, row_token.data_ptr(), n, out.data_ptr(), ws.data_ptr(),
                                   _bytes(ws), _current(x))
-    _moe_done(st, workspace, ws, "glowq_moe_dispatch")
+    if st != OK or workspace is None:
+        _moe_done(st, ws, "glowq_moe_dispatch")
     return out
 
 
@@ -761,7 +761,8 @@ def moe_combine(rows: torch.Tensor, pair_row: torch.Tensor, weights: Optional[to
     ws = _moe_ws(workspace, rows, _MOE_HEADER)
     st = lib().glowq_moe_combine(rows.data_ptr(), n, pair_row.data_ptr(), _addr(weights), _addr(add), T, k, d, dt,
                                  out.data_ptr(), ws.data_ptr(), _bytes(ws), _current(rows))
-    _moe_done(st, workspace, ws, "glowq_moe_combine")
+    if st != OK or workspace is None:
+        _moe_done(st, ws, "glowq_moe_combine")
     return out
 
 
@@ -799,7 +800,8 @@ def moe_combine_backward(dy: torch.Tensor, rows: torch.Tensor, pair_row: torch.T
     ws = _moe_ws(workspace, rows, _MOE_HEADER)
     st = f(dy.data_ptr(), rows.data_ptr(), n, pair_row.data_ptr(), row_token.data_ptr(), _addr(weights), T, k, d, dt,
            d_rows.data_ptr(), d_w.data_ptr(), ws.data_ptr(), _bytes(ws), _current(rows))
-    _moe_done(st, workspace, ws, "glowq_moe_combine_backward")
+    if st != OK or workspace is None:
+        _moe_done(st, ws, "glowq_moe_combine_backward")
     return d_rows, d_w
 
 
