@@ -5,6 +5,8 @@
 // baseline), then one launch computes every module's quantised product and adds R A_i^T.
 #include <hip/hip_runtime.h>
 
+#include <cfloat>
+#include <cmath>
 #include <cstdint>
 #include <algorithm>
 #include <cstring>
@@ -680,6 +682,22 @@ inline size_t dtype_bytes(int32_t dtype) { return dtype == GLOWQ_DTYPE_F16 ? 2u 
 
 inline int32_t* error_word(void* workspace) { return static_cast<int32_t*>(workspace) + kSyncError; }
 
+// Arguments shared by the router's calls.
+int validate_route(int64_t T, int32_t n_exp, int64_t top_k, int32_t dtype, int32_t score) {
+    if (dtype != GLOWQ_DTYPE_F16 && dtype != GLOWQ_DTYPE_F32) return GLOWQ_ERR_INVALID_ARG;
+    if (score != GLOWQ_SCORE_SOFTMAX && score != GLOWQ_SCORE_SIGMOID) return GLOWQ_ERR_INVALID_ARG;
+    if (T < 0 || n_exp < 1 || top_k < 1) return GLOWQ_ERR_SHAPE;
+    if (T > kMaxT || n_exp > GLOWQ_MOE_MAX_EXPERTS || top_k > kMoeMaxTopK) return GLOWQ_ERR_UNSUPPORTED;
+    return GLOWQ_OK;
+}
+
+int validate_norm(int64_t T, int64_t d, int32_t dtype) {
+    if (dtype != GLOWQ_DTYPE_F16 && dtype != GLOWQ_DTYPE_F32) return GLOWQ_ERR_INVALID_ARG;
+    if (T < 0 || d < 1) return GLOWQ_ERR_SHAPE;
+    if (T > kMaxT || d > kNormMaxD) return GLOWQ_ERR_UNSUPPORTED;
+    return GLOWQ_OK;
+}
+
 // Workgroups and pairs per workgroup of a routing-list call.
 void sort_plan(int64_t n, int64_t& blocks, int64_t& chunk) {
     blocks = 1, chunk = n;
@@ -1023,6 +1041,155 @@ int glowq_swiglu_backward(const void* dh, const void* gate, const void* up, int6
         if ((in != d_gate && overlap(d_gate, bytes, in, bytes)) || (in != d_up && overlap(d_up, bytes, in, bytes)))
             return GLOWQ_ERR_INVALID_ARG;
     return launch_swiglu_backward(dh, gate, up, n, dtype, d_gate, d_up, stream) == hipSuccess ? GLOWQ_OK : GLOWQ_ERR_HIP;
+}
+
+int glowq_moe_route(const void* logits, int64_t T, int32_t n_exp, int64_t top_k, int32_t dtype, int32_t score,
+                    const float* bias_dev, int32_t n_group, int32_t keep_groups, int32_t group_best, int32_t renorm,
+                    float scale, int32_t* expert_ids_dev, float* weights_dev, void* workspace, size_t workspace_bytes,
+                    hipStream_t stream) {
+    const int v = validate_route(T, n_exp, top_k, dtype, score);
+    if (v != GLOWQ_OK) return v;
+    if (top_k > n_exp) return GLOWQ_ERR_SHAPE;
+    if (n_group < 1 || n_exp % n_group != 0 || keep_groups < 1 || keep_groups > n_group) return GLOWQ_ERR_SHAPE;
+    if (n_group > GLOWQ_ROUTE_MAX_GROUPS) return GLOWQ_ERR_UNSUPPORTED;
+    if (group_best != 1 && group_best != 2) return GLOWQ_ERR_INVALID_ARG;
+    if (!(std::fabs(scale) <= FLT_MAX)) return GLOWQ_ERR_INVALID_ARG;
+    if (T == 0) return GLOWQ_OK;
+    if (logits == nullptr || expert_ids_dev == nullptr || weights_dev == nullptr) return GLOWQ_ERR_INVALID_ARG;
+    if (!aligned(logits, 16) || !aligned(bias_dev, 4) || !aligned(expert_ids_dev, 4) || !aligned(weights_dev, 4))
+        return GLOWQ_ERR_ALIGN;
+    const int w = validate_moe_workspace(workspace, workspace_bytes, kWsHeader);
+    if (w != GLOWQ_OK) return w;
+    const size_t in = (size_t)T * n_exp * dtype_bytes(dtype), out = (size_t)(T * top_k) * 4u;
+    if (overlap(expert_ids_dev, out, weights_dev, out)) return GLOWQ_ERR_INVALID_ARG;
+    for (const void* o : {(const void*)expert_ids_dev, (const void*)weights_dev})
+        if (overlap(o, out, logits, in) || overlap(o, out, bias_dev, (size_t)n_exp * 4u)) return GLOWQ_ERR_INVALID_ARG;
+    RouteArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.logits = logits;
+    a.bias = bias_dev;
+    a.T = (int32_t)T;
+    a.n_exp = n_exp;
+    a.top_k = (int32_t)top_k;
+    a.score = score;
+    a.n_group = n_group;
+    a.keep_groups = keep_groups;
+    a.group_best = group_best;
+    a.renorm = renorm != 0;
+    a.scale = scale;
+    a.ids = expert_ids_dev;
+    a.w = weights_dev;
+    a.err = error_word(workspace);
+    return launch_moe_route(a, dtype, stream) == hipSuccess ? GLOWQ_OK : GLOWQ_ERR_HIP;
+}
+
+int glowq_moe_route_backward(const float* d_weights_dev, const void* logits, const int32_t* expert_ids_dev, int64_t T,
+                             int32_t n_exp, int64_t top_k, int32_t dtype, int32_t score, int32_t renorm, float scale,
+                             void* d_logits, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    const int v = validate_route(T, n_exp, top_k, dtype, score);
+    if (v != GLOWQ_OK) return v;
+    if (!(std::fabs(scale) <= FLT_MAX)) return GLOWQ_ERR_INVALID_ARG;
+    if (T == 0) return GLOWQ_OK;
+    if (d_weights_dev == nullptr || logits == nullptr || expert_ids_dev == nullptr || d_logits == nullptr)
+        return GLOWQ_ERR_INVALID_ARG;
+    if (!aligned(logits, 16) || !aligned(d_weights_dev, 4) || !aligned(expert_ids_dev, 4) || !aligned(d_logits, 16))
+        return GLOWQ_ERR_ALIGN;
+    const int w = validate_moe_workspace(workspace, workspace_bytes, kWsHeader);
+    if (w != GLOWQ_OK) return w;
+    const size_t n = (size_t)T * n_exp * dtype_bytes(dtype), pairs = (size_t)(T * top_k) * 4u;
+    if ((d_logits != logits && overlap(d_logits, n, logits, n)) || overlap(d_logits, n, d_weights_dev, pairs) ||
+        overlap(d_logits, n, expert_ids_dev, pairs))
+        return GLOWQ_ERR_INVALID_ARG;
+    RouteArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.logits = logits;
+    a.T = (int32_t)T;
+    a.n_exp = n_exp;
+    a.top_k = (int32_t)top_k;
+    a.score = score;
+    a.renorm = renorm != 0;
+    a.scale = scale;
+    a.ids = const_cast<int32_t*>(expert_ids_dev);
+    a.w = const_cast<float*>(d_weights_dev);
+    a.out = d_logits;
+    a.err = error_word(workspace);
+    return launch_moe_route_backward(a, dtype, stream) == hipSuccess ? GLOWQ_OK : GLOWQ_ERR_HIP;
+}
+
+int glowq_layer_norm(const void* x, const void* weight, const void* bias, int64_t T, int64_t d, float eps, int32_t dtype,
+                     void* y, float* mean_dev, float* rstd_dev, hipStream_t stream) {
+    const int v = validate_norm(T, d, dtype);
+    if (v != GLOWQ_OK) return v;
+    if (!(eps >= 0.f && eps <= FLT_MAX)) return GLOWQ_ERR_INVALID_ARG;
+    if (T == 0) return GLOWQ_OK;
+    if (x == nullptr || y == nullptr) return GLOWQ_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || !aligned(weight, 16) || !aligned(bias, 16) || !aligned(y, 16) || !aligned(mean_dev, 4) ||
+        !aligned(rstd_dev, 4))
+        return GLOWQ_ERR_ALIGN;
+    const size_t row = (size_t)d * dtype_bytes(dtype), n = (size_t)T * row, stat = (size_t)T * 4u;
+    if ((y != x && overlap(y, n, x, n)) || overlap(mean_dev, stat, rstd_dev, stat)) return GLOWQ_ERR_INVALID_ARG;
+    for (const void* in : {weight, bias})
+        if (overlap(y, n, in, row) || overlap(mean_dev, stat, in, row) || overlap(rstd_dev, stat, in, row))
+            return GLOWQ_ERR_INVALID_ARG;
+    for (const void* s : {(const void*)mean_dev, (const void*)rstd_dev})
+        if (overlap(s, stat, x, n) || overlap(s, stat, y, n)) return GLOWQ_ERR_INVALID_ARG;
+    NormArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.x = x;
+    a.w = weight;
+    a.b = bias;
+    a.T = (int32_t)T;
+    a.d = (int32_t)d;
+    a.eps = eps;
+    a.out = y;
+    a.mean = mean_dev;
+    a.rstd = rstd_dev;
+    return launch_layer_norm(a, dtype, stream) == hipSuccess ? GLOWQ_OK : GLOWQ_ERR_HIP;
+}
+
+size_t glowq_layer_norm_workspace_bytes(int64_t T, int64_t d) {
+    if (T < 0 || T > kMaxT || d < 1 || d > kNormMaxD) return 0;
+    return round256((size_t)kNormParts * 2u * (size_t)d * 4u);
+}
+
+int glowq_layer_norm_backward(const void* dy, const void* x, const float* mean_dev, const float* rstd_dev,
+                              const void* weight, int64_t T, int64_t d, int32_t dtype, void* dx, float* d_weight_dev,
+                              float* d_bias_dev, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    const int v = validate_norm(T, d, dtype);
+    if (v != GLOWQ_OK) return v;
+    const bool sums = d_weight_dev != nullptr || d_bias_dev != nullptr;
+    if (T == 0 && !sums) return GLOWQ_OK;
+    if (T > 0 && (dy == nullptr || x == nullptr || mean_dev == nullptr || rstd_dev == nullptr || dx == nullptr))
+        return GLOWQ_ERR_INVALID_ARG;
+    if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(mean_dev, 4) || !aligned(rstd_dev, 4) || !aligned(weight, 16) ||
+        !aligned(dx, 16) || !aligned(d_weight_dev, 4) || !aligned(d_bias_dev, 4))
+        return GLOWQ_ERR_ALIGN;
+    if (sums) {
+        const int w = validate_moe_workspace(workspace, workspace_bytes, glowq_layer_norm_workspace_bytes(T, d));
+        if (w != GLOWQ_OK) return w;
+    }
+    const size_t row = (size_t)d * dtype_bytes(dtype), n = (size_t)T * row, stat = (size_t)T * 4u, col = (size_t)d * 4u;
+    if ((dx != x && overlap(dx, n, x, n)) || (dx != dy && overlap(dx, n, dy, n)) || overlap(dx, n, weight, row) ||
+        overlap(dx, n, mean_dev, stat) || overlap(dx, n, rstd_dev, stat) || overlap(d_weight_dev, col, d_bias_dev, col))
+        return GLOWQ_ERR_INVALID_ARG;
+    for (const void* s : {(const void*)d_weight_dev, (const void*)d_bias_dev})
+        if (overlap(s, col, dx, n) || overlap(s, col, x, n) || overlap(s, col, dy, n) || overlap(s, col, weight, row) ||
+            overlap(s, col, mean_dev, stat) || overlap(s, col, rstd_dev, stat))
+            return GLOWQ_ERR_INVALID_ARG;
+    NormArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.x = x;
+    a.w = weight;
+    a.dy = dy;
+    a.T = (int32_t)T;
+    a.d = (int32_t)d;
+    a.out = dx;
+    a.mean = const_cast<float*>(mean_dev);
+    a.rstd = const_cast<float*>(rstd_dev);
+    a.dw = d_weight_dev;
+    a.db = d_bias_dev;
+    a.part = sums ? static_cast<float*>(workspace) : nullptr;
+    return launch_layer_norm_backward(a, dtype, stream) == hipSuccess ? GLOWQ_OK : GLOWQ_ERR_HIP;
 }
 
 size_t glowq_w8_q_bytes(int64_t n_out, int64_t k_in) {

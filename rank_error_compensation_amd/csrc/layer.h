@@ -1,4 +1,4 @@
-// Launchers of the operators around the mixture-of-experts product (moe_rows.hip, gated.hip).
+// Launchers of the operators around the quantised products (moe_rows.hip, moe_route.hip, gated.hip, norm.hip).
 #pragma once
 
 #include "glowq_internal.h"
@@ -46,6 +46,38 @@ struct RowsArgs {
 hipError_t launch_moe_dispatch(const RowsArgs& a, hipStream_t stream);
 hipError_t launch_moe_combine(const RowsArgs& a, hipStream_t stream);
 hipError_t launch_moe_combine_backward(const RowsArgs& a, hipStream_t stream);
+
+// Router (moe_route.hip).
+struct RouteArgs {
+    const void* logits;   // [T][n_exp]
+    const float* bias;    // [n_exp] or nullptr
+    int32_t T, n_exp, top_k;
+    int32_t score;        // GLOWQ_SCORE_*
+    int32_t n_group, keep_groups, group_best;
+    int32_t renorm;
+    float scale;
+    int32_t* ids;         // [T][top_k]
+    float* w;             // [T][top_k]; gradient: d_weights
+    void* out;            // gradient: d_logits [T][n_exp]
+    int32_t* err;
+};
+hipError_t launch_moe_route(const RouteArgs& a, int32_t dtype, hipStream_t stream);
+hipError_t launch_moe_route_backward(const RouteArgs& a, int32_t dtype, hipStream_t stream);
+
+// Layer norm (norm.hip).
+constexpr int64_t kNormMaxD = 16384;  // a row in its threads' registers
+constexpr int kNormParts = 256;       // workgroups of a gradient launch, each with sums [2][d] of its own
+struct NormArgs {
+    const void *x, *w, *b, *dy;  // w, b may be nullptr
+    int32_t T, d;
+    float eps;
+    void* out;            // y; gradient: dx
+    float *mean, *rstd;   // [T]
+    float *dw, *db;       // [d], fp32
+    float* part;          // [kNormParts][2][d], nullptr where neither dw nor db is wanted
+};
+hipError_t launch_layer_norm(const NormArgs& a, int32_t dtype, hipStream_t stream);
+hipError_t launch_layer_norm_backward(const NormArgs& a, int32_t dtype, hipStream_t stream);
 
 hipError_t launch_swiglu(const void* gate, const void* up, int64_t n, int32_t dtype, void* h, hipStream_t stream);
 hipError_t launch_swiglu_backward(const void* dh, const void* gate, const void* up, int64_t n, int32_t dtype,

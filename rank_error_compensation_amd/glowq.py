@@ -38,6 +38,7 @@ FORMATS = {"int4": FMT_INT4_G128, "mxfp4": FMT_MXFP4, "mxfp6_e2m3": FMT_MXFP6_E2
 
 DTYPE_F32 = 0
 DTYPE_F16 = 1
+SCORES = {"softmax": 0, "sigmoid": 1}
 UNIT_GROUP = 0
 UNIT_SOLO = 1
 MAX_MODULES = 8
@@ -100,6 +101,13 @@ EXPORTS = {
                                                   _sz, _vp]),
     "glowq_moe_combine_backward_whole": (ctypes.c_int, [_vp, _vp, _i64, _vp, _vp, _vp, _i64, _i64, _i64, _i32, _vp, _vp,
                                                         _vp, _sz, _vp]),
+    "glowq_moe_route": (ctypes.c_int, [_vp, _i64, _i32, _i64, _i32, _i32, _vp, _i32, _i32, _i32, _i32, ctypes.c_float, _vp,
+                                       _vp, _vp, _sz, _vp]),
+    "glowq_moe_route_backward": (ctypes.c_int, [_vp, _vp, _vp, _i64, _i32, _i64, _i32, _i32, _i32, ctypes.c_float, _vp, _vp,
+                                                _sz, _vp]),
+    "glowq_layer_norm": (ctypes.c_int, [_vp, _vp, _vp, _i64, _i64, ctypes.c_float, _i32, _vp, _vp, _vp, _vp]),
+    "glowq_layer_norm_workspace_bytes": (_sz, [_i64, _i64]),
+    "glowq_layer_norm_backward": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i32, _vp, _vp, _vp, _vp, _sz, _vp]),
     "glowq_swiglu": (ctypes.c_int, [_vp, _vp, _i64, _i32, _vp, _vp]),
     "glowq_swiglu_backward": (ctypes.c_int, [_vp, _vp, _vp, _i64, _i32, _vp, _vp, _vp]),
     "glowq_moe_workspace_bytes": (_sz, [_i64, _i64, _i32, _i32]),
@@ -803,6 +811,136 @@ def moe_combine_backward(dy: torch.Tensor, rows: torch.Tensor, pair_row: torch.T
     if st != OK or workspace is None:
         _moe_done(st, ws, "glowq_moe_combine_backward")
     return d_rows, d_w
+
+
+# --------------------------------------------------------------------------- router
+def _score(what: str, score: str) -> int:
+    code = SCORES.get(score)
+    if code is None:
+        raise GlowQError(ERR_INVALID_ARG, f"{what}: score one of {sorted(SCORES)}")
+    return code
+
+
+def moe_route(logits: torch.Tensor, top_k: int, score: str = "softmax", bias: Optional[torch.Tensor] = None, n_group: int = 1,
+              keep_groups: int = 1, group_best: int = 1, renorm: bool = True, scale: float = 1.0,
+              workspace: Optional[torch.Tensor] = None, out=None, stream=None):
+    """glowq_moe_route: router logits [T][n_exp] -> (ids int32 [T][top_k], weights fp32 [T][top_k]) as moe_sort and
+    moe_combine take them; id -1 where a token's experts run out (logits of -inf are out).  bias fp32 [n_exp] decides,
+    with the scores, which experts are chosen, and is in no weight.  `out` may hold the two."""
+    what = "moe_route"
+    dt = _row_dtype(what, logits)
+    code = _score(what, score)
+    _same_place(what, logits, bias, workspace, *(out or ()))
+    ctx = _elsewhere(logits, stream)
+    if ctx is not None:
+        with ctx:
+            return moe_route(logits, top_k, score, bias, n_group, keep_groups, group_best, renorm, scale, workspace, out)
+    T, n_exp = logits.shape
+    _require(top_k >= 1, ERR_SHAPE, f"{what}: top_k >= 1")
+    if bias is not None and (bias.dtype != torch.float32 or bias.shape != (n_exp,)):
+        raise GlowQError(ERR_SHAPE, f"{what}: bias fp32 [n_exp]")
+    ids, w = out if out is not None else (None, None)
+    ids = _new(ids, (T, top_k), torch.int32, logits, what)
+    w = _new(w, (T, top_k), torch.float32, logits, what)
+    ws = _moe_ws(workspace, logits, _MOE_HEADER)
+    st = lib().glowq_moe_route(logits.data_ptr(), T, n_exp, top_k, dt, code, _addr(bias), n_group, keep_groups, group_best,
+                               1 if renorm else 0, scale, ids.data_ptr(), w.data_ptr(), ws.data_ptr(), _bytes(ws),
+                               _current(logits))
+    if st != OK or workspace is None:
+        _moe_done(st, ws, "glowq_moe_route")
+    return ids, w
+
+
+def moe_route_backward(d_weights: torch.Tensor, logits: torch.Tensor, ids: torch.Tensor, score: str = "softmax",
+                       renorm: bool = True, scale: float = 1.0, workspace: Optional[torch.Tensor] = None,
+                       out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Gradient of moe_route's weights: d_logits [T][n_exp] for d_weights fp32 [T][top_k], the chosen ids held
+    (glowq_moe_route_backward)."""
+    what = "moe_route_backward"
+    dt = _row_dtype(what, logits)
+    code = _score(what, score)
+    T, k = _pairs(what, ids, d_weights)
+    _same_place(what, logits, d_weights, ids, workspace, out)
+    ctx = _elsewhere(logits, stream)
+    if ctx is not None:
+        with ctx:
+            return moe_route_backward(d_weights, logits, ids, score, renorm, scale, workspace, out)
+    if logits.shape[0] != T:
+        raise GlowQError(ERR_SHAPE, f"{what}: logits [T][n_exp]")
+    out = _new(out, logits.shape, logits.dtype, logits, what)
+    ws = _moe_ws(workspace, logits, _MOE_HEADER)
+    st = lib().glowq_moe_route_backward(d_weights.data_ptr(), logits.data_ptr(), ids.data_ptr(), T, logits.shape[1], k, dt, code,
+                                        1 if renorm else 0, scale, out.data_ptr(), ws.data_ptr(), _bytes(ws),
+                                        _current(logits))
+    if st != OK or workspace is None:
+        _moe_done(st, ws, "glowq_moe_route_backward")
+    return out
+
+
+# --------------------------------------------------------------------------- layer norm
+def _norm_rows(what: str, x: torch.Tensor, *columns) -> int:
+    dt = _row_dtype(what, x)
+    for t in columns:
+        if t is not None and (t.dtype != x.dtype or t.shape != x.shape[1:]):
+            raise GlowQError(ERR_SHAPE, f"{what}: weight and bias [d] of x's type")
+    return dt
+
+
+def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+               eps: float = 1e-5, out=None, stream=None):
+    """glowq_layer_norm: rows x [T][d] -> (y [T][d], mean fp32 [T], rstd fp32 [T]); `out` may hold the three."""
+    what = "layer_norm"
+    dt = _norm_rows(what, x, weight, bias)
+    _same_place(what, x, weight, bias, *(out or ()))
+    ctx = _elsewhere(x, stream)
+    if ctx is not None:
+        with ctx:
+            return layer_norm(x, weight, bias, eps, out)
+    T, d = x.shape
+    y, mean, rstd = out if out is not None else (None, None, None)
+    y = _new(y, (T, d), x.dtype, x, what)
+    mean = _new(mean, (T,), torch.float32, x, what)
+    rstd = _new(rstd, (T,), torch.float32, x, what)
+    st = lib().glowq_layer_norm(x.data_ptr(), _addr(weight), _addr(bias), T, d, eps, dt, y.data_ptr(), mean.data_ptr(),
+                                rstd.data_ptr(), _current(x))
+    if st != OK:
+        check(st, "glowq_layer_norm")
+    return y, mean, rstd
+
+
+def layer_norm_workspace_bytes(T: int, d: int) -> int:
+    return int(lib().glowq_layer_norm_workspace_bytes(T, d))
+
+
+def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
+                        weight: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, out=None, stream=None):
+    """Gradients of layer_norm for dy [T][d]: (dx [T][d], d_weight fp32 [d], d_bias fp32 [d]); mean and rstd are the
+    forward's.  `out` may hold the three."""
+    what = "layer_norm_backward"
+    dt = _norm_rows(what, x, weight)
+    _same_place(what, x, dy, mean, rstd, weight, workspace, *(out or ()))
+    ctx = _elsewhere(x, stream)
+    if ctx is not None:
+        with ctx:
+            return layer_norm_backward(dy, x, mean, rstd, weight, workspace, out)
+    T, d = x.shape
+    if dy.dtype != x.dtype or dy.shape != x.shape:
+        raise GlowQError(ERR_SHAPE, f"{what}: dy [T][d] of x's type")
+    for t in (mean, rstd):
+        if t.dtype != torch.float32 or t.shape != (T,):
+            raise GlowQError(ERR_SHAPE, f"{what}: mean and rstd fp32 [T]")
+    dx, dw, db = out if out is not None else (None, None, None)
+    dx = _new(dx, (T, d), x.dtype, x, what)
+    dw = _new(dw, (d,), torch.float32, x, what)
+    db = _new(db, (d,), torch.float32, x, what)
+    if workspace is None:
+        workspace = torch.empty(max(layer_norm_workspace_bytes(T, d), 256), dtype=torch.uint8, device=x.device)
+    st = lib().glowq_layer_norm_backward(dy.data_ptr(), x.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _addr(weight), T, d, dt,
+                                         dx.data_ptr(), dw.data_ptr(), db.data_ptr(), workspace.data_ptr(), _bytes(workspace),
+                                         _current(x))
+    if st != OK:
+        check(st, "glowq_layer_norm_backward")
+    return dx, dw, db
 
 
 # --------------------------------------------------------------------------- gated activation
