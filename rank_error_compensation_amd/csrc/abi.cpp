@@ -14,6 +14,7 @@
 #include <vector>
 
 #include "glowq.h"
+#include "fp8.h"
 #include "glowq_internal.h"
 #include "glowq_offline.h"
 #include "layer.h"
@@ -74,6 +75,7 @@ struct Call {
     bool w4a8;  // 8-bit activations (glowq_group_forward_w4a8)
     bool mx8;   // MXFP4 weights x MXFP8 activations (glowq_group_forward_mx8)
     bool w8a8;  // INT8 weights x 8-bit activations (glowq_group_forward_w8a8)
+    bool fp8;   // block-scaled e4m3 weights x e4m3 activations (glowq_group_forward_fp8)
 };
 
 int validate(const Call& c, void* workspace, size_t ws_bytes) {
@@ -90,7 +92,8 @@ int validate(const Call& c, void* workspace, size_t ws_bytes) {
     for (int i = 0; i < c.m; ++i) {
         const glowq_qweight& w = c.w[i];
         if (w.q == nullptr || w.sz == nullptr) return GLOWQ_ERR_INVALID_ARG;
-        if (w.format < GLOWQ_FMT_INT4_G128 || w.format > (c.w8a8 ? GLOWQ_FMT_INT8_CHANNEL : GLOWQ_FMT_MXFP6_E3M2) ||
+        if (w.format < GLOWQ_FMT_INT4_G128 ||
+            w.format > (c.fp8 ? GLOWQ_FMT_FP8_BLOCK : c.w8a8 ? GLOWQ_FMT_INT8_CHANNEL : GLOWQ_FMT_MXFP6_E3M2) ||
             w.reserved != 0)
             return GLOWQ_ERR_INVALID_ARG;
         if (w.format != c.w[0].format) return GLOWQ_ERR_UNSUPPORTED;  // one format per call
@@ -106,6 +109,7 @@ int validate(const Call& c, void* workspace, size_t ws_bytes) {
     if (c.w4a8 && (c.d > kW4a8MaxD || c.w[0].format != GLOWQ_FMT_INT4_G128)) return GLOWQ_ERR_UNSUPPORTED;
     if (c.mx8 && c.w[0].format == GLOWQ_FMT_INT4_G128) return GLOWQ_ERR_UNSUPPORTED;  // MX weights only
     if (c.w8a8 && (c.d > kW8MaxD || c.w[0].format != GLOWQ_FMT_INT8_CHANNEL)) return GLOWQ_ERR_UNSUPPORTED;
+    if (c.fp8 && (c.d > kFp8MaxD || c.w[0].format != GLOWQ_FMT_FP8_BLOCK)) return GLOWQ_ERR_UNSUPPORTED;
     if (c.correct) {
         if (c.a == nullptr || c.b == nullptr) return GLOWQ_ERR_INVALID_ARG;
         for (int i = 0; i < c.m; ++i)
@@ -122,6 +126,7 @@ int validate(const Call& c, void* workspace, size_t ws_bytes) {
         const size_t need = c.w4a8  ? glowq_w4a8_workspace_bytes(c.T, c.d, c.correct ? c.r : 0)
                             : c.mx8 ? glowq_mx8_workspace_bytes(c.T, c.d, c.correct ? c.r : 0)
                             : c.w8a8 ? glowq_w8a8_workspace_bytes(c.T, c.d, c.correct ? c.r : 0)
+                            : c.fp8 ? glowq_fp8_workspace_bytes(c.T, c.d, c.correct ? c.r : 0)
                                     : (c.correct ? glowq_workspace_bytes(c.T, c.r, c.n_proj) : 0);
         if (need > 0) {
             if (workspace == nullptr || ws_bytes < need) return GLOWQ_ERR_WORKSPACE;
@@ -418,6 +423,7 @@ Call make_group(const void* x, int64_t T, int64_t d, int32_t m, const glowq_qwei
     c.w4a8 = false;
     c.mx8 = false;
     c.w8a8 = false;
+    c.fp8 = false;
     return c;
 }
 
@@ -658,6 +664,98 @@ int run_w8a8(const Call& c, void* workspace, hipStream_t stream) {
     return launch_w8a8(f, pa, stream) == hipSuccess ? GLOWQ_OK : GLOWQ_ERR_HIP;
 }
 
+// Block-scaled e4m3 form.  Workspace: codes [T][d] | scales fp32 [T][gp] | for a correcting call the projection's
+// fp32 K ranges | fp16 projection.
+struct Fp8Space {
+    uint8_t* xq;
+    float* xs;
+    float* part;
+    _Float16* R;
+};
+inline size_t fp8_codes_bytes(int64_t T, int64_t d) {
+    return round256((size_t)T * (size_t)d) + round256((size_t)(T * fp8_scale_stride(d)) * 4u);
+}
+Fp8Space fp8_space(uint8_t* base, int64_t T, int64_t d, int32_t r) {
+    Fp8Space s;
+    s.xq = base;
+    s.xs = reinterpret_cast<float*>(base + round256((size_t)T * (size_t)d));
+    base += fp8_codes_bytes(T, d);
+    s.part = reinterpret_cast<float*>(base);
+    s.R = reinterpret_cast<_Float16*>(base + (r > 0 ? w8_part_bytes(T, r) : 0));
+    return s;
+}
+
+// 16-token and 16-row tiles per workgroup for `rows` rows of one input (an expert's on average).
+void choose_fp8_shape(int64_t rows, int32_t& tt, int32_t& rr) {
+    tt = rows <= 16 ? 1 : (rows <= 32 ? 2 : 4);
+    rr = rows <= 16 ? 1 : 2;
+}
+
+// Codes, scales and the projection of T tokens: f.xq, f.xs and f.R.  ranges: R stays as its fp32 K ranges.
+hipError_t fp8_prepare(const void* x, int64_t T, int64_t d, const void* b, int32_t r, const Fp8Space& s, bool small,
+                       bool ranges, Fp8Args& f, hipStream_t stream) {
+    const PrepPlan plan = w8a8_prep_plan(T, d, r, small);
+    Fp8PrepArgs p;
+    std::memset(&p, 0, sizeof(p));
+    p.x = static_cast<const _Float16*>(x);
+    p.b = static_cast<const _Float16*>(b);
+    p.T = (int32_t)T;
+    p.d = (int32_t)d;
+    p.r = r;
+    p.rp = r > 0 ? (int32_t)w8_r_pad(r) : 0;
+    p.range = plan.range;
+    p.ks = plan.ks;
+    p.gp = (int32_t)fp8_scale_stride(d);
+    p.xq = s.xq;
+    p.xs = s.xs;
+    if (r > 0) {
+        if (ranges || plan.ks > 1) {
+            p.part = s.part;
+            if ((size_t)plan.ks * (size_t)T * (size_t)p.rp * 4u > w8_part_bytes(T, r)) return hipErrorInvalidValue;
+        }
+        p.R = s.R;
+    }
+    f.xq = s.xq;
+    f.xs = s.xs;
+    f.gp = p.gp;
+    f.R = ranges ? static_cast<const void*>(s.part) : static_cast<const void*>(s.R);
+    f.r_ranges = ranges ? plan.ks : 0;
+    f.r_rows = (int32_t)T;
+    return launch_fp8_prep(p, plan.tt, plan.nj, !ranges, stream);
+}
+
+int run_fp8(const Call& c, void* workspace, hipStream_t stream) {
+    if (c.T == 0) return GLOWQ_OK;
+    const int32_t r = c.correct ? c.r : 0;
+    Fp8Args f;
+    std::memset(&f, 0, sizeof(f));
+    f.T = (int32_t)c.T;
+    f.d = (int32_t)c.d;
+    f.G = (int32_t)(c.d / kGroup);
+    f.n_mod = c.m;
+    f.r = r;
+    f.rp = r > 0 ? (int32_t)w8_r_pad(r) : 0;
+    choose_fp8_shape(c.T, f.tt, f.rr);
+    int64_t blocks = 0;
+    for (int i = 0; i < c.m; ++i) {
+        Fp8Module& M = f.mod[i];
+        M.q = static_cast<const uint8_t*>(c.w[i].q);
+        M.sz = static_cast<const float*>(c.w[i].sz);
+        M.a = c.correct ? static_cast<const _Float16*>(c.a[i]) : nullptr;
+        M.y = static_cast<_Float16*>(c.y[i]);
+        M.n_out = (int32_t)c.w[i].n_out;
+        M.n_tiles16 = (int32_t)ceil_div(c.w[i].n_out, 16);
+        M.block_begin = (int32_t)blocks;
+        blocks += ceil_div(M.n_tiles16, f.rr);
+    }
+    f.row_blocks = (int32_t)blocks;
+    f.m_blocks = (int32_t)ceil_div(c.T, 16 * f.tt);
+    const Fp8Space s = fp8_space(static_cast<uint8_t*>(workspace), c.T, c.d, r);
+    if (fp8_prepare(c.x, c.T, c.d, c.correct ? c.b[0] : nullptr, r, s, c.T <= kW8SmallT, true, f, stream) != hipSuccess)
+        return GLOWQ_ERR_HIP;
+    return launch_fp8(f, blocks * f.m_blocks, stream) == hipSuccess ? GLOWQ_OK : GLOWQ_ERR_HIP;
+}
+
 // Arguments shared by the calls that move routed rows.
 int validate_rows(int64_t T, int64_t top_k, int64_t n_rows, int64_t d, int32_t dtype) {
     if (dtype != GLOWQ_DTYPE_F16 && dtype != GLOWQ_DTYPE_F32) return GLOWQ_ERR_INVALID_ARG;
@@ -681,6 +779,37 @@ inline bool overlap(const void* a, size_t na, const void* b, size_t nb) {
 inline size_t dtype_bytes(int32_t dtype) { return dtype == GLOWQ_DTYPE_F16 ? 2u : 4u; }
 
 inline int32_t* error_word(void* workspace) { return static_cast<int32_t*>(workspace) + kSyncError; }
+
+// Arguments shared by the experts' products; n_rows == 0 (a no-op) is valid whatever the pointers.
+int validate_moe(const void* x, int64_t T, int64_t d, int32_t n_exp, int32_t m, const glowq_moe_module* mods, const void* b,
+                 int32_t share, int32_t r, bool correct, const int32_t* row_token_dev, const int32_t* offsets_dev,
+                 int64_t n_rows) {
+    if (n_exp < 1 || n_exp > GLOWQ_MOE_MAX_EXPERTS || m < 1 || m > GLOWQ_MOE_MAX_MODULES) return GLOWQ_ERR_UNSUPPORTED;
+    if (share != GLOWQ_MOE_SHARE_EXPERT && share != GLOWQ_MOE_SHARE_ALL) return GLOWQ_ERR_INVALID_ARG;
+    if (n_rows < 0 || T < 0 || d < kGroup || d % kGroup != 0) return GLOWQ_ERR_SHAPE;
+    if (r < 0) return GLOWQ_ERR_SHAPE;
+    if (r > GLOWQ_MAX_RANK || r % 8 != 0) return GLOWQ_ERR_UNSUPPORTED;
+    if (n_rows > kMaxT * 8 || T > kMaxT || d > kMaxD || T * d > kMaxActElems) return GLOWQ_ERR_UNSUPPORTED;
+    if (mods == nullptr) return GLOWQ_ERR_INVALID_ARG;
+    if (n_rows == 0) return GLOWQ_OK;
+    if (x == nullptr || offsets_dev == nullptr) return GLOWQ_ERR_INVALID_ARG;
+    if (row_token_dev == nullptr && T != n_rows) return GLOWQ_ERR_SHAPE;
+    if (T < 1) return GLOWQ_ERR_SHAPE;
+    for (int i = 0; i < m; ++i) {
+        const glowq_moe_module& M = mods[i];
+        if (M.q == nullptr || M.sz == nullptr || M.y == nullptr) return GLOWQ_ERR_INVALID_ARG;
+        if (M.n_out < 1 || M.k_in != d) return GLOWQ_ERR_SHAPE;
+        if (M.n_out > kMaxRows) return GLOWQ_ERR_UNSUPPORTED;
+        if (!aligned(M.q, 16) || !aligned(M.sz, 16) || !aligned(M.y, 16)) return GLOWQ_ERR_ALIGN;
+        if (correct && (M.a == nullptr)) return GLOWQ_ERR_INVALID_ARG;
+        if (correct && !aligned(M.a, 16)) return GLOWQ_ERR_ALIGN;
+    }
+    if (correct && b == nullptr) return GLOWQ_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || !aligned(offsets_dev, 4) || (row_token_dev && !aligned(row_token_dev, 4)) ||
+        (correct && !aligned(b, 16)))
+        return GLOWQ_ERR_ALIGN;
+    return GLOWQ_OK;
+}
 
 // Arguments shared by the router's calls.
 int validate_route(int64_t T, int32_t n_exp, int64_t top_k, int32_t dtype, int32_t score) {
@@ -803,33 +932,12 @@ int glowq_moe_forward(const void* x, int64_t T, int64_t d, int32_t n_exp, int32_
                       const void* b, int32_t share, int32_t r, int32_t restore, const int32_t* row_token_dev,
                       const int32_t* offsets_dev, int64_t n_rows, void* workspace, size_t workspace_bytes,
                       hipStream_t stream) {
-    if (n_exp < 1 || n_exp > GLOWQ_MOE_MAX_EXPERTS || m < 1 || m > GLOWQ_MOE_MAX_MODULES) return GLOWQ_ERR_UNSUPPORTED;
-    if (share != GLOWQ_MOE_SHARE_EXPERT && share != GLOWQ_MOE_SHARE_ALL) return GLOWQ_ERR_INVALID_ARG;
-    if (n_rows < 0 || T < 0 || d < kGroup || d % kGroup != 0) return GLOWQ_ERR_SHAPE;
-    if (r < 0) return GLOWQ_ERR_SHAPE;
-    if (r > GLOWQ_MAX_RANK || r % 8 != 0) return GLOWQ_ERR_UNSUPPORTED;
-    if (n_rows > kMaxT * 8 || T > kMaxT || d > kMaxD || T * d > kMaxActElems) return GLOWQ_ERR_UNSUPPORTED;
-    if (mods == nullptr) return GLOWQ_ERR_INVALID_ARG;
-    if (n_rows == 0) return GLOWQ_OK;
-    if (x == nullptr || offsets_dev == nullptr) return GLOWQ_ERR_INVALID_ARG;
-    if (row_token_dev == nullptr && T != n_rows) return GLOWQ_ERR_SHAPE;
-    if (T < 1) return GLOWQ_ERR_SHAPE;
     const bool correct = restore != 0 && r > 0;
+    const int v = validate_moe(x, T, d, n_exp, m, mods, b, share, r, correct, row_token_dev, offsets_dev, n_rows);
+    if (v != GLOWQ_OK) return v;
+    if (n_rows == 0) return GLOWQ_OK;
     int64_t rb = 0;
-    for (int i = 0; i < m; ++i) {
-        const glowq_moe_module& M = mods[i];
-        if (M.q == nullptr || M.sz == nullptr || M.y == nullptr) return GLOWQ_ERR_INVALID_ARG;
-        if (M.n_out < 1 || M.k_in != d) return GLOWQ_ERR_SHAPE;
-        if (M.n_out > kMaxRows) return GLOWQ_ERR_UNSUPPORTED;
-        if (!aligned(M.q, 16) || !aligned(M.sz, 16) || !aligned(M.y, 16)) return GLOWQ_ERR_ALIGN;
-        if (correct && (M.a == nullptr)) return GLOWQ_ERR_INVALID_ARG;
-        if (correct && !aligned(M.a, 16)) return GLOWQ_ERR_ALIGN;
-        rb += ceil_div(ceil_div(M.n_out, 16), 4 * 2);
-    }
-    if (correct && b == nullptr) return GLOWQ_ERR_INVALID_ARG;
-    if (!aligned(x, 16) || !aligned(offsets_dev, 4) || (row_token_dev && !aligned(row_token_dev, 4)) ||
-        (correct && !aligned(b, 16)))
-        return GLOWQ_ERR_ALIGN;
+    for (int i = 0; i < m; ++i) rb += ceil_div(ceil_div(mods[i].n_out, 16), 4 * 2);
     if (workspace == nullptr || workspace_bytes < glowq_moe_workspace_bytes(n_rows, T, correct ? r : 0, share))
         return GLOWQ_ERR_WORKSPACE;
     if (!aligned(workspace, 256)) return GLOWQ_ERR_ALIGN;
@@ -1238,6 +1346,133 @@ int glowq_group_forward_w8a8(const void* x, int64_t T, int64_t d, int32_t m, con
     const int v = validate(c, workspace, workspace_bytes);
     if (v != GLOWQ_OK) return v;
     return run_w8a8(c, workspace, stream);
+}
+
+size_t glowq_fp8_q_bytes(int64_t n_out, int64_t k_in) {
+    if (n_out < 1 || n_out > kMaxRows || k_in < kGroup || k_in % kGroup != 0 || k_in > kFp8MaxD) return 0;
+    return (size_t)ceil_div(n_out, 16) * (size_t)(k_in / kGroup) * (size_t)kFp8Block;
+}
+
+size_t glowq_fp8_sz_bytes(int64_t n_out, int64_t k_in) {
+    return glowq_fp8_q_bytes(n_out, k_in) == 0 ? 0 : fp8_sz_bytes(n_out, k_in);
+}
+
+int glowq_repack_fp8(const void* codes_dev, const float* scales_dev, int64_t n_out, int64_t k_in, void* q_dev,
+                     void* sz_dev, int32_t* flag_dev, hipStream_t stream) {
+    if (!codes_dev || !scales_dev || !q_dev || !sz_dev || !flag_dev) return GLOWQ_ERR_INVALID_ARG;
+    if (n_out < 1 || k_in < kGroup || k_in % kGroup != 0) return GLOWQ_ERR_SHAPE;
+    if (n_out > kMaxRows || k_in > kFp8MaxD) return GLOWQ_ERR_UNSUPPORTED;
+    if (!aligned(codes_dev, 16) || !aligned(scales_dev, 4) || !aligned(q_dev, 16) || !aligned(sz_dev, 16) ||
+        !aligned(flag_dev, 4))
+        return GLOWQ_ERR_ALIGN;
+    if (launch_flag_clear(flag_dev, stream) != hipSuccess) return GLOWQ_ERR_HIP;
+    if (launch_repack_fp8(static_cast<const uint8_t*>(codes_dev), scales_dev, n_out, k_in, static_cast<uint8_t*>(q_dev),
+                          static_cast<float*>(sz_dev), flag_dev, stream) != hipSuccess)
+        return GLOWQ_ERR_HIP;
+    int32_t flag = 0;
+    if (hipMemcpyAsync(&flag, flag_dev, sizeof(flag), hipMemcpyDeviceToHost, stream) != hipSuccess)
+        return GLOWQ_ERR_HIP;
+    if (hipStreamSynchronize(stream) != hipSuccess) return GLOWQ_ERR_HIP;
+    return flag ? GLOWQ_ERR_RANGE : GLOWQ_OK;
+}
+
+size_t glowq_fp8_workspace_bytes(int64_t T, int64_t d, int32_t r) {
+    if (T <= 0 || T > kMaxT || d < kGroup || d % kGroup != 0 || d > kFp8MaxD || r < 0 || r > GLOWQ_MAX_RANK) return 0;
+    return fp8_codes_bytes(T, d) + (r > 0 ? w8_part_bytes(T, r) + w8_r_bytes(T, r) : 0);
+}
+
+int glowq_group_forward_fp8(const void* x, int64_t T, int64_t d, int32_t m, const glowq_qweight* w,
+                            const void* b_shared, const void* const* a, int32_t r, int32_t restore,
+                            void* workspace, size_t workspace_bytes, void* const* y, hipStream_t stream) {
+    const void* bp[1] = {b_shared};
+    Call c = make_group(x, T, d, m, w, bp, 1, a, r, restore, y);
+    c.fp8 = true;
+    const int v = validate(c, workspace, workspace_bytes);
+    if (v != GLOWQ_OK) return v;
+    return run_fp8(c, workspace, stream);
+}
+
+size_t glowq_moe_fp8_workspace_bytes(int64_t n_rows, int64_t T, int64_t d, int32_t r, int32_t share) {
+    if (n_rows < 0 || n_rows > kMaxT * 8 || T < 0 || T > kMaxT || d < kGroup || d % kGroup != 0 || d > kFp8MaxD || r < 0 ||
+        r > GLOWQ_MAX_RANK)
+        return 0;
+    if (share != GLOWQ_MOE_SHARE_EXPERT && share != GLOWQ_MOE_SHARE_ALL) return 0;
+    size_t n = kWsHeader + fp8_codes_bytes(T, d);
+    if (r > 0) n += share == GLOWQ_MOE_SHARE_ALL ? w8_part_bytes(T, r) + w8_r_bytes(T, r) : w8_r_bytes(n_rows, r);
+    return n;
+}
+
+int glowq_moe_forward_fp8(const void* x, int64_t T, int64_t d, int32_t n_exp, int32_t m, const glowq_moe_module* mods,
+                          const void* b, int32_t share, int32_t r, int32_t restore, const int32_t* row_token_dev,
+                          const int32_t* offsets_dev, int64_t n_rows, void* workspace, size_t workspace_bytes,
+                          hipStream_t stream) {
+    const bool correct = restore != 0 && r > 0;
+    const int v = validate_moe(x, T, d, n_exp, m, mods, b, share, r, correct, row_token_dev, offsets_dev, n_rows);
+    if (v != GLOWQ_OK) return v;
+    if (d > kFp8MaxD) return GLOWQ_ERR_UNSUPPORTED;
+    if (n_rows == 0) return GLOWQ_OK;
+    const int ws = validate_moe_workspace(workspace, workspace_bytes,
+                                          glowq_moe_fp8_workspace_bytes(n_rows, T, d, correct ? r : 0, share));
+    if (ws != GLOWQ_OK) return ws;
+    if (!correct) r = 0;
+    // every expert with rows holds at least one: (expert, block) pairs number at most n_rows / block plus those experts
+    const int64_t active = std::min<int64_t>(n_exp, n_rows);
+    Fp8Args f;
+    std::memset(&f, 0, sizeof(f));
+    f.T = (int32_t)T;
+    f.d = (int32_t)d;
+    f.G = (int32_t)(d / kGroup);
+    f.n_mod = m;
+    f.r = r;
+    f.rp = r > 0 ? (int32_t)w8_r_pad(r) : 0;
+    choose_fp8_shape(ceil_div(n_rows, active), f.tt, f.rr);
+    int64_t blocks = 0;
+    for (int i = 0; i < m; ++i) {
+        Fp8Module& M = f.mod[i];
+        M.q = static_cast<const uint8_t*>(mods[i].q);
+        M.sz = static_cast<const float*>(mods[i].sz);
+        M.a = correct ? static_cast<const _Float16*>(mods[i].a) : nullptr;
+        M.y = static_cast<_Float16*>(mods[i].y);
+        M.q_step = (int64_t)glowq_fp8_q_bytes(mods[i].n_out, d);
+        M.sz_step = (int64_t)(glowq_fp8_sz_bytes(mods[i].n_out, d) / 4);
+        M.a_step = mods[i].n_out * r;
+        M.n_out = (int32_t)mods[i].n_out;
+        M.n_tiles16 = (int32_t)ceil_div(mods[i].n_out, 16);
+        M.block_begin = (int32_t)blocks;
+        blocks += ceil_div(M.n_tiles16, f.rr);
+    }
+    const int64_t items = blocks * (ceil_div(n_rows, 16 * f.tt) + active);
+    if (items > kMaxTiles / 512) return GLOWQ_ERR_UNSUPPORTED;
+    f.row_blocks = (int32_t)blocks;
+    f.row_token = row_token_dev;
+    f.offsets = offsets_dev;
+    f.n_exp = n_exp;
+    f.n_rows = (int32_t)n_rows;
+    f.r_by_token = share == GLOWQ_MOE_SHARE_ALL;
+    f.err = error_word(workspace);
+    const Fp8Space s = fp8_space(static_cast<uint8_t*>(workspace) + kWsHeader, T, d, share == GLOWQ_MOE_SHARE_ALL ? r : 0);
+    const bool all = share == GLOWQ_MOE_SHARE_ALL && r > 0;
+    if (fp8_prepare(x, T, d, b, all ? r : 0, s, T <= kW8SmallT, all, f, stream) != hipSuccess) return GLOWQ_ERR_HIP;
+    if (r > 0 && !all) {
+        MoeArgs p;
+        std::memset(&p, 0, sizeof(p));
+        p.x = static_cast<const _Float16*>(x);
+        p.T = f.T;
+        p.d = f.d;
+        p.G = f.G;
+        p.row_token = row_token_dev;
+        p.offsets = offsets_dev;
+        p.n_exp = n_exp;
+        p.n_rows = f.n_rows;
+        p.r = r;
+        p.r_pad = f.rp;
+        p.b = static_cast<const _Float16*>(b);
+        p.Rout = s.R;
+        p.err = f.err;
+        f.r_rows = f.n_rows;
+        if (launch_moe_proj(p, ceil_div(n_rows, 16) + active, stream) != hipSuccess) return GLOWQ_ERR_HIP;
+    }
+    return launch_fp8(f, items, stream) == hipSuccess ? GLOWQ_OK : GLOWQ_ERR_HIP;
 }
 
 size_t glowq_q_bytes(int64_t n_out, int64_t k_in) {

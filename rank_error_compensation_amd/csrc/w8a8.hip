@@ -19,6 +19,7 @@
 #include <type_traits>
 
 #include "glowq_internal.h"
+#include "project.h"
 #include "w8a8.h"
 
 namespace glowq {
@@ -73,8 +74,6 @@ __global__ __launch_bounds__(256) void repack_w8_scales_kernel(const float* __re
 // What bounds it: up to some 40 tokens the launch and one load's latency (d = 4096, r = 64: 4.9 us for one token,
 // 6.4 us for 37); then memory (T = 2048: 16.8 MB of X and 8.9 MB of codes, scales and sums, 15.2 us; X again by the
 // projection's workgroups, out of the caches).
-constexpr int kPrepThreads = 512;
-constexpr int kPrepWaves = kPrepThreads / 64;
 constexpr int kPrepChunks = 8;  // 8-input chunks per thread at most
 constexpr int kPrepMaxD = 16384;
 
@@ -149,75 +148,6 @@ __device__ void quant_tokens(const _Float16* __restrict__ x, int t0, int T, int 
     }
 }
 
-// Sums of R over the 32-input steps [s_begin, s_end) for 16 TT tokens and 16 NJ rank columns: the
-// wavefronts take steps in turn (U in flight) and add their tiles through LDS in wavefront order.
-// part != nullptr: fp32 sums of this range to part [T][rp]; else one rounding to fp16 into R.
-// Columns r .. r_pad - 1 are zero.
-template <int TT, int NJ>
-__device__ void project_tile(const PrepArgs& a, int tb, int jb, int s_begin, int s_end, float* part, f4* red) {
-    constexpr int U = TT * NJ == 1 ? 8 : 4, N = TT * NJ;
-    const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    const int kofs = 8 * (lane >> 4), T = a.T, d = a.d, r = a.r, rp = a.rp;
-    const _Float16 *xr[TT], *br[NJ];
-#pragma unroll
-    for (int tt = 0; tt < TT; ++tt) xr[tt] = a.x + (size_t)min(16 * (TT * tb + tt) + (lane & 15), T - 1) * d + kofs;
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) br[j] = a.b + (size_t)min(16 * (NJ * jb + j) + (lane & 15), r - 1) * d + kofs;
-    f4 acc[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) acc[i] = f4{0.f, 0.f, 0.f, 0.f};
-    for (int s0 = s_begin + wave; s0 < s_end; s0 += U * kPrepWaves) {
-        h8 xv[U][TT], bv[U][NJ];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int k = 32 * min(s0 + u * kPrepWaves, s_end - 1);
-#pragma unroll
-            for (int tt = 0; tt < TT; ++tt) xv[u][tt] = load_h8(xr[tt] + k);
-#pragma unroll
-            for (int j = 0; j < NJ; ++j) bv[u][j] = load_h8(br[j] + k);
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (s0 + u * kPrepWaves < s_end) {
-#pragma unroll
-                for (int tt = 0; tt < TT; ++tt)
-#pragma unroll
-                    for (int j = 0; j < NJ; ++j) acc[tt * NJ + j] = mfma16(xv[u][tt], bv[u][j], acc[tt * NJ + j]);
-            }
-    }
-    // the upper half's tiles into the lower half, then wavefront i < N sums tile i (half the LDS of one
-    // step: the token workgroups of the same launch need the room to run side by side)
-    constexpr int H = kPrepWaves / 2;
-    if (wave >= H) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) red[((wave - H) * N + i) * 64 + lane] = acc[i];
-    }
-    __syncthreads();
-    if (wave < H) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            f4* own = red + (wave * N + i) * 64 + lane;
-            *own = acc[i] + *own;
-        }
-    }
-    __syncthreads();
-    if (wave >= N) return;
-    f4 v = red[wave * 64 + lane];
-#pragma unroll
-    for (int w = 1; w < H; ++w) v += red[(w * N + wave) * 64 + lane];
-    const int col = 16 * (NJ * jb + wave % NJ) + (lane & 15);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int t = 16 * (TT * tb + wave / NJ) + 4 * (lane >> 4) + i;
-        const float o = col < r ? v[i] : 0.f;
-        if (t < T && col < rp) {
-            if (part != nullptr) part[(size_t)t * rp + col] = o;
-            else a.R[(size_t)t * rp + col] = (_Float16)o;
-        }
-    }
-}
-
 // TPT: threads per token of the code workgroups.
 template <int TT, int NJ, int TPT>
 __global__ __launch_bounds__(kPrepThreads) void prep_kernel(const PrepArgs a, int proj_blocks) {
@@ -234,19 +164,6 @@ __global__ __launch_bounds__(kPrepThreads) void prep_kernel(const PrepArgs a, in
     const int per = a.range / 32;
     project_tile<TT, NJ>(a, tb, jb, k * per, min((k + 1) * per, a.d / 32),
                          a.part != nullptr ? a.part + (size_t)k * a.T * a.rp : nullptr, red);
-}
-
-// R = the K ranges' sums added in order, rounded once to fp16; four values from value 4 i.  A few MB out of
-// the caches (T = 2048, r = 64, 4 ranges: 2.1 MB, 4.9 us): bound by its launch.
-__device__ __forceinline__ void join_ranges(const PrepArgs& a, size_t i) {
-    const size_t n = (size_t)a.T * a.rp / 4;
-    if (i >= n) return;
-    const f4* p = reinterpret_cast<const f4*>(a.part) + i;
-    f4 v = p[0];
-#pragma unroll 4
-    for (int k = 1; k < a.ks; ++k) v += p[(size_t)k * n];
-    const h2 lo = {(_Float16)v[0], (_Float16)v[1]}, hi = {(_Float16)v[2], (_Float16)v[3]};
-    reinterpret_cast<u2*>(a.R)[i] = u2{as_u32(lo), as_u32(hi)};
 }
 
 __global__ __launch_bounds__(256) void prep_join_kernel(const PrepArgs a) {

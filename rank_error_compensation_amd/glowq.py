@@ -34,6 +34,7 @@ FMT_MXFP4 = 1
 FMT_MXFP6_E2M3 = 2
 FMT_MXFP6_E3M2 = 3
 FMT_INT8_CHANNEL = 4
+FMT_FP8_BLOCK = 5
 FORMATS = {"int4": FMT_INT4_G128, "mxfp4": FMT_MXFP4, "mxfp6_e2m3": FMT_MXFP6_E2M3, "mxfp6_e3m2": FMT_MXFP6_E3M2}
 
 DTYPE_F32 = 0
@@ -93,6 +94,14 @@ EXPORTS = {
     "glowq_w8a8_workspace_bytes": (_sz, [_i64, _i64, _i32]),
     # host arrays as addresses (packed bytes or ctypes arrays)
     "glowq_group_forward_w8a8": (ctypes.c_int, [_vp, _i64, _i64, _i32, _vp, _vp, _vp, _i32, _i32, _vp, _sz, _vp, _vp]),
+    "glowq_fp8_q_bytes": (_sz, [_i64, _i64]),
+    "glowq_fp8_sz_bytes": (_sz, [_i64, _i64]),
+    "glowq_repack_fp8": (ctypes.c_int, [_vp, _vp, _i64, _i64, _vp, _vp, _vp, _vp]),
+    "glowq_fp8_workspace_bytes": (_sz, [_i64, _i64, _i32]),
+    "glowq_group_forward_fp8": (ctypes.c_int, [_vp, _i64, _i64, _i32, _vp, _vp, _vp, _i32, _i32, _vp, _sz, _vp, _vp]),
+    "glowq_moe_fp8_workspace_bytes": (_sz, [_i64, _i64, _i64, _i32, _i32]),
+    "glowq_moe_forward_fp8": (ctypes.c_int, [_vp, _i64, _i64, _i32, _i32, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _i64, _vp,
+                                             _sz, _vp]),
     "glowq_moe_sort_workspace_bytes": (_sz, [_i64, _i64, _i32]),
     "glowq_moe_sort": (ctypes.c_int, [_vp, _i64, _i64, _i32, _vp, _vp, _vp, _vp, _sz, _vp]),
     "glowq_moe_dispatch": (ctypes.c_int, [_vp, _i64, _i64, _i32, _vp, _i64, _vp, _vp, _sz, _vp]),
@@ -295,6 +304,33 @@ class QWeight:
             check(L.glowq_repack_w8(_ptr(c), _ptr(s), n_out, k_in, _ptr(q_dev), _ptr(sz_dev), _ptr(flag),
                                     _stream(stream)), "glowq_repack_w8")
         return QWeight(q_dev, sz_dev, n_out, k_in, FMT_INT8_CHANNEL)
+
+    @staticmethod
+    def from_fp8(codes: torch.Tensor, scales: torch.Tensor, device=None, stream=None) -> "QWeight":
+        """Repack e4m3 codes (torch.float8_e4m3fn, or their bytes as uint8, [n_out][k_in]) and the scales of their
+        128 x 128 blocks (fp32 [ceil(n_out / 128)][k_in / 128]) into the device layout of group_forward_fp8
+        (glowq_repack_fp8; synchronises the stream)."""
+        device = torch.device("cuda" if device is None else device)
+        _require(codes.dim() == 2 and codes.dtype in (torch.float8_e4m3fn, torch.uint8) and scales.dtype == torch.float32,
+                 ERR_INVALID_ARG, "from_fp8: e4m3 codes [n_out][k_in], fp32 scales [ceil(n_out / 128)][k_in / 128]")
+        n_out, k_in = (int(n) for n in codes.shape)
+        L = lib()
+        qb, zb = L.glowq_fp8_q_bytes(n_out, k_in), L.glowq_fp8_sz_bytes(n_out, k_in)
+        if qb == 0 or zb == 0:
+            raise GlowQError(ERR_SHAPE, "glowq_fp8_q_bytes")
+        _require(tuple(scales.shape) == (-(-n_out // 128), k_in // 128), ERR_SHAPE, "from_fp8: one scale per 128 x 128 block")
+        _require(device.type == "cuda", ERR_INVALID_ARG, "from_fp8: a GPU device")
+        _require(stream is None or device.index is None or stream.device == device, ERR_INVALID_ARG,
+                 "from_fp8: stream of another device")
+        # copies, allocations and the repack all on the one stream
+        with torch.cuda.device(device) if stream is None else torch.cuda.stream(stream):
+            c, s = codes.to(device).contiguous(), scales.to(device).contiguous()
+            q_dev = torch.empty(qb, dtype=torch.uint8, device=c.device)
+            sz_dev = torch.empty(zb, dtype=torch.uint8, device=c.device)
+            flag = torch.empty(1, dtype=torch.int32, device=c.device)
+            check(L.glowq_repack_fp8(_ptr(c), _ptr(s), n_out, k_in, _ptr(q_dev), _ptr(sz_dev), _ptr(flag),
+                                     _stream(stream)), "glowq_repack_fp8")
+        return QWeight(q_dev, sz_dev, n_out, k_in, FMT_FP8_BLOCK)
 
     @staticmethod
     def from_workload(qw, device=None, stream=None) -> "QWeight":
@@ -596,29 +632,84 @@ def group_forward_w8a8(x: torch.Tensor, weights: Sequence[QWeight], b: Optional[
     return y
 
 
+def fp8_workspace_bytes(T: int, d: int, r: int) -> int:
+    return int(lib().glowq_fp8_workspace_bytes(T, d, r))
+
+
+def group_forward_fp8(x: torch.Tensor, weights: Sequence[QWeight], b: Optional[torch.Tensor],
+                       a: Sequence[torch.Tensor], r: int, restore: bool = True,
+                       workspace: Optional[torch.Tensor] = None, y: Optional[List[torch.Tensor]] = None,
+                       stream=None) -> List[torch.Tensor]:
+    """glowq_group_forward_fp8: e4m3 weights (QWeight.from_fp8) and activations, a scale for each block of 128, the
+    correction on the fp16 activations."""
+    what = "group_forward_fp8"
+    a = a or ()
+    _same_place(what, x, b, workspace, *a, *(y or ()))
+    dev = x.get_device()
+    for w in weights:
+        if w.q.get_device() != dev or w.sz.get_device() != dev:
+            raise GlowQError(ERR_INVALID_ARG, f"{what}: weights on the device of x")
+    ctx = _elsewhere(x, stream)
+    if ctx is not None:
+        with ctx:
+            return group_forward_fp8(x, weights, b, a, r, restore, workspace, y)
+    if x.dim() != 2 or x.dtype != torch.float16:
+        raise GlowQError(ERR_INVALID_ARG, f"{what}: x fp16 [T][d]")
+    T, d = x.shape
+    m = len(weights)
+    correct = bool(restore) and r > 0
+    ap = None
+    if correct:
+        if b is None or len(a) != m or b.dtype != torch.float16:
+            raise GlowQError(ERR_INVALID_ARG, f"{what}: fp16 factors, one per module")
+        _require(b.shape == (r, d), ERR_SHAPE, f"{what}: b [r][d]")
+        for t, w in zip(a, weights):
+            if t.dtype != torch.float16 or t.shape != (w.n_out, r):
+                raise GlowQError(ERR_SHAPE, f"{what}: a[i] fp16 [n_out][r]")
+        ap = struct.pack(f"{m}Q", *[t.data_ptr() for t in a])
+    if y is None:
+        y = [x.new_empty((T, w.n_out)) for w in weights]
+    else:
+        _require(len(y) == m, ERR_SHAPE, f"{what}: an output per module")
+        for t, w in zip(y, weights):
+            _require(t.dtype == torch.float16 and t.shape == (T, w.n_out), ERR_SHAPE, f"{what}: y[i] fp16 [T][n_out]")
+    if workspace is None and T > 0:
+        workspace = torch.empty(max(fp8_workspace_bytes(T, d, r if correct else 0), 256), dtype=torch.uint8,
+                                device=x.device)
+    wp = b"".join([_WEIGHT.pack(w.q.data_ptr(), w.sz.data_ptr(), w.n_out, w.k_in, w.fmt, 0) for w in weights])
+    yp = struct.pack(f"{m}Q", *[t.data_ptr() for t in y])
+    st = lib().glowq_group_forward_fp8(x.data_ptr(), T, d, m, wp, _addr(b), ap, r, 1 if correct else 0,
+                                        _addr(workspace), _bytes(workspace), yp, _current(x))
+    if st != OK:
+        check(st, "glowq_group_forward_fp8")
+    return y
+
+
 # --------------------------------------------------------------------------- mixture of experts
 @dataclass
 class MoeModule:
     """One module (gate, up or down) of every expert, stacked: expert e's device layout at
-    e * q_bytes / e * sz_bytes, its left factor a[e] fp16 [n_out][r].  INT4 weights of one shape:
-    the experts' product knows no other layout, and takes expert e's place from these sizes."""
+    e * q_bytes / e * sz_bytes, its left factor a[e] fp16 [n_out][r].  Weights of one format and shape, INT4
+    (moe_forward) or block-scaled FP8 (moe_forward_fp8): the experts' products take expert e's place from these sizes."""
     q: torch.Tensor
     sz: torch.Tensor
     a: Optional[torch.Tensor]   # fp16 [n_exp][n_out][r]
     n_out: int
     k_in: int
+    fmt: int = FMT_INT4_G128
 
     @staticmethod
     def stack(weights: Sequence[QWeight], a: Optional[Sequence[torch.Tensor]]) -> "MoeModule":
         _require(len(weights) > 0, ERR_SHAPE, "MoeModule.stack: a weight per expert")
         for w in weights:
-            _require(w.fmt == FMT_INT4_G128, ERR_UNSUPPORTED, "MoeModule.stack: INT4 weights")
+            _require(w.fmt == weights[0].fmt and w.fmt in (FMT_INT4_G128, FMT_FP8_BLOCK), ERR_UNSUPPORTED,
+                     "MoeModule.stack: INT4 or FP8 weights")
             _require((w.n_out, w.k_in) == (weights[0].n_out, weights[0].k_in), ERR_SHAPE,
                      "MoeModule.stack: weights of one shape")
         q = torch.cat([w.q for w in weights]).contiguous()
         sz = torch.cat([w.sz for w in weights]).contiguous()
         a_st = torch.stack(list(a)).contiguous() if a is not None else None
-        return MoeModule(q, sz, a_st, weights[0].n_out, weights[0].k_in)
+        return MoeModule(q, sz, a_st, weights[0].n_out, weights[0].k_in, weights[0].fmt)
 
 
 def moe_workspace_bytes(n_rows: int, T: int, r: int, share: int) -> int:
@@ -631,6 +722,7 @@ def moe_forward(x: torch.Tensor, n_exp: int, modules: Sequence[MoeModule], b: Op
                 stream=None) -> List[torch.Tensor]:
     """glowq_moe_forward: outputs y_i fp16 [n_rows][n_out_i] in routed-row order."""
     for mm in modules:
+        _require(mm.fmt == FMT_INT4_G128, ERR_UNSUPPORTED, "moe_forward: INT4 modules")
         blocks = n_exp * (-(-mm.n_out // 16) * (mm.k_in // 128))  # 16 x 128 weights: 1024 bytes of codes, 64 of scales
         if mm.q.nbytes < 1024 * blocks or mm.sz.nbytes < 64 * blocks:
             raise GlowQError(ERR_SHAPE, "moe_forward: INT4 modules of n_exp experts")
@@ -645,6 +737,65 @@ def moe_forward(x: torch.Tensor, n_exp: int, modules: Sequence[MoeModule], b: Op
     check(lib().glowq_moe_forward(_ptr(x), x.shape[0], x.shape[1], n_exp, len(modules), mc, _ptr(b), share, r,
                                   int(bool(restore)), _ptr(row_token), _ptr(offsets), n_rows, _ptr(workspace),
                                   workspace.numel(), _stream(stream)), "glowq_moe_forward")
+    return y
+
+
+def moe_fp8_workspace_bytes(n_rows: int, T: int, d: int, r: int, share: int) -> int:
+    return int(lib().glowq_moe_fp8_workspace_bytes(n_rows, T, d, r, share))
+
+
+_MOE_MODULE = struct.Struct("QQQQqq")
+
+
+def moe_forward_fp8(x: torch.Tensor, n_exp: int, modules: Sequence[MoeModule], b: Optional[torch.Tensor], share: int,
+                    r: int, restore: bool, row_token: Optional[torch.Tensor], offsets: torch.Tensor, n_rows: int,
+                    workspace: Optional[torch.Tensor] = None, y: Optional[List[torch.Tensor]] = None,
+                    stream=None) -> List[torch.Tensor]:
+    """glowq_moe_forward_fp8: moe_forward on block-scaled FP8 modules (stacked QWeight.from_fp8), outputs y_i fp16
+    [n_rows][n_out_i] in routed-row order.  workspace None: as with the routed rows below, a fresh one; the call then
+    synchronises, raises ERR_ROUTING itself and cannot be captured."""
+    what = "moe_forward_fp8"
+    correct = bool(restore) and r > 0
+    m = len(modules)
+    used = [t for mm in modules for t in (mm.q, mm.sz, mm.a if correct else None)]
+    _same_place(what, x, b if correct else None, row_token, offsets, workspace, *used, *(y or ()))
+    ctx = _elsewhere(x, stream)
+    if ctx is not None:
+        with ctx:
+            return moe_forward_fp8(x, n_exp, modules, b, share, r, restore, row_token, offsets, n_rows, workspace, y)
+    if x.dim() != 2 or x.dtype != torch.float16:
+        raise GlowQError(ERR_INVALID_ARG, f"{what}: x fp16 [T][d]")
+    T, d = x.shape
+    if offsets.dtype != torch.int32 or (row_token is not None and row_token.dtype != torch.int32):
+        raise GlowQError(ERR_INVALID_ARG, f"{what}: int32 lists")
+    if offsets.numel() != n_exp + 1 or (row_token is not None and row_token.numel() < n_rows):
+        raise GlowQError(ERR_SHAPE, f"{what}: offsets [n_exp + 1], row_token [n_rows]")
+    for mm in modules:
+        _require(mm.fmt == FMT_FP8_BLOCK, ERR_UNSUPPORTED, f"{what}: FP8 modules")
+        if (mm.q.nbytes < n_exp * lib().glowq_fp8_q_bytes(mm.n_out, mm.k_in)
+                or mm.sz.nbytes < n_exp * lib().glowq_fp8_sz_bytes(mm.n_out, mm.k_in)):
+            raise GlowQError(ERR_SHAPE, f"{what}: modules of n_exp experts")
+        if correct and (mm.a is None or mm.a.dtype != torch.float16 or mm.a.shape != (n_exp, mm.n_out, r)):
+            raise GlowQError(ERR_SHAPE, f"{what}: a fp16 [n_exp][n_out][r]")
+    if correct and (b is None or b.dtype != torch.float16 or b.shape != ((n_exp, r, d) if share == MOE_SHARE_EXPERT else (r, d))):
+        raise GlowQError(ERR_SHAPE, f"{what}: b fp16 [n_exp][r][d], or [r][d] shared by all")
+    _require(n_rows >= 0, ERR_SHAPE, f"{what}: n_rows >= 0")
+    if y is None:
+        y = [x.new_empty((n_rows, mm.n_out)) for mm in modules]
+    else:
+        _require(len(y) == m, ERR_SHAPE, f"{what}: an output per module")
+        for t, mm in zip(y, modules):
+            _require(t.dtype == torch.float16 and t.shape == (n_rows, mm.n_out), ERR_SHAPE, f"{what}: y[i] fp16 [n_rows][n_out]")
+    ws = workspace
+    if ws is None:
+        ws = _moe_ws(None, x, max(moe_fp8_workspace_bytes(n_rows, T, d, r if correct else 0, share), _MOE_HEADER))
+    mc = b"".join([_MOE_MODULE.pack(mm.q.data_ptr(), mm.sz.data_ptr(), mm.a.data_ptr() if correct else 0, t.data_ptr(),
+                                    mm.n_out, mm.k_in) for mm, t in zip(modules, y)])
+    st = lib().glowq_moe_forward_fp8(x.data_ptr(), T, d, n_exp, m, mc, _addr(b) if correct else None, share, r,
+                                     1 if correct else 0, _addr(row_token), offsets.data_ptr(), n_rows, ws.data_ptr(),
+                                     _bytes(ws), _current(x))
+    if st != OK or workspace is None:
+        _moe_done(st, ws, "glowq_moe_forward_fp8")
     return y
 
 
