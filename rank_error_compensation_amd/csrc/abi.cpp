@@ -665,7 +665,7 @@ int run_w8a8(const Call& c, void* workspace, hipStream_t stream) {
 }
 
 // Block-scaled e4m3 form.  Workspace: codes [T][d] | scales fp32 [T][gp] | for a correcting call the projection's
-// fp32 K ranges | fp16 projection.
+// fp32 K ranges | fp16 projection | the K ranges' fp32 tiles.
 struct Fp8Space {
     uint8_t* xq;
     float* xs;
@@ -685,17 +685,56 @@ Fp8Space fp8_space(uint8_t* base, int64_t T, int64_t d, int32_t r) {
     return s;
 }
 
-// 16-token and 16-row tiles per workgroup for `rows` rows of one input (an expert's on average).
-void choose_fp8_shape(int64_t rows, int32_t& tt, int32_t& rr) {
-    tt = rows <= 16 ? 1 : (rows <= 32 ? 2 : 4);
-    rr = rows <= 16 ? 1 : 2;
+// The K ranges' fp32 tiles of a call of more than 32 tokens: at most 256 of 64 KB.
+constexpr size_t kFp8PartBytes = (size_t)16 << 20;
+
+// Launch shape of a group call.
+void choose_fp8_shape(const Call& c, Fp8Args& f) {
+    auto set = [&](int tt, int rr, int kh) { f.tt = tt, f.rr = rr, f.kh = kh; };
+    auto tiles = [&](int tt, int rr) {
+        int64_t n = 0;
+        for (int i = 0; i < c.m; ++i) n += ceil_div(ceil_div(c.w[i].n_out, 16), rr);
+        return n * ceil_div(c.T, 16 * tt);
+    };
+    // K ranges of at least `least` groups up to a tile a CU; whole turns of the ring for every team
+    auto ranges = [&](int64_t n, int64_t least) {
+        const int64_t ks = std::max<int64_t>(1, std::min<int64_t>(256 / n, c.d / kGroup / least));
+        f.gk = (int32_t)(ceil_div(ceil_div(c.d / kGroup, ks), 4 * f.kh) * 4 * f.kh);
+        f.ks = (int32_t)ceil_div(c.d / kGroup, f.gk);
+    };
+    f.ks = 1;
+    f.gk = (int32_t)(ceil_div(c.d / kGroup, 4) * 4);
+    set(c.T <= 16 ? 1 : (c.T <= 32 ? 2 : 4), c.T <= 16 ? 1 : 2, 1);
+    if (c.T <= kW8SmallT) {
+        if (c.T <= kW8TinyT) return;
+        const int64_t n = tiles(4, 8);
+        if (n <= 64 && c.T * c.d < ((int64_t)1 << 19)) return;
+        set(4, 8, 4);
+        return ranges(n, 24);
+    }
+    set(8, 16, 1);
+    if (tiles(8, 16) > 256) return;
+    set(8, 8, 1);
+    const int64_t n = tiles(8, 8);
+    if (n > 256 || c.d / kGroup < 16) return;
+    set(8, 8, 2);
+    ranges(n, 8);
 }
 
-// Codes, scales and the projection of T tokens: f.xq, f.xs and f.R.  ranges: R stays as its fp32 K ranges.
+// And of the experts' product, for `rows` rows an expert on average.
+void choose_fp8_experts_shape(int64_t rows, Fp8Args& f) {
+    f.ks = 1;
+    f.gk = (int32_t)(ceil_div((int64_t)f.G, 4) * 4);
+    f.kh = 1;
+    f.tt = rows <= 16 ? 1 : (rows <= 32 ? 2 : (rows <= 64 ? 4 : 8));
+    f.rr = rows <= 16 ? 1 : (rows <= 64 ? 2 : 16);
+}
+
+// Codes, scales and the projection of T tokens: f.xq, f.xs and f.R.  ranges: R stays as its fp32 K ranges; join: they
+// are added up here.
 hipError_t fp8_prepare(const void* x, int64_t T, int64_t d, const void* b, int32_t r, const Fp8Space& s, bool small,
-                       bool ranges, Fp8Args& f, hipStream_t stream) {
+                       bool ranges, bool join, Fp8Args& f, Fp8PrepArgs& p, hipStream_t stream) {
     const PrepPlan plan = w8a8_prep_plan(T, d, r, small);
-    Fp8PrepArgs p;
     std::memset(&p, 0, sizeof(p));
     p.x = static_cast<const _Float16*>(x);
     p.b = static_cast<const _Float16*>(b);
@@ -721,7 +760,7 @@ hipError_t fp8_prepare(const void* x, int64_t T, int64_t d, const void* b, int32
     f.R = ranges ? static_cast<const void*>(s.part) : static_cast<const void*>(s.R);
     f.r_ranges = ranges ? plan.ks : 0;
     f.r_rows = (int32_t)T;
-    return launch_fp8_prep(p, plan.tt, plan.nj, !ranges, stream);
+    return launch_fp8_prep(p, plan.tt, plan.nj, join, stream);
 }
 
 int run_fp8(const Call& c, void* workspace, hipStream_t stream) {
@@ -735,7 +774,7 @@ int run_fp8(const Call& c, void* workspace, hipStream_t stream) {
     f.n_mod = c.m;
     f.r = r;
     f.rp = r > 0 ? (int32_t)w8_r_pad(r) : 0;
-    choose_fp8_shape(c.T, f.tt, f.rr);
+    choose_fp8_shape(c, f);
     int64_t blocks = 0;
     for (int i = 0; i < c.m; ++i) {
         Fp8Module& M = f.mod[i];
@@ -751,9 +790,17 @@ int run_fp8(const Call& c, void* workspace, hipStream_t stream) {
     f.row_blocks = (int32_t)blocks;
     f.m_blocks = (int32_t)ceil_div(c.T, 16 * f.tt);
     const Fp8Space s = fp8_space(static_cast<uint8_t*>(workspace), c.T, c.d, r);
-    if (fp8_prepare(c.x, c.T, c.d, c.correct ? c.b[0] : nullptr, r, s, c.T <= kW8SmallT, true, f, stream) != hipSuccess)
+    if (f.ks > 1) {
+        if ((size_t)(blocks * f.m_blocks * f.ks * f.tt) * 8192u > kFp8PartBytes) return GLOWQ_ERR_WORKSPACE;
+        f.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + glowq_fp8_workspace_bytes(c.T, c.d, r) - kFp8PartBytes);
+    }
+    const bool small = f.rr <= 2;
+    const bool ranges = small || (f.kh > 1 && f.ks == 1);  // the product adds up the projection's K ranges itself
+    Fp8PrepArgs p;
+    if (fp8_prepare(c.x, c.T, c.d, c.correct ? c.b[0] : nullptr, r, s, small, ranges, !ranges && f.ks == 1, f, p, stream) !=
+        hipSuccess)
         return GLOWQ_ERR_HIP;
-    return launch_fp8(f, blocks * f.m_blocks, stream) == hipSuccess ? GLOWQ_OK : GLOWQ_ERR_HIP;
+    return launch_fp8(f, p, blocks * f.m_blocks, stream) == hipSuccess ? GLOWQ_OK : GLOWQ_ERR_HIP;
 }
 
 // Arguments shared by the calls that move routed rows.
@@ -1378,7 +1425,7 @@ int glowq_repack_fp8(const void* codes_dev, const float* scales_dev, int64_t n_o
 
 size_t glowq_fp8_workspace_bytes(int64_t T, int64_t d, int32_t r) {
     if (T <= 0 || T > kMaxT || d < kGroup || d % kGroup != 0 || d > kFp8MaxD || r < 0 || r > GLOWQ_MAX_RANK) return 0;
-    return fp8_codes_bytes(T, d) + (r > 0 ? w8_part_bytes(T, r) + w8_r_bytes(T, r) : 0);
+    return fp8_codes_bytes(T, d) + (r > 0 ? w8_part_bytes(T, r) + w8_r_bytes(T, r) : 0) + (T > kW8TinyT ? kFp8PartBytes : 0);
 }
 
 int glowq_group_forward_fp8(const void* x, int64_t T, int64_t d, int32_t m, const glowq_qweight* w,
@@ -1425,7 +1472,7 @@ int glowq_moe_forward_fp8(const void* x, int64_t T, int64_t d, int32_t n_exp, in
     f.n_mod = m;
     f.r = r;
     f.rp = r > 0 ? (int32_t)w8_r_pad(r) : 0;
-    choose_fp8_shape(ceil_div(n_rows, active), f.tt, f.rr);
+    choose_fp8_experts_shape(ceil_div(n_rows, active), f);
     int64_t blocks = 0;
     for (int i = 0; i < m; ++i) {
         Fp8Module& M = f.mod[i];
@@ -1451,8 +1498,10 @@ int glowq_moe_forward_fp8(const void* x, int64_t T, int64_t d, int32_t n_exp, in
     f.r_by_token = share == GLOWQ_MOE_SHARE_ALL;
     f.err = error_word(workspace);
     const Fp8Space s = fp8_space(static_cast<uint8_t*>(workspace) + kWsHeader, T, d, share == GLOWQ_MOE_SHARE_ALL ? r : 0);
-    const bool all = share == GLOWQ_MOE_SHARE_ALL && r > 0;
-    if (fp8_prepare(x, T, d, b, all ? r : 0, s, T <= kW8SmallT, all, f, stream) != hipSuccess) return GLOWQ_ERR_HIP;
+    const bool all = share == GLOWQ_MOE_SHARE_ALL && r > 0, ranges = all && f.rr <= 2;
+    Fp8PrepArgs prep;
+    if (fp8_prepare(x, T, d, b, all ? r : 0, s, T <= kW8SmallT, ranges, !ranges, f, prep, stream) != hipSuccess)
+        return GLOWQ_ERR_HIP;
     if (r > 0 && !all) {
         MoeArgs p;
         std::memset(&p, 0, sizeof(p));
@@ -1472,7 +1521,7 @@ int glowq_moe_forward_fp8(const void* x, int64_t T, int64_t d, int32_t n_exp, in
         f.r_rows = f.n_rows;
         if (launch_moe_proj(p, ceil_div(n_rows, 16) + active, stream) != hipSuccess) return GLOWQ_ERR_HIP;
     }
-    return launch_fp8(f, items, stream) == hipSuccess ? GLOWQ_OK : GLOWQ_ERR_HIP;
+    return launch_fp8(f, prep, items, stream) == hipSuccess ? GLOWQ_OK : GLOWQ_ERR_HIP;
 }
 
 size_t glowq_q_bytes(int64_t n_out, int64_t k_in) {

@@ -48,7 +48,10 @@ struct Fp8Args {
     int32_t r, rp;
     const void* R;        // r_ranges fp32 K ranges [.][r_rows][rp], or fp16 [r_rows][rp] where r_ranges is 0
     int32_t r_ranges, r_rows;
-    int32_t tt, rr;       // 16-token and 16-row tiles per workgroup
+    int32_t tt, rr;       // 16-token and 16-row tiles per workgroup; rr >= 8: the large tiles
+    int32_t kh;           // teams of wavefronts in a workgroup that split its input groups (large tiles)
+    int32_t ks, gk;       // K ranges over workgroups, input groups per range (large tiles)
+    float* part;          // the K ranges' fp32 tiles
     int32_t row_blocks;   // of all modules
     int32_t m_blocks;     // token blocks
     // experts (offsets != nullptr): rows listed by expert
@@ -63,7 +66,9 @@ struct Fp8Args {
 hipError_t launch_repack_fp8(const uint8_t* codes, const float* scales, int64_t n_out, int64_t k_in, uint8_t* q, float* sz,
                              int32_t* flag, hipStream_t stream);
 hipError_t launch_fp8_prep(const Fp8PrepArgs& a, int tt, int nj, bool join, hipStream_t stream);
-// items: an upper bound of the launch's work tiles
-hipError_t launch_fp8(const Fp8Args& a, int64_t items, hipStream_t stream);
+// Large tiles by Fp8Args::tt x rr: 8 x 16 and 8 x 8 on four wavefronts, 4 x 8 on two, times kh teams.
+// items: an upper bound of the launch's work tiles.  p: the preparation of the same call, whose projection ranges a launch
+// with K ranges joins.
+hipError_t launch_fp8(const Fp8Args& a, const Fp8PrepArgs& p, int64_t items, hipStream_t stream);
 
 }  // namespace glowq

@@ -17,6 +17,7 @@
 // activation operand takes the same inputs in the same places, so the order of inputs inside the step does not matter.
 // Rows >= n_out are zero.  Codes of the activations lie in their natural order [T][d], scales [T][G rounded up to 4].
 #include <algorithm>
+#include <type_traits>
 
 #include "fp8.h"
 #include "project.h"
@@ -27,9 +28,13 @@ typedef int32_t i8v __attribute__((ext_vector_type(8)));
 
 namespace {
 
-__device__ __forceinline__ f4 mfma_fp8(const u4& w0, const u4& w1, const u4& x0, const u4& x1) {
-    const i8v w = {(int)w0[0], (int)w0[1], (int)w0[2], (int)w0[3], (int)w1[0], (int)w1[1], (int)w1[2], (int)w1[3]};
-    const i8v x = {(int)x0[0], (int)x0[1], (int)x0[2], (int)x0[3], (int)x1[0], (int)x1[1], (int)x1[2], (int)x1[3]};
+// The two 16-byte pieces of an operand, as the eight registers that the matrix core reads.
+__device__ __forceinline__ i8v load_operand(const void* p0, const void* p1) {
+    typedef int32_t i4v __attribute__((ext_vector_type(4)));
+    return __builtin_shufflevector(*static_cast<const i4v*>(p0), *static_cast<const i4v*>(p1), 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+__device__ __forceinline__ f4 mfma_fp8(const i8v& w, const i8v& x) {
     // scale operands of zero: the form without block scales
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, f4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
 }
@@ -127,8 +132,10 @@ struct Work {
 };
 
 // Item of the launch with experts, in the order (expert, row block, block of its rows).  Every wavefront finds its own,
-// four experts a lane.  Offsets out of order or range are clamped and reported by item 0.
-__device__ __forceinline__ bool expert_work(const Fp8Args& a, int rows_per_block, int item, Work& w) {
+// four experts a lane.  Offsets out of order or range are clamped and reported by the first workgroup.  SPREAD: XCD x
+// (workgroups b with b % 8 == x) takes a run of consecutive items, so that an expert's row block stays in one L2.
+template <bool SPREAD>
+__device__ __forceinline__ bool expert_work(const Fp8Args& a, int rows_per_block, Work& w) {
     const int lane = threadIdx.x & 63;
     int lo[4], hi[4], nb[4], sum = 0;
     bool bad = false;
@@ -145,12 +152,18 @@ __device__ __forceinline__ bool expert_work(const Fp8Args& a, int rows_per_block
             sum += nb[q];
         }
     }
-    if (bad && item == 0) __hip_atomic_fetch_or(a.err, 2, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (bad && blockIdx.x == 0) __hip_atomic_fetch_or(a.err, 2, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     int upto = sum;
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
         const int n = __shfl_up(upto, off, 64);
         if (lane >= off) upto += n;
+    }
+    int item = blockIdx.x;
+    if constexpr (SPREAD) {
+        const int total = __builtin_amdgcn_readlane(upto, 63) * a.row_blocks, run = (total + 7) >> 3;
+        if ((item >> 3) >= run) return false;
+        item = (item & 7) * run + (item >> 3);
     }
     int at = (upto - sum) * a.row_blocks, e = 0, blocks = 1, first = 0, l = 0, h = 0;
     bool hit = false;
@@ -235,7 +248,7 @@ __global__ __launch_bounds__(64 * kFp8Waves) void fp8_split_kernel(const Fp8Args
     __shared__ f4 red[NW][NT][64];
     Work wk;
     if constexpr (EXPERTS) {
-        if (!expert_work(args, 16 * TT, blockIdx.x, wk)) return;
+        if (!expert_work<false>(args, 16 * TT, wk)) return;
     } else {
         wk.e = 0;
         wk.rb = blockIdx.x / args.m_blocks;
@@ -275,21 +288,19 @@ __global__ __launch_bounds__(64 * kFp8Waves) void fp8_split_kernel(const Fp8Args
         for (int rr = 0; rr < RR; ++rr) acc[tt][rr] = f4{0.f, 0.f, 0.f, 0.f};
     constexpr int U = 2;
     for (int g0 = wave; g0 < G; g0 += U * NW) {
-        u4 w[U][RR][2], x[U][TT][2];
+        i8v w[U][RR], x[U][TT];
         float xs[U][TT], ws[U][RR];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int g = min(g0 + u * NW, G - 1);
 #pragma unroll
             for (int rr = 0; rr < RR; ++rr) {
-                w[u][rr][0] = *reinterpret_cast<const u4*>(qp[rr] + (size_t)g * qstride);
-                w[u][rr][1] = *reinterpret_cast<const u4*>(qp[rr] + (size_t)g * qstride + 1024);
+                w[u][rr] = load_operand(qp[rr] + (size_t)g * qstride, qp[rr] + (size_t)g * qstride + 1024);
                 ws[u][rr] = sp[rr][g];
             }
 #pragma unroll
             for (int tt = 0; tt < TT; ++tt) {
-                x[u][tt][0] = *reinterpret_cast<const u4*>(xp[tt] + (size_t)g * kGroup);
-                x[u][tt][1] = *reinterpret_cast<const u4*>(xp[tt] + (size_t)g * kGroup + 64);
+                x[u][tt] = load_operand(xp[tt] + (size_t)g * kGroup, xp[tt] + (size_t)g * kGroup + 64);
                 xs[u][tt] = xsp[tt][g];
             }
         }
@@ -300,7 +311,7 @@ __global__ __launch_bounds__(64 * kFp8Waves) void fp8_split_kernel(const Fp8Args
                 for (int tt = 0; tt < TT; ++tt)
 #pragma unroll
                     for (int rr = 0; rr < RR; ++rr) {
-                        const f4 p = mfma_fp8(w[u][rr][0], w[u][rr][1], x[u][tt][0], x[u][tt][1]);
+                        const f4 p = mfma_fp8(w[u][rr], x[u][tt]);
                         const float s = xs[u][tt] * ws[u][rr];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) acc[tt][rr][i] = fmaf(p[i], s, acc[tt][rr][i]);
@@ -332,6 +343,425 @@ __global__ __launch_bounds__(64 * kFp8Waves) void fp8_split_kernel(const Fp8Args
         }
     }
     if (ok) store_rows(M, j, rt * 16 + 4 * (lane >> 4), v);
+}
+
+// --------------------------------------------------------------------- large tiles
+// 16 TT WM tokens x 64 WN rows per workgroup: WM x WN wavefronts, each 16 TT tokens x 4 row tiles.
+// The token codes of an input group (128 bytes a token) go memory -> LDS by the load unit into a ring of four stages, CA
+// groups ahead; a wavefront's weight operands come straight into registers, WA groups ahead (the WM wavefronts that share
+// rows find them in the L1 cache), so that LDS carries only the codes.  A token's scales of four groups come as one
+// 16-byte piece every fourth group; the scale of the wavefront's 64 rows (one 128-row block) is a lane of a register.
+// A group's sums leave the matrix core into four registers a tile and are added, scaled, while the next
+// steps run: per step 4 additions to 32 cycles of matrix core, which two wavefronts a SIMD overlap.
+// In a stage, row r keeps its 16-byte piece c at position c ^ f(r), f(r) = (r / 2) ^ ((r / 4 ^ r / 8) % 2).  LDS serves
+// a 16-byte read 16 lanes at a time: rows 0-3 and 12-15 of one piece with rows 4-11 of its neighbour, then the others.
+// Rows of one parity share a half of the banks, and f puts the eight of them at eight places.
+// Groups past the workgroup's range repeat the last one with a scale of zero; token rows past the block repeat its last
+// row and row tiles past the module its last tile, neither is stored.
+//
+// Where the tiles do not fill the GPU, KH such teams of WM x WN wavefronts share a workgroup: each takes a part of the
+// input groups through a ring of its own, the sums meet in LDS, and a team finishes TT / KH of the token
+// tiles.  With args.ks > 1 the input groups are split over workgroups too: each writes its fp32 tile to the
+// workspace, and fp8_tile_join_kernel adds them in order and finishes.
+typedef __attribute__((address_space(3))) void lds_void;
+template <int I>
+using ic = std::integral_constant<int, I>;
+
+// Column of the launch (row block of a module and K range) and token block of a workgroup: XCD x (workgroups b with
+// b % 8 == x) takes the columns x, x + 8, ..., eight token blocks at a time, so that a column's weights stay in one L2
+// and its workgroups run together.
+__device__ __forceinline__ bool tile_place(const Fp8Args& args, int block, int& mb, int& col) {
+    const int cols = args.row_blocks * args.ks;
+    const int xcd = block & 7, local = block >> 3;
+    const int mine = (cols - xcd + 7) >> 3;  // columns of this XCD
+    if (mine <= 0) return false;
+    const int per = 8 * mine;
+    const int ms = local / per, in = local - ms * per;
+    const int width = min(8, args.m_blocks - 8 * ms);
+    if (width <= 0) return false;
+    const int c = in / width;
+    if (c >= mine) return false;
+    mb = 8 * ms + (in - c * width);
+    col = xcd + 8 * c;
+    return true;
+}
+
+enum : int { kFp8Plain = 0, kFp8Correct = 1, kFp8Split = 2 };  // what follows the sums
+
+template <int WM, int WN, int TT, int KH, int MODE, bool EXPERTS>
+__global__ __launch_bounds__(64 * WM * WN * KH, 2) void fp8_tile_kernel(const Fp8Args args, const Fp8PrepArgs prep,
+                                                                       int join_blocks) {
+    constexpr int RR = 4, NW = WM * WN, BM = 16 * TT * WM, SB = BM * 128;
+    constexpr int NC = BM / 8 / NW;        // 1 KB code copies per wavefront and group
+    constexpr int TE = TT / KH;            // token tiles that a wavefront finishes
+    constexpr int NE = BM / 8 / (NW * KH); // copies per wavefront of a stage that all fill
+    constexpr int CA = 2;                  // groups that the copies are ahead
+    constexpr int WA = TT <= 4 ? 3 : 1;    // and the weights, as registers allow
+    constexpr int WS = WA + 1;             // register slots of a group's weights
+    constexpr int N = 2 * RR + (CA - 1) * (NC + 2 * RR);  // loads behind a copy when its group is due, at least
+    static_assert(NC * 8 * NW == BM && NC % 2 == 0 && N < 64 && BM % 64 == 0 && NE > 0 && TE * KH == TT, "copies");
+    __shared__ __attribute__((aligned(16))) uint8_t st0[KH * SB];
+    __shared__ __attribute__((aligned(16))) uint8_t st1[KH * SB];
+    __shared__ __attribute__((aligned(16))) uint8_t st2[KH * SB];
+    __shared__ __attribute__((aligned(16))) uint8_t st3[KH * SB];
+    // scales [token][4 groups] of a turn of the ring, for its first two groups and for its last two: an array is filled
+    // while the other is read
+    __shared__ __attribute__((aligned(16))) uint8_t sc0[KH * BM * 16];
+    __shared__ __attribute__((aligned(16))) uint8_t sc1[KH * BM * 16];
+    // With a K split the projection is only used by the launch after this one: the first workgroups (a
+    // multiple of 8) join its ranges instead of a launch of their own
+    if constexpr (MODE == kFp8Split) {
+        if ((int)blockIdx.x < join_blocks) {
+            join_ranges(prep, (size_t)blockIdx.x * (64 * NW * KH) + threadIdx.x);
+            return;
+        }
+    }
+    Work wk;
+    int kr = 0, mb = 0;
+    if constexpr (EXPERTS) {
+        if (!expert_work<true>(args, BM, wk)) return;
+    } else {
+        int col;
+        if (!tile_place(args, (int)blockIdx.x - join_blocks, mb, col)) return;
+        const int ks = MODE == kFp8Split ? args.ks : 1;
+        wk.e = 0;
+        wk.rb = col / ks;
+        kr = col - wk.rb * ks;
+        wk.j0 = mb * BM;
+        wk.j1 = min(wk.j0 + BM, args.T);
+    }
+    const Fp8Module& M = args.mod[fp8_module_of(args, wk.rb)];
+    const int lane = threadIdx.x & 63;
+    const int wave_all = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int kh = KH > 1 ? wave_all / NW : 0, wave = KH > 1 ? wave_all % NW : wave_all;  // team, wavefront of it
+    const int wm = wave % WM, wn = wave / WM;
+    const int d = args.d, NT = M.n_tiles16, n_out = M.n_out;
+    const uint8_t* q = M.q + (EXPERTS ? (size_t)wk.e * M.q_step : 0);
+    const int j0 = wk.j0, j1 = wk.j1, rt0 = (wk.rb - M.block_begin) * RR * WN + wn * RR;
+    // groups of the workgroup, and the KH-th part of them, whole turns of the ring, that this team takes (the last may be
+    // shorter, or none)
+    const int n_all = min(args.gk, args.G - kr * args.gk), n_turn = ((n_all + KH - 1) / KH + 3) & ~3;
+    const int g_begin = kr * args.gk + kh * n_turn, n_g = max(0, min(n_turn, n_all - kh * n_turn));
+    const int g_last = min(g_begin + max(n_g, 1), args.G) - 1;
+    // copy i of wave w fills rows 8 (NC w + i) .. + 7 of the stage; lane l lands at row + l / 8, position l % 8, which
+    // holds the row's piece (l % 8) ^ f(row)
+    uint32_t xoff[NC];
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+        const int row = 8 * (NC * wave + i) + (lane >> 3);
+        const uint32_t t = (uint32_t)token_of<EXPERTS>(args, min(j0 + row, j1 - 1));
+        xoff[i] = t * (uint32_t)d + 16 * (uint32_t)((lane & 7) ^ (((row >> 1) & 7) ^ (((row >> 2) ^ (row >> 3)) & 1)));
+    }
+    const int srow = 64 * (wave % (BM / 64)) + lane;  // token row whose scales the lane copies
+    uint32_t soff = (uint32_t)token_of<EXPERTS>(args, min(j0 + srow, j1 - 1)) * (uint32_t)args.gp * 4u;
+    const int lr = lane & 15, fr = (lr >> 1) ^ (((lr >> 2) ^ (lr >> 3)) & 1);
+    const int rbase = (16 * TT * wm + lr) * 128;
+    int rofs0 = rbase + 16 * ((lane >> 4) ^ fr), rofs1 = rbase + 16 * ((4 + (lane >> 4)) ^ fr);
+    int sofs = (kh * BM + 16 * TT * wm + lr) * 16;
+    uint32_t rts[RR];  // the wavefront's row tiles (scalar: weight addresses are scalar but for the lane's 16 bytes)
+#pragma unroll
+    for (int rr = 0; rr < RR; ++rr) rts[rr] = (uint32_t)min(rt0 + rr, NT - 1);
+    const uint32_t lofs = lane * 16;
+    float wsc[2];  // scales of the wavefront's 128-row block, group g_begin + 64 i + lane
+    {
+        const float* sz = M.sz + (EXPERTS ? (size_t)wk.e * M.sz_step : 0) + (size_t)(rts[0] >> 3) * args.G;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) wsc[i] = 64 * i + lane < n_g ? sz[g_begin + 64 * i + lane] : 0.f;
+    }
+
+    auto copy = [&](int v, uint8_t* stg) {
+        const uint8_t* base = args.xq + (size_t)min(g_begin + v, g_last) * kGroup;
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            asm volatile("" : "+v"(xoff[i]));  // one register each: not widened to 64 bits in front of the loop
+            __builtin_amdgcn_global_load_lds((const void*)(base + xoff[i]), (lds_void*)(stg + kh * SB + 8 * (NC * wave + i) * 128),
+                                             16, 0, 0);
+        }
+    };
+    // scales of the groups v .. v + 3 (g_begin and v are multiples of 4; past the row's end the last four again)
+    auto copy_scales = [&](int v, uint8_t* sc) {
+        asm volatile("" : "+v"(soff));
+        const uint8_t* base = reinterpret_cast<const uint8_t*>(args.xs) + (size_t)min(g_begin + v, args.gp - 4) * 4u;
+        __builtin_amdgcn_global_load_lds((const void*)(base + soff),
+                                         (lds_void*)(sc + (kh * BM + 64 * (wave % (BM / 64))) * 16), 16, 0, 0);
+    };
+    i8v w[WS][RR];
+    auto wload = [&](int v, int slot) {
+        const size_t g = (size_t)min(g_begin + v, g_last) * NT;
+#pragma unroll
+        for (int rr = 0; rr < RR; ++rr) {
+            const uint8_t* at = q + (g + rts[rr]) * kFp8Block + lofs;
+            w[slot][rr] = load_operand(at, at + 1024);
+        }
+    };
+    f4 acc[TT][RR];
+#pragma unroll
+    for (int tt = 0; tt < TT; ++tt)
+#pragma unroll
+        for (int rr = 0; rr < RR; ++rr) acc[tt][rr] = f4{0.f, 0.f, 0.f, 0.f};
+
+    // The waits of the ring count the loads behind a copy, so that no operand load may move in front of one: the
+    // barriers keep the order under any scheduling.
+    copy_scales(0, sc0);
+    copy(0, st0);
+    copy(1, st1);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int v = 0; v < WA; ++v) wload(v, v);
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): the first groups are there
+    __builtin_amdgcn_sched_barrier(0);
+
+    // Group v in stage S = v % 4.  At the barrier its copies have landed, and the scales that were requested before them:
+    // after them at least N loads were issued.  The copies of v + CA go to a stage whose last reads were before this
+    // barrier, and so do the scales (at S = 0 this turn's for its last two groups, at S = 2 the next turn's for
+    // its first two); operands go to slots whose last steps were issued.
+    auto step = [&](int v, auto Sc) {
+        constexpr int S = decltype(Sc)::value;
+        uint8_t* const st[4] = {st0, st1, st2, st3};
+        const uint8_t* cur = st[S] + kh * SB;
+        asm volatile("" : "+v"(rofs0), "+v"(rofs1), "+v"(sofs));  // no addresses for every stage in front of the loop
+        const uint8_t* sc = (S < 2 ? sc0 : sc1) + sofs;
+        __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | ((N >> 4) << 14));  // vmcnt(N)
+        __builtin_amdgcn_s_barrier();
+        if constexpr (S == 0) copy_scales(v, sc1);
+        if constexpr (S == 2) copy_scales(v + 2, sc0);
+        __builtin_amdgcn_sched_barrier(0);
+        copy(v + CA, st[(S + CA) & 3]);
+        __builtin_amdgcn_sched_barrier(0);
+        wload(v + WA, (S + WA) % WS);
+        __builtin_amdgcn_sched_barrier(0);
+        const float sw = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v < 64 ? wsc[0] : wsc[1]), v & 63));
+        if constexpr (WA == 1) {  // the group's weights: behind them this step's loads
+            constexpr int H = (S % 2 == 0 ? 1 : 0) + NC + 2 * RR;
+            __builtin_amdgcn_s_waitcnt(0x0F70 | (H & 15) | ((H >> 4) << 14));
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        constexpr int D = 2;  // token tiles whose operands are in flight
+        i8v x[D];
+        float s[D], last = 0.f;
+        f4 p[RR];
+#pragma unroll
+        for (int tt = 0; tt < TT + 1; ++tt) {
+            if (tt == 0) {
+#pragma unroll
+                for (int i = 0; i < D - 1; ++i) {
+                    x[i] = load_operand(cur + rofs0 + i * 2048, cur + rofs1 + i * 2048);
+                    s[i] = *reinterpret_cast<const float*>(sc + i * 256 + 4 * S);
+                }
+            }
+            if (tt + D - 1 < TT) {
+                x[(tt + D - 1) % D] = load_operand(cur + rofs0 + (tt + D - 1) * 2048, cur + rofs1 + (tt + D - 1) * 2048);
+                s[(tt + D - 1) % D] = *reinterpret_cast<const float*>(sc + (tt + D - 1) * 256 + 4 * S);
+            }
+            // tile tt - 1's sums are added just before their registers take tile tt's
+#pragma unroll
+            for (int rr = 0; rr < RR; ++rr) {
+                if (tt > 0) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[tt - 1][rr][i] = fmaf(p[rr][i], last, acc[tt - 1][rr][i]);
+                }
+                if (tt < TT) p[rr] = mfma_fp8(w[S % WS][rr], x[tt % D]);
+            }
+            if (tt < TT) last = s[tt % D] * sw;
+            if (tt > 0 && tt < TT) {
+#pragma unroll
+                for (int rr = 0; rr < RR; ++rr) {
+                    __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    // whole turns of the ring; steps past the range only keep time
+    for (int v = 0; v < n_turn; v += 4) {
+        step(v, ic<0>{});
+        step(v + 1, ic<1>{});
+        step(v + 2, ic<2>{});
+        step(v + 3, ic<3>{});
+    }
+    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): no copy may land in LDS after this
+    __syncthreads();
+    // Team kh finishes token tiles TE kh .. + TE - 1: the others' sums of them come through LDS, past the
+    // first SB bytes of the stages (those are R's).
+    if constexpr (KH > 1) {
+        constexpr int kPiece = TE * RR * 1024, kStage = (KH - 1) * SB / kPiece;
+        static_assert(kStage * kPiece == (KH - 1) * SB && 4 * kStage == KH * NW * (KH - 1), "sums fill the stages");
+        auto piece_at = [&](int to, int from) {
+            const int at_ = (to * NW + wave) * (KH - 1) + (from - to + KH) % KH - 1, at = at_ / kStage;
+            return (at == 0 ? st0 : (at == 1 ? st1 : (at == 2 ? st2 : st3))) + SB + (at_ % kStage) * kPiece + 16 * lane;
+        };
+#pragma unroll
+        for (int to = 0; to < KH; ++to)
+            if (to != kh) {
+                uint8_t* dst = piece_at(to, kh);
+#pragma unroll
+                for (int i = 0; i < TE * RR; ++i) *reinterpret_cast<f4*>(dst + 1024 * i) = acc[to * TE + i / RR][i % RR];
+            }
+        f4 own[TE][RR];
+#pragma unroll
+        for (int to = 0; to < KH; ++to)
+            if (to == kh) {
+#pragma unroll
+                for (int i = 0; i < TE * RR; ++i) own[i / RR][i % RR] = acc[to * TE + i / RR][i % RR];
+            }
+        __syncthreads();
+        // added in the order of the teams, whichever finishes
+#pragma unroll
+        for (int i = 0; i < TE * RR; ++i) {
+            f4 sum = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < KH; ++k)
+                sum += k == kh ? own[i / RR][i % RR] : *reinterpret_cast<const f4*>(piece_at(kh, k) + 1024 * i);
+            acc[i / RR][i % RR] = sum;
+        }
+    }
+    if constexpr (MODE == kFp8Split) {
+        f4* part = reinterpret_cast<f4*>(args.part) +
+                   ((((size_t)mb * args.row_blocks + wk.rb) * args.ks + kr) * NW + wave) * (TT * RR * 64) + kh * (TE * RR * 64);
+#pragma unroll
+        for (int tt = 0; tt < TE; ++tt)
+#pragma unroll
+            for (int rr = 0; rr < RR; ++rr) part[(tt * RR + rr) * 64 + lane] = acc[tt][rr];
+        return;
+    }
+    const int te0 = TT * wm + TE * kh;  // first of the wavefront's token tiles
+    // The correction: R's columns 64 j .. + 63 (128 bytes a token, as a group of codes) go to stage j (r <= 256), A's
+    // operands to registers.  Rows of A past the module and token rows past the block repeat the last one
+    // (their results are not stored); columns of A past r are taken as zero, R's are zero up to rp, a multiple of 64.
+    if constexpr (MODE == kFp8Correct) {
+        const int r = args.r, rp = args.rp;
+        auto r_row = [&](int row) {
+            const int j = min(j0 + row, j1 - 1);
+            return EXPERTS && args.r_by_token ? token_of<EXPERTS>(args, j) : j;
+        };
+        auto rcopy = [&](int j, uint8_t* stg) {
+            if (64 * j >= rp) return;
+            if (args.r_ranges > 0) {  // R as the K ranges' fp32 sums: added in order, rounded once to fp16 here
+                for (int i = threadIdx.x; i < BM * 8; i += 64 * NW * KH) {
+                    const int row = i >> 3, c = i & 7;
+                    *reinterpret_cast<h8*>(stg + row * 128 + 16 * (c ^ ((row >> 1) & 7) ^ (((row >> 2) ^ (row >> 3)) & 1))) =
+                        r_columns(args, r_row(row), 64 * j + 8 * c);
+                }
+                return;
+            }
+            const uint8_t* base = static_cast<const uint8_t*>(args.R) + 128 * j;
+#pragma unroll
+            for (int i = 0; i < NE; ++i) {
+                const int row = 8 * (NE * wave_all + i) + (lane >> 3);
+                const int piece = (lane & 7) ^ ((row >> 1) & 7) ^ (((row >> 2) ^ (row >> 3)) & 1);
+                __builtin_amdgcn_global_load_lds((const void*)(base + (size_t)r_row(row) * rp * 2 + 16 * piece),
+                                                 (lds_void*)(stg + 8 * (NE * wave_all + i) * 128), 16, 0, 0);
+            }
+        };
+        const uint8_t* Ab = reinterpret_cast<const uint8_t*>(M.a + (EXPERTS ? (size_t)wk.e * M.a_step : 0)) + (size_t)rts[0] * 32 * r;
+        rcopy(0, st0);
+        rcopy(1, st1);
+        rcopy(2, st2);
+        rcopy(3, st3);
+        __builtin_amdgcn_s_waitcnt(0x0F70);
+        __syncthreads();
+        int j = 0;
+#pragma unroll 1
+        do {
+            const uint8_t* cur = j == 0 ? st0 : (j == 1 ? st1 : (j == 2 ? st2 : st3));
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                const int c = 64 * j + 32 * m + 8 * (lane >> 4);
+                h8 av[RR];
+#pragma unroll
+                for (int rr = 0; rr < RR; ++rr) {
+                    const uint32_t row = (uint32_t)min((rt0 + rr) * 16 + lr, n_out - 1) - rts[0] * 16;
+                    const u4 bits = *reinterpret_cast<const u4*>(Ab + (row * (uint32_t)r + (uint32_t)min(c, r - 8)) * 2u);
+                    av[rr] = __builtin_bit_cast(h8, c < r ? bits : u4{0u, 0u, 0u, 0u});
+                }
+#pragma unroll
+                for (int tt = 0; tt < TE; ++tt) {
+                    const h8 xv = *reinterpret_cast<const h8*>(cur + (m == 0 ? rofs0 : rofs1) + (TE * kh + tt) * 2048);
+#pragma unroll
+                    for (int rr = 0; rr < RR; ++rr) acc[tt][rr] = mfma16(av[rr], xv, acc[tt][rr]);
+                }
+            }
+        } while (64 * ++j < rp);
+    }
+    // To memory through the wavefront's own part of the (finished) ring: [16 TE tokens][64 rows] fp16, a token's eight
+    // 16-byte pieces p at p ^ (token % 8), then whole 128-byte lines.
+    __syncthreads();
+    constexpr int kPart = 16 * TE * 128, kPer = SB / kPart;
+    static_assert(NW * KH * kPart <= 4 * SB && SB % kPart == 0, "a part per wavefront");
+    const int sel = wave_all / kPer;
+    uint8_t* out = (sel == 0 ? st0 : (sel == 1 ? st1 : (sel == 2 ? st2 : st3))) + (wave_all % kPer) * kPart;
+#pragma unroll
+    for (int tt = 0; tt < TE; ++tt)
+#pragma unroll
+        for (int rr = 0; rr < RR; ++rr) {
+            const f4 v = acc[tt][rr];
+            const h2 lo = {(_Float16)v[0], (_Float16)v[1]}, hi = {(_Float16)v[2], (_Float16)v[3]};
+            const int p = 2 * rr + (lane >> 5);
+            *reinterpret_cast<u2*>(out + (16 * tt + lr) * 128 + 16 * (p ^ (lane & 7)) + 8 * ((lane >> 4) & 1)) =
+                u2{as_u32(lo), as_u32(hi)};
+        }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    const int row0 = rt0 * 16 + 8 * (lane & 7);
+    const bool vec = (n_out & 7) == 0 && row0 + 7 < n_out;
+#pragma unroll 4
+    for (int i = 0; i < 2 * TE; ++i) {
+        const int tl = 8 * i + (lane >> 3), j = j0 + 16 * te0 + tl;
+        const uint8_t* piece = out + tl * 128 + 16 * ((lane & 7) ^ (tl & 7));
+        if (j >= j1) continue;
+        _Float16* y = M.y + (size_t)j * n_out + row0;
+        if (vec) *reinterpret_cast<h8*>(y) = *reinterpret_cast<const h8*>(piece);
+        else {
+#pragma unroll 1
+            for (int e = 0; e < min(8, n_out - row0); ++e) y[e] = reinterpret_cast<const _Float16*>(piece)[e];
+        }
+    }
+}
+
+// Sums of the K ranges of one 16-token x 64-row piece per wavefront (pieces numbered as the tile kernel stores
+// them), in order, correction, one rounding to fp16.
+template <int WM, int WN, int TT>
+__global__ __launch_bounds__(256) void fp8_tile_join_kernel(const Fp8Args args, int pieces) {
+    constexpr int RR = 4, NW = WM * WN;
+    const int lane = threadIdx.x & 63;
+    const int piece = (int)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    if (piece >= pieces) return;
+    const int ks = args.ks, cols = args.row_blocks;
+    const int tt = piece % TT, wave = piece / TT % NW, tile = piece / TT / NW;
+    const int mb = tile / cols, rb = tile - mb * cols;
+    const Fp8Module& M = args.mod[fp8_module_of(args, rb)];
+    const int rt0 = (rb - M.block_begin) * RR * WN + (wave / WM) * RR;
+    const int t = (mb * WM + wave % WM) * 16 * TT + 16 * tt + (lane & 15);
+    if (rt0 >= M.n_tiles16) return;
+    const bool ok = t < args.T;
+    const f4* part = reinterpret_cast<const f4*>(args.part);
+    f4 v[RR];
+#pragma unroll
+    for (int rr = 0; rr < RR; ++rr) v[rr] = f4{0.f, 0.f, 0.f, 0.f};
+    for (int k = 0; k < ks; ++k) {
+        const f4* p = part + ((((size_t)tile * ks + k) * NW + wave) * TT + tt) * (RR * 64) + lane;
+#pragma unroll
+        for (int rr = 0; rr < RR; ++rr) v[rr] += p[rr * 64];
+    }
+    if (args.r > 0) {
+        const int r = args.r, rp = args.rp;
+        const h8 zero8 = {0, 0, 0, 0, 0, 0, 0, 0};
+        for (int kb = 0; kb < rp / 32; ++kb) {
+            const int c = 32 * kb + 8 * (lane >> 4);
+            const h8 bv = r_columns(args, ok ? t : 0, c);
+#pragma unroll
+            for (int rr = 0; rr < RR; ++rr) {
+                const int row = (rt0 + rr) * 16 + (lane & 15);
+                const h8 av = (row < M.n_out && c < r) ? load_h8(M.a + (size_t)row * r + c) : zero8;
+                v[rr] = mfma16(av, bv, v[rr]);
+            }
+        }
+    }
+    if (!ok) return;
+#pragma unroll
+    for (int rr = 0; rr < RR; ++rr)
+        if (rt0 + rr < M.n_tiles16) store_rows(M, t, (rt0 + rr) * 16 + 4 * (lane >> 4), v[rr]);
 }
 
 }  // namespace
@@ -378,8 +808,51 @@ static hipError_t launch_fp8_split(const Fp8Args& a, int64_t items, hipStream_t 
     return hipGetLastError();
 }
 
-hipError_t launch_fp8(const Fp8Args& a, int64_t items, hipStream_t stream) {
-    return a.offsets != nullptr ? launch_fp8_split<true>(a, items, stream) : launch_fp8_split<false>(a, items, stream);
+// Every XCD takes an eighth of the work, rounded up; workgroups without any return at once.
+template <int WM, int WN, int TT>
+static hipError_t launch_fp8_experts(const Fp8Args& a, const Fp8PrepArgs& p, int64_t items, hipStream_t stream) {
+    const dim3 grid((unsigned)(8 * ceil_div(items, 8))), block(64 * WM * WN);
+    if (a.r > 0) hipLaunchKernelGGL((fp8_tile_kernel<WM, WN, TT, 1, kFp8Correct, true>), grid, block, 0, stream, a, p, 0);
+    else hipLaunchKernelGGL((fp8_tile_kernel<WM, WN, TT, 1, kFp8Plain, true>), grid, block, 0, stream, a, p, 0);
+    return hipGetLastError();
+}
+
+// SPLIT: the tile takes K ranges.
+template <int WM, int WN, int TT, int KH, bool SPLIT>
+static hipError_t launch_fp8_tile(const Fp8Args& a, const Fp8PrepArgs& p, hipStream_t stream) {
+    const int64_t join = a.ks > 1 && a.r > 0 && p.part != nullptr
+                             ? ceil_div(ceil_div((int64_t)p.T * p.rp / 4, 64 * WM * WN * KH), 8) * 8 : 0;
+    const int64_t grid = join + 8 * ceil_div((int64_t)a.row_blocks * a.ks, 8) * a.m_blocks;
+    if (grid * 64 * WM * WN * KH > (int64_t)UINT32_MAX) return hipErrorInvalidConfiguration;
+    const dim3 g((unsigned)grid), block(64 * WM * WN * KH);
+    if constexpr (SPLIT) {
+        if (a.ks > 1) {
+            hipLaunchKernelGGL((fp8_tile_kernel<WM, WN, TT, KH, kFp8Split, false>), g, block, 0, stream, a, p, (int)join);
+            const hipError_t e = hipGetLastError();
+            if (e != hipSuccess) return e;
+            const int pieces = a.m_blocks * a.row_blocks * WM * WN * TT;
+            hipLaunchKernelGGL((fp8_tile_join_kernel<WM, WN, TT>), dim3((unsigned)ceil_div(pieces, 4)), dim3(256), 0, stream, a,
+                               pieces);
+            return hipGetLastError();
+        }
+    }
+    if (a.ks > 1) return hipErrorInvalidValue;
+    if (a.r > 0) hipLaunchKernelGGL((fp8_tile_kernel<WM, WN, TT, KH, kFp8Correct, false>), g, block, 0, stream, a, p, 0);
+    else hipLaunchKernelGGL((fp8_tile_kernel<WM, WN, TT, KH, kFp8Plain, false>), g, block, 0, stream, a, p, 0);
+    return hipGetLastError();
+}
+
+hipError_t launch_fp8(const Fp8Args& a, const Fp8PrepArgs& p, int64_t items, hipStream_t stream) {
+    if (a.offsets != nullptr) {
+        if (a.rr == 16) return launch_fp8_experts<1, 4, 8>(a, p, items, stream);
+        if (a.rr == 8 && a.tt == 8) return launch_fp8_experts<2, 2, 4>(a, p, items, stream);
+        return launch_fp8_split<true>(a, items, stream);
+    }
+    if (a.rr == 16) return launch_fp8_tile<1, 4, 8, 1, false>(a, p, stream);
+    if (a.rr == 8 && a.tt == 8)
+        return a.kh == 2 ? launch_fp8_tile<2, 2, 4, 2, true>(a, p, stream) : launch_fp8_tile<2, 2, 4, 1, false>(a, p, stream);
+    if (a.rr == 8) return launch_fp8_tile<1, 2, 4, 4, true>(a, p, stream);
+    return launch_fp8_split<false>(a, items, stream);
 }
 
 }  // namespace glowq

@@ -64,7 +64,7 @@ SHAPES = [(1, 128, [16], 0), (1, 256, [1], 8), (1, 4096, [520, 17, 130], 64), (2
           (48, 2176, [300], 128), (64, 1024, [1024, 512, 512], 64), (65, 256, [48, 32], 16), (130, 384, [300, 200], 40),
           (300, 512, [2048, 2048], 128), (8, 2048, [64], 256), (257, 896, [1030, 515], 64), (513, 128, [770], 256),
           (77, 14336, [128], 64), (40, 8192, [256], 8), (70, 2048, [130, 250], 64), (129, 4096, [640], 72), (1025, 640, [300], 0),
-          (129, 1280, [4096, 20], 24), (300, 16384, [160], 8)]
+          (129, 1280, [4096, 20], 24), (300, 16384, [160], 8), (2100, 256, [4000], 24), (1400, 640, [2100, 2500, 1301], 0)]
 
 
 @pytest.mark.parametrize("idx", range(len(SHAPES)), ids=[f"T{s[0]}_d{s[1]}_m{len(s[2])}_r{s[3]}" for s in SHAPES])
