@@ -17,12 +17,13 @@
 // fp32 value widened (exactly, which leaves 29 bits), the expert in the low 8, so that one maximum finds value and
 // lowest expert at once; then the best of the list heads leaves top_k times.  16 lanes serve up to 8 choices, 64 more.
 // Decisions are those of exact arithmetic: logits are compared as they are.  Where scores decide (a bias, or
-// groups by two scores) they are fp32 values within 2^-19 (1 + |value|) of the exact ones (exp and the quotient a few
-// steps of 2^-24, a sum over E one step for each of its up to 20 additions in a row), so two values further apart
-// than 2^-18 (1 + |value|) are in their exact order; a token with a closer pair at any place that matters is
-// decided again in fp64.
+// groups by two scores) they are fp32 values a little off the exact ones, in steps of 2^-24:
+//   sigmoid  exp is off by 2 |l| + 4 steps of itself (its argument's rounding, its own), which moves s by s (1 - s) of
+//            that, 1.5 at most; the quotient and the product add 3, the bias one of the value: 6 + |v|
+//   softmax  exp as above, and the sum by one for each of its 20 additions in a row at most, all of s: 32 + |v|
+// So two values further apart than 2^-20 (1 + |v|), or 2^-18 (1 + |v|), are in their exact order, and two sums of two
+// at twice that; a token with a closer pair at a place that matters is decided again in fp64.
 #include <algorithm>
-#include <type_traits>
 
 #include "glowq.h"
 #include "layer.h"
@@ -32,7 +33,6 @@ namespace glowq {
 namespace {
 
 constexpr int kRouteThreads = 256;
-constexpr float kClose = 0x1p-18f;
 constexpr double kOut = -1.7e308;  // key of an expert that is out; every value's key is above
 
 // Rotation of the 16-lane row by N.
@@ -106,100 +106,124 @@ __device__ __forceinline__ F sigmoid_of(F l) {
     return l >= (F)0 ? q : e * q;
 }
 
+// How near two values may be before fp64 decides (above), for values v about 1 + |v| large.
+__device__ __forceinline__ float close_to(const RouteArgs& a) { return a.score == GLOWQ_SCORE_SIGMOID ? 0x1p-20f : 0x1p-18f; }
+
 // Standings of the groups from the token's values `by` [E] in LDS (-inf: out): bit g of the answer is set where group g
 // stays.  `near`: two groups are closer than fp32 scores tell apart.
 template <int L, typename F>
-__device__ uint32_t groups_that_stay(const F* by, const RouteArgs& a, int i, bool& near) {
+__device__ __forceinline__ uint32_t groups_that_stay(const F* by, const RouteArgs& a, int i, bool& near) {
     const int n = a.n_exp / a.n_group;
     F b1 = (F)-INFINITY, b2 = (F)-INFINITY;
-    if (i < a.n_group)
+    if (i < a.n_group) {
+        int at = i < n ? i : 0;  // starts spread over the LDS banks
+#pragma unroll 4
         for (int q = 0; q < n; ++q) {
-            const int at = q + i < n ? q + i : (q + i) % n;  // starts spread over the LDS banks
             const F v = by[i * n + at];
+            at = at + 1 == n ? 0 : at + 1;
             b2 = fmax(b2, fmin(b1, v));
             b1 = fmax(b1, v);
         }
+    }
     const F stand = a.group_best == 2 && b2 > (F)-INFINITY ? b1 + b2 : b1;
     int rank = 0;
-    bool close = false;
+#pragma unroll 4
     for (int h = 0; h < a.n_group; ++h) {
         const F other = __shfl(stand, h, L);
-        if (h == i) continue;
         rank += other > stand || (other == stand && h < i) ? 1 : 0;
-        close |= fabs(other - stand) <= (F)kClose * ((F)1 + fabs(stand));  // (-inf from -inf: NaN, not close)
     }
-    near = lanes_with<L>(close && i < a.n_group) != 0;
+    // the last group that stays and the first that does not (-inf from -inf: NaN, not near)
+    const uint64_t last = lanes_with<L>(i < a.n_group && rank == a.keep_groups - 1);
+    const uint64_t next = lanes_with<L>(i < a.n_group && rank == a.keep_groups);
+    const F in = __shfl(stand, __ffsll((unsigned long long)last) - 1, L), out = __shfl(stand, __ffsll((unsigned long long)next) - 1, L);
+    near = next != 0 && in - out <= (F)(2.f * close_to(a)) * ((F)1 + fabs(in));
     return (uint32_t)lanes_with<L>(rank < a.keep_groups && i < a.n_group);
 }
 
 // Expert e's group stays.  e / n without a division: e < 256, 1 <= n <= 256.
 __device__ __forceinline__ bool stays(uint32_t mask, int e, uint32_t inv) { return mask >> ((e * inv) >> 16) & 1u; }
 
-// The choice of one token in fp64, by the definition: the lanes that hold it call it together.  v: its logits, lane i's
-// expert j at e = i + L j.  Lane j < top_k gets the j-th expert.  At its end no lane reads `by` any more.
-template <int L, int EPL>
-__device__ __forceinline__ int choose_exact(const float (&v)[EPL], const RouteArgs& a, double* by, int i) {
-    double s[EPL], u[EPL];
-    double top = -INFINITY, sum = 0.0;
+// 1 / v to the last bits of fp64, without a division's special cases (v in 1 .. 2).
+__device__ __forceinline__ double inverse(double v) {
+    double r = __builtin_amdgcn_rcp(v);
+    r = fma(fma(-v, r, 1.0), r, r);
+    return fma(fma(-v, r, 1.0), r, r);
+}
+
+// The choice of one token in fp64, by the definition.  The whole wavefront calls it, whatever number of lanes share a
+// token else: it is rare (under one token in a hundred) but has to be short, since its wavefront ends last.
+// row: the token's logits, `by` [E] its LDS.  Lane j < top_k gets the j-th expert.
+template <typename S>
+__device__ __forceinline__ int choose_exact(const S* row, const RouteArgs& a, double* by) {
+    constexpr int M = GLOWQ_MOE_MAX_EXPERTS / 64;
+    const int lane = threadIdx.x & 63, E = a.n_exp;
+    const bool softmax = a.score == GLOWQ_SCORE_SOFTMAX;
+    float v[M], b[M], most = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) top = fmax(top, (double)v[j]);
-    top = lanes_max<L>(top);
+    for (int j = 0; j < M; ++j) {
+        const int e = lane + 64 * j;
+        v[j] = e < E ? (float)row[e] : -INFINITY;
+        b[j] = a.bias != nullptr && e < E ? a.bias[e] : 0.f;
+        most = fmaxf(most, v[j]);
+    }
+    const double top = lanes_max<64>(most);
+    double s[M], u[M], sum = 0.0;
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) {
-        s[j] = v[j] == -INFINITY ? 0.0 : (a.score == GLOWQ_SCORE_SIGMOID ? sigmoid_of((double)v[j]) : exp((double)v[j] - top));
+    for (int j = 0; j < M; ++j) {
+        const double l = (double)v[j], x = exp(softmax ? l - top : -fabs(l));
+        s[j] = v[j] == -INFINITY ? 0.0 : (softmax ? x : (v[j] >= 0.f ? inverse(1.0 + x) : x * inverse(1.0 + x)));
         sum += s[j];
     }
-    if (a.score == GLOWQ_SCORE_SOFTMAX) {
-        sum = lanes_sum<L>(sum);
+    sum = softmax ? lanes_sum<64>(sum) : 1.0;
 #pragma unroll
-        for (int j = 0; j < EPL; ++j) s[j] = s[j] / sum;
-    }
-    uint32_t mask = ~0u, inv = 0;
-#pragma unroll
-    for (int j = 0; j < EPL; ++j) {
-        const int e = i + L * j;
-        if (a.bias != nullptr && e < a.n_exp) s[j] += (double)a.bias[e];
-        if (v[j] == -INFINITY) s[j] = -INFINITY;
+    for (int j = 0; j < M; ++j) {
+        if (softmax) s[j] /= sum;
+        s[j] = v[j] == -INFINITY ? -INFINITY : s[j] + (double)b[j];
         u[j] = a.bias != nullptr ? s[j] : (double)v[j];
     }
     if (a.keep_groups < a.n_group) {
 #pragma unroll
-        for (int j = 0; j < EPL; ++j)
-            if (i + L * j < a.n_exp) by[i + L * j] = a.group_best == 2 ? s[j] : u[j];
+        for (int j = 0; j < M; ++j)
+            if (lane + 64 * j < E) by[lane + 64 * j] = a.group_best == 2 ? s[j] : u[j];
         wave_sync();
         bool near;
-        mask = groups_that_stay<L>(by, a, i, near);
+        const uint32_t mask = groups_that_stay<64>(by, a, lane, near);
         wave_sync();
-        inv = (65535u + (uint32_t)(a.n_exp / a.n_group)) / (uint32_t)(a.n_exp / a.n_group);
+        const uint32_t inv = (65535u + (uint32_t)(E / a.n_group)) / (uint32_t)(E / a.n_group);
+#pragma unroll
+        for (int j = 0; j < M; ++j)
+            if (lane + 64 * j < E && !stays(mask, lane + 64 * j, inv)) u[j] = -INFINITY;
     }
     int mine = -1;
+#pragma unroll 1
     for (int r = 0; r < a.top_k; ++r) {
-        double best = -INFINITY;
-        int at = 1 << 20;
+        double best = u[0];
 #pragma unroll
-        for (int j = 0; j < EPL; ++j) {  // ascending experts: the first of equal values stays
-            const int e = i + L * j;
-            if (u[j] > best && (inv == 0 || stays(mask, e, inv))) best = u[j], at = e;
+        for (int j = 1; j < M; ++j) best = fmax(best, u[j]);
+        best = lanes_max<64>(best);
+        if (best == -INFINITY) break;
+        int at = 0;  // the lowest expert that has it
+#pragma unroll
+        for (int j = M - 1; j >= 0; --j) {
+            const uint64_t who = __ballot(u[j] == best);
+            if (who != 0) at = 64 * j + __ffsll((unsigned long long)who) - 1;
         }
 #pragma unroll
-        for (int off = L / 2; off > 0; off >>= 1) {
-            const double ob = __shfl_xor(best, off, L);
-            const int oa = __shfl_xor(at, off, L);
-            if (ob > best || (ob == best && oa < at)) best = ob, at = oa;
-        }
-#pragma unroll
-        for (int j = 0; j < EPL; ++j)
-            if (i + L * j == at) u[j] = -INFINITY;
-        if (i == r) mine = best == -INFINITY ? -1 : at;
+        for (int j = 0; j < M; ++j)
+            if (lane + 64 * j == at) u[j] = -INFINITY;
+        if (lane == r) mine = at;
     }
     return mine;
 }
 
 // SCORED: scores decide (a bias, or groups by two scores).
 template <typename S, int L, int EPL, int KL, bool SCORED>
-__global__ __launch_bounds__(kRouteThreads) void route_kernel(const RouteArgs a) {
+__global__ __launch_bounds__(kRouteThreads, 6) void route_kernel(const RouteArgs a) {
     constexpr int TB = kRouteThreads / L;
-    __shared__ typename std::conditional<SCORED, double, float>::type by_all[TB][L * EPL];  // a token's values, fp32 or fp64
+    // values of each token, and when those are used up, of one token of a wavefront in fp64
+    constexpr int W = TB / (kRouteThreads / 64), kEach = SCORED && L * EPL * W < 2 * GLOWQ_MOE_MAX_EXPERTS
+                                                             ? 2 * GLOWQ_MOE_MAX_EXPERTS / W : L * EPL;
+    __shared__ __attribute__((aligned(16))) float by_all[TB][kEach];
     const int i = threadIdx.x % L, slot = threadIdx.x / L;
     const int t = blockIdx.x * TB + slot;
     const bool live = t < a.T;
@@ -232,14 +256,14 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(const RouteArgs a)
     float u[EPL];
     if constexpr (SCORED) {
         const float rs = 1.f / sum;
-        float* by = reinterpret_cast<float*>(by_all[slot]);
+        float* by = by_all[slot];
 #pragma unroll
         for (int j = 0; j < EPL; ++j) {
             float s;
             if (softmax) {
                 s = __expf(v[j] - top) * rs;
             } else {
-                const float x = __expf(-fabsf(v[j])), q = 1.f / (1.f + x);
+                const float x = __expf(-fabsf(v[j])), q = __builtin_amdgcn_rcpf(1.f + x);
                 s = v[j] >= 0.f ? q : x * q;
             }
             s += b[j];
@@ -251,13 +275,13 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(const RouteArgs a)
 #pragma unroll
         for (int j = 0; j < EPL; ++j) {
             u[j] = v[j];
-            if (groups && i + L * j < E) reinterpret_cast<float*>(by_all[slot])[i + L * j] = v[j];
+            if (groups && i + L * j < E) by_all[slot][i + L * j] = v[j];
         }
     }
     if (groups) {
         wave_sync();
         bool close;
-        mask = groups_that_stay<L>(reinterpret_cast<const float*>(by_all[slot]), a, i, close);
+        mask = groups_that_stay<L>(static_cast<const float*>(by_all[slot]), a, i, close);
         near = SCORED && close;
         inv = (65535u + (uint32_t)(E / a.n_group)) / (uint32_t)(E / a.n_group);
         wave_sync();
@@ -289,14 +313,22 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(const RouteArgs a)
         }
         if (SCORED && a.bias != nullptr && r > 0 && best > kOut) {
             const float hi = key_value(last), lo = key_value(best);
-            near |= hi - lo <= kClose * (1.f + fabsf(hi));
+            near |= hi - lo <= close_to(a) * (1.f + fabsf(hi));
         }
         last = best;
         if (i == r) mine = best;
     }
     int e = mine > kOut ? key_expert(mine) : -1;
     if constexpr (SCORED) {
-        if (near) e = choose_exact<L, EPL>(v, a, by_all[slot], i);
+        // one token after another, all lanes for each
+        for (uint64_t todo = __ballot(near && live && i == 0); todo != 0; todo &= todo - 1) {
+            const int first = __ffsll((unsigned long long)todo) - 1;  // its first lane
+            const int who = ((int)threadIdx.x & ~63) / L + first / L;
+            const int got = choose_exact(static_cast<const S*>(a.logits) + (size_t)(blockIdx.x * TB + who) * E, a,
+                                         reinterpret_cast<double*>(by_all[((int)threadIdx.x & ~63) / L]));
+            const int mine_now = __shfl(got, i, 64);
+            if (slot == who) e = mine_now;
+        }
     }
     if (bad || i >= K) e = -1;
     // weights: lane j has the j-th expert
@@ -408,8 +440,8 @@ template <typename S>
 hipError_t launch_route_t(const RouteArgs& a, hipStream_t stream) {
     if (a.top_k > 8) return launch_route_n<S, 64, 4, 4>(a, stream);
     if (a.n_exp <= 64) return launch_route_n<S, 16, 4, 4>(a, stream);
-    if (a.n_exp <= 128) return a.top_k <= 4 ? launch_route_n<S, 16, 8, 4>(a, stream) : launch_route_n<S, 16, 8, 8>(a, stream);
-    return a.top_k <= 4 ? launch_route_n<S, 16, 16, 4>(a, stream) : launch_route_n<S, 16, 16, 8>(a, stream);
+    if (a.n_exp <= 128) return a.top_k <= 4 ? launch_route_n<S, 16, 8, 5>(a, stream) : launch_route_n<S, 16, 8, 8>(a, stream);
+    return a.top_k <= 4 ? launch_route_n<S, 16, 16, 5>(a, stream) : launch_route_n<S, 16, 16, 9>(a, stream);
 }
 
 template <typename S>

@@ -157,13 +157,15 @@ __global__ __launch_bounds__(norm_threads<TPR>()) void norm_kernel(const S* x, c
     }
 }
 
+constexpr int kBackThreads = 1024;
+
 // part [gridDim.x][2][d]: the workgroup's sums of dy xhat and dy, its teams' added in order.
 template <typename S, int TPR, int V, bool NT>
-__global__ __launch_bounds__(norm_threads<TPR>()) void norm_backward_kernel(const S* dy, const S* x, const float* __restrict__ mean,
+__global__ __launch_bounds__(kBackThreads) void norm_backward_kernel(const S* dy, const S* x, const float* __restrict__ mean,
                                                                             const float* __restrict__ rstd,
                                                                             const S* __restrict__ w, int T, int d, S* dx,
                                                                             float* __restrict__ part) {
-    constexpr int N = Piece<S>::N, P = V / N, B = norm_threads<TPR>(), RG = B / TPR;
+    constexpr int N = Piece<S>::N, P = V / N, B = kBackThreads, RG = B / TPR;
     __shared__ float slots[2][B / 64 * 2];
     __shared__ float cols[RG > 1 ? B * N : 1];
     const int sub = threadIdx.x % TPR, team = threadIdx.x / TPR;
@@ -187,13 +189,15 @@ __global__ __launch_bounds__(norm_threads<TPR>()) void norm_backward_kernel(cons
         m = mean[row];
         r = rstd[row];
     };
+    constexpr bool kAhead = V <= 8;  // the next row requested before this one is used, as registers allow
     int turn = 0;
-    load(blockIdx.x * RG + team, vx, vg, mu, rs);
+    if (kAhead) load(blockIdx.x * RG + team, vx, vg, mu, rs);
     for (int row0 = blockIdx.x * RG; row0 < T; row0 += gridDim.x * RG, turn ^= 1) {
         const int row = row0 + team;
         Piece<S> nx[P], ng[P];
         float nm = 0.f, nr = 0.f;
-        if (row0 + (int)gridDim.x * RG < T) load(row + gridDim.x * RG, nx, ng, nm, nr);
+        if (!kAhead) load(row, vx, vg, mu, rs);
+        else if (row0 + (int)gridDim.x * RG < T) load(row + gridDim.x * RG, nx, ng, nm, nr);
         float s[2] = {0.f, 0.f};
 #pragma unroll
         for (int p = 0; p < P; ++p)
@@ -226,37 +230,36 @@ __global__ __launch_bounds__(norm_threads<TPR>()) void norm_backward_kernel(cons
                 store_piece<S, NT>(out, (p * TPR + sub) * N, d, o);
             }
         }
+        if (kAhead) {
 #pragma unroll
-        for (int p = 0; p < P; ++p) vx[p] = nx[p], vg[p] = ng[p];
-        mu = nm;
-        rs = nr;
+            for (int p = 0; p < P; ++p) vx[p] = nx[p], vg[p] = ng[p];
+            mu = nm;
+            rs = nr;
+        }
     }
     if (part == nullptr) return;
     float* mine = part + (size_t)blockIdx.x * 2 * d;
+    constexpr int C = TPR * N;  // columns of one piece of every thread of a team
 #pragma unroll
     for (int which = 0; which < 2; ++which)
 #pragma unroll
         for (int p = 0; p < P; ++p) {
-            const int col = (p * TPR + sub) * N;
-            float v[N];
+            const float* v = (which == 0 ? aw : ab) + p * N;
+            if constexpr (RG == 1) {
 #pragma unroll
-            for (int k = 0; k < N; ++k) v[k] = which == 0 ? aw[p * N + k] : ab[p * N + k];
-            if constexpr (RG > 1) {
+                for (int k = 0; k < N; ++k)
+                    if ((p * TPR + sub) * N + k < d) mine[(size_t)which * d + (p * TPR + sub) * N + k] = v[k];
+            } else {
                 __syncthreads();
 #pragma unroll
                 for (int k = 0; k < N; ++k) cols[threadIdx.x * N + k] = v[k];
                 __syncthreads();
-                if (team == 0) {
-#pragma unroll
-                    for (int t = 1; t < RG; ++t)
-#pragma unroll
-                        for (int k = 0; k < N; ++k) v[k] += cols[(t * TPR + sub) * N + k];
+                for (int c = threadIdx.x; c < C && p * C + c < d; c += B) {
+                    float s = cols[c];
+#pragma unroll 4
+                    for (int t = 1; t < RG; ++t) s += cols[t * C + c];
+                    mine[(size_t)which * d + p * C + c] = s;
                 }
-            }
-            if (team == 0) {
-#pragma unroll
-                for (int k = 0; k < N; ++k)
-                    if (col + k < d) mine[(size_t)which * d + col + k] = v[k];
             }
         }
 }
@@ -302,7 +305,7 @@ hipError_t launch_norm_n(const NormArgs& a, hipStream_t stream) {
 
 template <typename S, int TPR, int V>
 hipError_t launch_norm_backward_n(const NormArgs& a, hipStream_t stream) {
-    constexpr int B = norm_threads<TPR>(), RG = B / TPR;
+    constexpr int B = kBackThreads, RG = B / TPR;
     const int grid = (int)std::min<int64_t>(ceil_div(a.T, RG), kNormParts);
     const S *dy = static_cast<const S*>(a.dy), *x = static_cast<const S*>(a.x), *w = static_cast<const S*>(a.w);
     if ((int64_t)a.T * a.d * (int64_t)sizeof(S) > kStreamBytes)
@@ -318,25 +321,33 @@ hipError_t launch_norm_backward_n(const NormArgs& a, hipStream_t stream) {
     return hipGetLastError();
 }
 
-template <typename S, bool BACK>
+template <typename S>
 hipError_t launch_norm_t(const NormArgs& a, hipStream_t stream) {
-#define GLOWQ_NORM(TPR, V) (BACK ? launch_norm_backward_n<S, TPR, V>(a, stream) : launch_norm_n<S, TPR, V>(a, stream))
-    if (a.d <= 128) return GLOWQ_NORM(16, 8);
-    if (a.d <= 256) return GLOWQ_NORM(16, 16);
-    if (a.d <= 512) return GLOWQ_NORM(64, 8);
-    if (a.d <= 1024) return GLOWQ_NORM(64, 16);
-    if (a.d <= 2048) return GLOWQ_NORM(256, 8);
-    if (a.d <= 4096) return GLOWQ_NORM(256, 16);
-    if (a.d <= 8192) return GLOWQ_NORM(512, 16);
-    if (a.d <= kNormMaxD) return GLOWQ_NORM(512, 32);
-#undef GLOWQ_NORM
-    return hipErrorInvalidValue;
+    if (a.d <= 128) return launch_norm_n<S, 16, 8>(a, stream);
+    if (a.d <= 256) return launch_norm_n<S, 16, 16>(a, stream);
+    if (a.d <= 512) return launch_norm_n<S, 64, 8>(a, stream);
+    if (a.d <= 1024) return launch_norm_n<S, 64, 16>(a, stream);
+    if (a.d <= 2048) return launch_norm_n<S, 256, 8>(a, stream);
+    if (a.d <= 4096) return launch_norm_n<S, 256, 16>(a, stream);
+    if (a.d <= 8192) return launch_norm_n<S, 512, 16>(a, stream);
+    return launch_norm_n<S, 512, 32>(a, stream);
+}
+
+template <typename S>
+hipError_t launch_norm_backward_t(const NormArgs& a, hipStream_t stream) {
+    if (a.d <= 128) return launch_norm_backward_n<S, 16, 8>(a, stream);
+    if (a.d <= 512) return launch_norm_backward_n<S, 64, 8>(a, stream);
+    if (a.d <= 1024) return launch_norm_backward_n<S, 128, 8>(a, stream);
+    if (a.d <= 2048) return launch_norm_backward_n<S, 256, 8>(a, stream);
+    if (a.d <= 4096) return launch_norm_backward_n<S, 512, 8>(a, stream);
+    if (a.d <= 8192) return launch_norm_backward_n<S, 1024, 8>(a, stream);
+    return launch_norm_backward_n<S, 1024, 16>(a, stream);
 }
 
 }  // namespace
 
 hipError_t launch_layer_norm(const NormArgs& a, int32_t dtype, hipStream_t stream) {
-    return dtype == GLOWQ_DTYPE_F16 ? launch_norm_t<_Float16, false>(a, stream) : launch_norm_t<float, false>(a, stream);
+    return dtype == GLOWQ_DTYPE_F16 ? launch_norm_t<_Float16>(a, stream) : launch_norm_t<float>(a, stream);
 }
 
 hipError_t launch_layer_norm_backward(const NormArgs& a, int32_t dtype, hipStream_t stream) {
@@ -345,7 +356,7 @@ hipError_t launch_layer_norm_backward(const NormArgs& a, int32_t dtype, hipStrea
                            stream, a.part, 0, a.d, a.dw, a.db);
         return hipGetLastError();
     }
-    return dtype == GLOWQ_DTYPE_F16 ? launch_norm_t<_Float16, true>(a, stream) : launch_norm_t<float, true>(a, stream);
+    return dtype == GLOWQ_DTYPE_F16 ? launch_norm_backward_t<_Float16>(a, stream) : launch_norm_backward_t<float>(a, stream);
 }
 
 }  // namespace glowq
