@@ -11,7 +11,7 @@
 // exact ones at that of the rounding to fp16 (2.1e-4); fp32 throughout would cost the step at half the rate (16x16x32).
 // A group with an infinity or a NaN has scale NaN: the token's results are NaN.
 //
-// Weight layout: G x NT blocks of 2048 bytes, block (g, rt) at (g NT + rt) 2048 holding rows 16 rt .. + 15 and
+// Weight layout: NT x G blocks of 2048 bytes, block (rt, g) at (rt G + g) 2048 holding rows 16 rt .. + 15 and
 // inputs 128 g .. + 127 as two 1024-byte halves: half m, lane l (16 bytes at 1024 m + 16 l) is row 16 rt + l % 16, inputs
 // 128 g + 64 m + 16 (l / 16) .. + 15.  A lane's 32 bytes of the step's operand are its pieces of both halves; the
 // activation operand takes the same inputs in the same places, so the order of inputs inside the step does not matter.
@@ -41,10 +41,10 @@ __device__ __forceinline__ f4 mfma_fp8(const i8v& w, const i8v& x) {
 
 // --------------------------------------------------------------------- load step
 // One workgroup per (128-input group, row tile): 128 threads, each one lane's 16 bytes.  NaN codes (0x7F, 0xFF) are reported.
-__global__ __launch_bounds__(128) void repack_fp8_kernel(const uint8_t* __restrict__ codes, int64_t n_out, int64_t k_in, int nt,
+__global__ __launch_bounds__(128) void repack_fp8_kernel(const uint8_t* __restrict__ codes, int64_t n_out, int64_t k_in, int groups,
                                                          uint8_t* __restrict__ q, int32_t* __restrict__ flag) {
-    const int64_t blk = blockIdx.x;  // g nt + rt
-    const int64_t g = blk / nt, rt = blk - g * nt;
+    const int64_t blk = blockIdx.x;  // rt G + g
+    const int64_t rt = blk / groups, g = blk - rt * groups;
     const int m = threadIdx.x >> 6, l = threadIdx.x & 63;
     const int64_t row = 16 * rt + (l & 15);
     u4 v = {0u, 0u, 0u, 0u};
@@ -268,10 +268,9 @@ __global__ __launch_bounds__(64 * kFp8Waves) void fp8_split_kernel(const Fp8Args
 #pragma unroll
     for (int rr = 0; rr < RR; ++rr) {
         const int rt = min(rt0 + rr, nt16 - 1);
-        qp[rr] = q + (size_t)rt * kFp8Block + lane * 16;
+        qp[rr] = q + (size_t)rt * G * kFp8Block + lane * 16;
         sp[rr] = sz + (size_t)(rt >> 3) * G;
     }
-    const size_t qstride = (size_t)nt16 * kFp8Block;
     const uint8_t* xp[TT];
     const float* xsp[TT];
     int tok[TT];
@@ -295,7 +294,7 @@ __global__ __launch_bounds__(64 * kFp8Waves) void fp8_split_kernel(const Fp8Args
             const int g = min(g0 + u * NW, G - 1);
 #pragma unroll
             for (int rr = 0; rr < RR; ++rr) {
-                w[u][rr] = load_operand(qp[rr] + (size_t)g * qstride, qp[rr] + (size_t)g * qstride + 1024);
+                w[u][rr] = load_operand(qp[rr] + (size_t)g * kFp8Block, qp[rr] + (size_t)g * kFp8Block + 1024);
                 ws[u][rr] = sp[rr][g];
             }
 #pragma unroll
@@ -347,10 +346,10 @@ __global__ __launch_bounds__(64 * kFp8Waves) void fp8_split_kernel(const Fp8Args
 
 // --------------------------------------------------------------------- large tiles
 // 16 TT WM tokens x 64 WN rows per workgroup: WM x WN wavefronts, each 16 TT tokens x 4 row tiles.
-// The token codes of an input group (128 bytes a token) go memory -> LDS by the load unit into a ring of four stages, CA
-// groups ahead; a wavefront's weight operands come straight into registers, WA groups ahead (the WM wavefronts that share
-// rows find them in the L1 cache), so that LDS carries only the codes.  A token's scales of four groups come as one
-// 16-byte piece every fourth group; the scale of the wavefront's 64 rows (one 128-row block) is a lane of a register.
+// The token codes of an input group (128 bytes a token) go memory -> LDS by the load unit into a ring of four stages, two
+// groups ahead, with one barrier for two groups; a wavefront's weight operands come straight into registers, WA groups
+// ahead (the WM wavefronts that share rows find them in the L1 cache), so that LDS carries only the codes.  A token's scales
+// of four groups come as one 16-byte piece; the scale of the wavefront's 64 rows (one 128-row block) is a lane of a register.
 // A group's sums leave the matrix core into four registers a tile and are added, scaled, while the next
 // steps run: per step 4 additions to 32 cycles of matrix core, which two wavefronts a SIMD overlap.
 // In a stage, row r keeps its 16-byte piece c at position c ^ f(r), f(r) = (r / 2) ^ ((r / 4 ^ r / 8) % 2).  LDS serves
@@ -395,11 +394,9 @@ __global__ __launch_bounds__(64 * WM * WN * KH, 2) void fp8_tile_kernel(const Fp
     constexpr int NC = BM / 8 / NW;        // 1 KB code copies per wavefront and group
     constexpr int TE = TT / KH;            // token tiles that a wavefront finishes
     constexpr int NE = BM / 8 / (NW * KH); // copies per wavefront of a stage that all fill
-    constexpr int CA = 2;                  // groups that the copies are ahead
-    constexpr int WA = TT <= 4 ? 3 : 1;    // and the weights, as registers allow
+    constexpr int WA = TT <= 4 ? 3 : 1;    // groups that the weights are ahead, as registers allow
     constexpr int WS = WA + 1;             // register slots of a group's weights
-    constexpr int N = 2 * RR + (CA - 1) * (NC + 2 * RR);  // loads behind a copy when its group is due, at least
-    static_assert(NC * 8 * NW == BM && NC % 2 == 0 && N < 64 && BM % 64 == 0 && NE > 0 && TE * KH == TT, "copies");
+    static_assert(NC * 8 * NW == BM && NC % 2 == 0 && BM % 64 == 0 && NE > 0 && TE * KH == TT, "copies");
     __shared__ __attribute__((aligned(16))) uint8_t st0[KH * SB];
     __shared__ __attribute__((aligned(16))) uint8_t st1[KH * SB];
     __shared__ __attribute__((aligned(16))) uint8_t st2[KH * SB];
@@ -469,14 +466,11 @@ __global__ __launch_bounds__(64 * WM * WN * KH, 2) void fp8_tile_kernel(const Fp
         for (int i = 0; i < 2; ++i) wsc[i] = 64 * i + lane < n_g ? sz[g_begin + 64 * i + lane] : 0.f;
     }
 
-    auto copy = [&](int v, uint8_t* stg) {
+    auto copy = [&](int v, uint8_t* stg, int i) {
         const uint8_t* base = args.xq + (size_t)min(g_begin + v, g_last) * kGroup;
-#pragma unroll
-        for (int i = 0; i < NC; ++i) {
-            asm volatile("" : "+v"(xoff[i]));  // one register each: not widened to 64 bits in front of the loop
-            __builtin_amdgcn_global_load_lds((const void*)(base + xoff[i]), (lds_void*)(stg + kh * SB + 8 * (NC * wave + i) * 128),
-                                             16, 0, 0);
-        }
+        asm volatile("" : "+v"(xoff[i]));  // one register each: not widened to 64 bits in front of the loop
+        __builtin_amdgcn_global_load_lds((const void*)(base + xoff[i]), (lds_void*)(stg + kh * SB + 8 * (NC * wave + i) * 128),
+                                         16, 0, 0);
     };
     // scales of the groups v .. v + 3 (g_begin and v are multiples of 4; past the row's end the last four again)
     auto copy_scales = [&](int v, uint8_t* sc) {
@@ -486,13 +480,9 @@ __global__ __launch_bounds__(64 * WM * WN * KH, 2) void fp8_tile_kernel(const Fp
                                          (lds_void*)(sc + (kh * BM + 64 * (wave % (BM / 64))) * 16), 16, 0, 0);
     };
     i8v w[WS][RR];
-    auto wload = [&](int v, int slot) {
-        const size_t g = (size_t)min(g_begin + v, g_last) * NT;
-#pragma unroll
-        for (int rr = 0; rr < RR; ++rr) {
-            const uint8_t* at = q + (g + rts[rr]) * kFp8Block + lofs;
-            w[slot][rr] = load_operand(at, at + 1024);
-        }
+    auto wload = [&](int v, int slot, int rr) {
+        const uint8_t* at = q + ((size_t)rts[rr] * args.G + min(g_begin + v, g_last)) * kFp8Block + lofs;
+        w[slot][rr] = load_operand(at, at + 1024);
     };
     f4 acc[TT][RR];
 #pragma unroll
@@ -500,87 +490,116 @@ __global__ __launch_bounds__(64 * WM * WN * KH, 2) void fp8_tile_kernel(const Fp
 #pragma unroll
         for (int rr = 0; rr < RR; ++rr) acc[tt][rr] = f4{0.f, 0.f, 0.f, 0.f};
 
-    // The waits of the ring count the loads behind a copy, so that no operand load may move in front of one: the
-    // barriers keep the order under any scheduling.
     copy_scales(0, sc0);
-    copy(0, st0);
-    copy(1, st1);
-    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int v = 0; v < WA; ++v) wload(v, v);
-    __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): the first groups are there
+    for (int i = 0; i < 2 * NC; ++i) copy(i / NC, i < NC ? st0 : st1, i % NC);
+#pragma unroll
+    for (int i = 0; i < WA * RR; ++i) wload(i / RR, i / RR, i % RR);
     __builtin_amdgcn_sched_barrier(0);
 
-    // Group v in stage S = v % 4.  At the barrier its copies have landed, and the scales that were requested before them:
-    // after them at least N loads were issued.  The copies of v + CA go to a stage whose last reads were before this
-    // barrier, and so do the scales (at S = 0 this turn's for its last two groups, at S = 2 the next turn's for
-    // its first two); operands go to slots whose last steps were issued.
+    // Groups v and v + 1 in the stages S = v % 4 and S + 1.  At the barrier their copies have landed, and the scales.  The
+    // copies of v + 2 and v + 3 go to stages whose last reads were before this barrier, and so do the scales (at S = 0
+    // this turn's for its last two groups, at S = 2 the next turn's for its first two); operands go to slots whose last
+    // steps were issued.  Loads are requested a few with each tile: a burst of them fills the load unit's queue, and a
+    // wavefront that waits there issues no matrix-core steps either (all at the group's start: 204 us for the 200 of
+    // the first case below, 76 of them lost to the 48 KB a group in a timing copy without loads).
+    // The waits count the loads behind the one that is due, so that none may move: the barriers keep the
+    // order under any scheduling.
+    // A tile's sums are added just before their registers take the next tile's, the last ones after the next barrier.
+    f4 p[RR];
+#pragma unroll
+    for (int rr = 0; rr < RR; ++rr) p[rr] = f4{0.f, 0.f, 0.f, 0.f};
+    float last = 0.f;
+    auto wait_for = [](auto Nc) {  // vmcnt(N)
+        constexpr int N = decltype(Nc)::value;
+        static_assert(N < 64, "vmcnt");
+        __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | ((N >> 4) << 14));
+    };
+    auto scale_of = [&](int v) {
+        return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v < 64 ? wsc[0] : wsc[1]), v & 63));
+    };
     auto step = [&](int v, auto Sc) {
         constexpr int S = decltype(Sc)::value;
         uint8_t* const st[4] = {st0, st1, st2, st3};
-        const uint8_t* cur = st[S] + kh * SB;
         asm volatile("" : "+v"(rofs0), "+v"(rofs1), "+v"(sofs));  // no addresses for every stage in front of the loop
-        const uint8_t* sc = (S < 2 ? sc0 : sc1) + sofs;
-        __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | ((N >> 4) << 14));  // vmcnt(N)
-        __builtin_amdgcn_s_barrier();
-        if constexpr (S == 0) copy_scales(v, sc1);
-        if constexpr (S == 2) copy_scales(v + 2, sc0);
-        __builtin_amdgcn_sched_barrier(0);
-        copy(v + CA, st[(S + CA) & 3]);
-        __builtin_amdgcn_sched_barrier(0);
-        wload(v + WA, (S + WA) % WS);
-        __builtin_amdgcn_sched_barrier(0);
-        const float sw = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v < 64 ? wsc[0] : wsc[1]), v & 63));
-        if constexpr (WA == 1) {  // the group's weights: behind them this step's loads
-            constexpr int H = (S % 2 == 0 ? 1 : 0) + NC + 2 * RR;
-            __builtin_amdgcn_s_waitcnt(0x0F70 | (H & 15) | ((H >> 4) << 14));
+        const uint8_t* sc = (S == 0 ? sc0 : sc1) + sofs;
+        // WA == 1, tiles 0 .. 15: weights of v + 1 with the tiles 0 .. 3, copies with 4 .. 7, weights of v + 2 with 8 .. 11.
+        // WA == 3, tiles 0 .. 7: copies with the tiles 0 .. 3, weights of v + 3 with 0 .. 3, of v + 4 with 4 .. 7.
+        auto request = [&](auto Ic) {
+            constexpr int I = decltype(Ic)::value, C0 = WA == 1 ? 4 : 0;
+            if constexpr (I == C0) copy_scales(S == 0 ? v : v + 2, S == 0 ? sc1 : sc0);
+            if constexpr (I >= C0 && I < C0 + 4) {
+#pragma unroll
+                for (int i = 2 * NC / 4 * (I - C0); i < 2 * NC / 4 * (I - C0 + 1); ++i)
+                    copy(v + 2 + i / NC, st[(S + 2 + i / NC) & 3], i % NC);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            if constexpr (I < 4) wload(v + WA, (S + WA) % WS, I);
+            else if constexpr (I >= TT && I < TT + 4) wload(v + 1 + WA, (S + 1 + WA) % WS, I - TT);
             __builtin_amdgcn_sched_barrier(0);
-        }
-        constexpr int D = 2;  // token tiles whose operands are in flight
-        i8v x[D];
-        float s[D], last = 0.f;
-        f4 p[RR];
-#pragma unroll
-        for (int tt = 0; tt < TT + 1; ++tt) {
-            if (tt == 0) {
-#pragma unroll
-                for (int i = 0; i < D - 1; ++i) {
-                    x[i] = load_operand(cur + rofs0 + i * 2048, cur + rofs1 + i * 2048);
-                    s[i] = *reinterpret_cast<const float*>(sc + i * 256 + 4 * S);
-                }
-            }
-            if (tt + D - 1 < TT) {
-                x[(tt + D - 1) % D] = load_operand(cur + rofs0 + (tt + D - 1) * 2048, cur + rofs1 + (tt + D - 1) * 2048);
-                s[(tt + D - 1) % D] = *reinterpret_cast<const float*>(sc + (tt + D - 1) * 256 + 4 * S);
-            }
-            // tile tt - 1's sums are added just before their registers take tile tt's
+        };
+        static_assert(RR == 4 && NC % 2 == 0, "requests with four tiles");
+        wait_for(ic<WA == 1 ? 2 * RR : 2 + 2 * RR>{});  // the copies: behind them the weights of v, or of v + 2
+        __builtin_amdgcn_s_barrier();
+        if constexpr (WA == 1) wait_for(ic<0>{});       // the weights of v, the last that were requested
+        __builtin_amdgcn_sched_barrier(0);
+        const float sw[2] = {scale_of(v), scale_of(v + 1)};
+        i8v x[2];
+        float s[2];
+        auto xread = [&](int i) {
+            const uint8_t* at = st[S + i / TT] + kh * SB + (i % TT) * 2048;
+            x[i % 2] = load_operand(at + rofs0, at + rofs1);
+            s[i % 2] = *reinterpret_cast<const float*>(sc + (i % TT) * 256 + 4 * (S + i / TT));
+        };
+        xread(0);
+        auto tile = [&](auto Ic) {
+            constexpr int I = decltype(Ic)::value;
+            if constexpr (I == TT) wait_for(ic<1 + 2 * NC + (WA == 1 ? 0 : 4 * RR)>{});  // the weights of v + 1
+            request(Ic);
+            if constexpr (I + 1 < 2 * TT) xread(I + 1);
 #pragma unroll
             for (int rr = 0; rr < RR; ++rr) {
-                if (tt > 0) {
+                f4& sum = acc[(I + TT - 1) % TT][rr];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[tt - 1][rr][i] = fmaf(p[rr][i], last, acc[tt - 1][rr][i]);
-                }
-                if (tt < TT) p[rr] = mfma_fp8(w[S % WS][rr], x[tt % D]);
+                for (int e = 0; e < 4; ++e) sum[e] = fmaf(p[rr][e], last, sum[e]);
+                p[rr] = mfma_fp8(w[(S + I / TT) % WS][rr], x[I % 2]);
             }
-            if (tt < TT) last = s[tt % D] * sw;
-            if (tt > 0 && tt < TT) {
+            last = s[I % 2] * sw[I / TT];
 #pragma unroll
-                for (int rr = 0; rr < RR; ++rr) {
-                    __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
-                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-                }
+            for (int rr = 0; rr < RR; ++rr) {
+                __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
             }
             __builtin_amdgcn_sched_barrier(0);
+        };
+        tile(ic<0>{});
+        tile(ic<1>{});
+        tile(ic<2>{});
+        tile(ic<3>{});
+        tile(ic<4>{});
+        tile(ic<5>{});
+        tile(ic<6>{});
+        tile(ic<7>{});
+        if constexpr (TT == 8) {
+            tile(ic<8>{});
+            tile(ic<9>{});
+            tile(ic<10>{});
+            tile(ic<11>{});
+            tile(ic<12>{});
+            tile(ic<13>{});
+            tile(ic<14>{});
+            tile(ic<15>{});
         }
     };
     // whole turns of the ring; steps past the range only keep time
     for (int v = 0; v < n_turn; v += 4) {
         step(v, ic<0>{});
-        step(v + 1, ic<1>{});
         step(v + 2, ic<2>{});
-        step(v + 3, ic<3>{});
     }
+#pragma unroll
+    for (int rr = 0; rr < RR; ++rr)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[TT - 1][rr][e] = fmaf(p[rr][e], last, acc[TT - 1][rr][e]);
     __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): no copy may land in LDS after this
     __syncthreads();
     // Team kh finishes token tiles TE kh .. + TE - 1: the others' sums of them come through LDS, past the
@@ -769,7 +788,7 @@ __global__ __launch_bounds__(256) void fp8_tile_join_kernel(const Fp8Args args, 
 hipError_t launch_repack_fp8(const uint8_t* codes, const float* scales, int64_t n_out, int64_t k_in, uint8_t* q, float* sz,
                              int32_t* flag, hipStream_t stream) {
     const int64_t nt = ceil_div(n_out, 16), G = k_in / kGroup;
-    hipLaunchKernelGGL(repack_fp8_kernel, dim3((unsigned)(nt * G)), dim3(128), 0, stream, codes, n_out, k_in, (int)nt, q, flag);
+    hipLaunchKernelGGL(repack_fp8_kernel, dim3((unsigned)(nt * G)), dim3(128), 0, stream, codes, n_out, k_in, (int)G, q, flag);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const int64_t n = ceil_div(n_out, 128) * G, n_pad = (int64_t)fp8_sz_bytes(n_out, k_in) / 4;
