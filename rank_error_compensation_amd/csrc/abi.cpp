@@ -675,13 +675,13 @@ struct Fp8Space {
 inline size_t fp8_codes_bytes(int64_t T, int64_t d) {
     return round256((size_t)T * (size_t)d) + round256((size_t)(T * fp8_scale_stride(d)) * 4u);
 }
-Fp8Space fp8_space(uint8_t* base, int64_t T, int64_t d, int32_t r) {
+Fp8Space fp8_space(uint8_t* base, int64_t T, int64_t d, int32_t r, int64_t r_rows) {
     Fp8Space s;
     s.xq = base;
     s.xs = reinterpret_cast<float*>(base + round256((size_t)T * (size_t)d));
     base += fp8_codes_bytes(T, d);
     s.part = reinterpret_cast<float*>(base);
-    s.R = reinterpret_cast<_Float16*>(base + (r > 0 ? w8_part_bytes(T, r) : 0));
+    s.R = reinterpret_cast<_Float16*>(base + (r > 0 ? w8_part_bytes(r_rows, r) : 0));
     return s;
 }
 
@@ -730,11 +730,11 @@ void choose_fp8_experts_shape(int64_t rows, Fp8Args& f) {
     f.rr = rows <= 16 ? 1 : (rows <= 64 ? 2 : 16);
 }
 
-// Codes, scales and the projection of T tokens: f.xq, f.xs and f.R.  ranges: R stays as its fp32 K ranges; join: they
-// are added up here.
-hipError_t fp8_prepare(const void* x, int64_t T, int64_t d, const void* b, int32_t r, const Fp8Space& s, bool small,
-                       bool ranges, bool join, Fp8Args& f, Fp8PrepArgs& p, hipStream_t stream) {
-    const PrepPlan plan = w8a8_prep_plan(T, d, r, small);
+// Codes and scales of T tokens and the projection by `plan`: of the tokens, or with f.offsets and by_expert of the experts'
+// rows, by each one's own B.  f.xq, f.xs and f.R.  ranges: R stays as its fp32 K ranges; join: they are added up here.
+hipError_t fp8_prepare(const void* x, int64_t T, int64_t d, const void* b, int32_t r, const Fp8Space& s, const PrepPlan& plan,
+                       bool by_expert, bool ranges, bool join, Fp8Args& f, Fp8PrepArgs& p, hipStream_t stream) {
+    const int64_t rows = by_expert ? f.n_rows : T;  // of R
     std::memset(&p, 0, sizeof(p));
     p.x = static_cast<const _Float16*>(x);
     p.b = static_cast<const _Float16*>(b);
@@ -750,7 +750,7 @@ hipError_t fp8_prepare(const void* x, int64_t T, int64_t d, const void* b, int32
     if (r > 0) {
         if (ranges || plan.ks > 1) {
             p.part = s.part;
-            if ((size_t)plan.ks * (size_t)T * (size_t)p.rp * 4u > w8_part_bytes(T, r)) return hipErrorInvalidValue;
+            if ((size_t)plan.ks * (size_t)rows * (size_t)p.rp * 4u > w8_part_bytes(rows, r)) return hipErrorInvalidValue;
         }
         p.R = s.R;
     }
@@ -759,8 +759,26 @@ hipError_t fp8_prepare(const void* x, int64_t T, int64_t d, const void* b, int32
     f.gp = p.gp;
     f.R = ranges ? static_cast<const void*>(s.part) : static_cast<const void*>(s.R);
     f.r_ranges = ranges ? plan.ks : 0;
-    f.r_rows = (int32_t)T;
-    return launch_fp8_prep(p, plan.tt, plan.nj, join, stream);
+    f.r_rows = (int32_t)rows;
+    const int64_t blocks = by_expert ? ceil_div(rows, 16 * plan.tt) + std::min<int64_t>(f.n_exp, rows) : 0;
+    return launch_fp8_prep(p, plan.tt, plan.nj, join, by_expert ? &f : nullptr, blocks, stream);
+}
+
+// The experts' own projections: with few rows an expert 16 columns a workgroup and K ranges of 2048 inputs or more, else 32
+// rows and 64 columns a workgroup and K ranges up to a workgroup a CU.
+PrepPlan fp8_experts_plan(const Fp8Args& f, bool small) {
+    PrepPlan p = {1, 1, f.d, 1};
+    if (f.r == 0) return p;
+    if (small) {
+        p.ks = (int)std::max<int64_t>(1, std::min<int64_t>(ceil_div(f.d, 2048), 8192 / f.n_rows));
+    } else {
+        p.tt = 2, p.nj = 4;
+        const int64_t blocks = (ceil_div(f.n_rows, 32) + std::min(f.n_exp, f.n_rows)) * ceil_div(f.r, 64);
+        p.ks = (int)std::max<int64_t>(1, std::min<int64_t>(256 / blocks, f.d / 1024));
+    }
+    p.range = (int)(ceil_div(ceil_div(f.d, p.ks), 32) * 32);
+    p.ks = (int)ceil_div(f.d, p.range);
+    return p;
 }
 
 int run_fp8(const Call& c, void* workspace, hipStream_t stream) {
@@ -789,7 +807,7 @@ int run_fp8(const Call& c, void* workspace, hipStream_t stream) {
     }
     f.row_blocks = (int32_t)blocks;
     f.m_blocks = (int32_t)ceil_div(c.T, 16 * f.tt);
-    const Fp8Space s = fp8_space(static_cast<uint8_t*>(workspace), c.T, c.d, r);
+    const Fp8Space s = fp8_space(static_cast<uint8_t*>(workspace), c.T, c.d, r, c.T);
     if (f.ks > 1) {
         if ((size_t)(blocks * f.m_blocks * f.ks * f.tt) * 8192u > kFp8PartBytes) return GLOWQ_ERR_WORKSPACE;
         f.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + glowq_fp8_workspace_bytes(c.T, c.d, r) - kFp8PartBytes);
@@ -797,8 +815,8 @@ int run_fp8(const Call& c, void* workspace, hipStream_t stream) {
     const bool small = f.rr <= 2;
     const bool ranges = small || (f.kh > 1 && f.ks == 1);  // the product adds up the projection's K ranges itself
     Fp8PrepArgs p;
-    if (fp8_prepare(c.x, c.T, c.d, c.correct ? c.b[0] : nullptr, r, s, small, ranges, !ranges && f.ks == 1, f, p, stream) !=
-        hipSuccess)
+    if (fp8_prepare(c.x, c.T, c.d, c.correct ? c.b[0] : nullptr, r, s, w8a8_prep_plan(c.T, c.d, r, small), false, ranges,
+                    !ranges && f.ks == 1, f, p, stream) != hipSuccess)
         return GLOWQ_ERR_HIP;
     return launch_fp8(f, p, blocks * f.m_blocks, stream) == hipSuccess ? GLOWQ_OK : GLOWQ_ERR_HIP;
 }
@@ -1445,7 +1463,8 @@ size_t glowq_moe_fp8_workspace_bytes(int64_t n_rows, int64_t T, int64_t d, int32
         return 0;
     if (share != GLOWQ_MOE_SHARE_EXPERT && share != GLOWQ_MOE_SHARE_ALL) return 0;
     size_t n = kWsHeader + fp8_codes_bytes(T, d);
-    if (r > 0) n += share == GLOWQ_MOE_SHARE_ALL ? w8_part_bytes(T, r) + w8_r_bytes(T, r) : w8_r_bytes(n_rows, r);
+    const int64_t rows = share == GLOWQ_MOE_SHARE_ALL ? T : n_rows;
+    if (r > 0) n += w8_part_bytes(rows, r) + w8_r_bytes(rows, r);
     return n;
 }
 
@@ -1497,30 +1516,12 @@ int glowq_moe_forward_fp8(const void* x, int64_t T, int64_t d, int32_t n_exp, in
     f.n_rows = (int32_t)n_rows;
     f.r_by_token = share == GLOWQ_MOE_SHARE_ALL;
     f.err = error_word(workspace);
-    const Fp8Space s = fp8_space(static_cast<uint8_t*>(workspace) + kWsHeader, T, d, share == GLOWQ_MOE_SHARE_ALL ? r : 0);
-    const bool all = share == GLOWQ_MOE_SHARE_ALL && r > 0, ranges = all && f.rr <= 2;
+    const bool by_expert = share == GLOWQ_MOE_SHARE_EXPERT && r > 0, small = f.rr <= 2;
+    const Fp8Space s = fp8_space(static_cast<uint8_t*>(workspace) + kWsHeader, T, d, r, by_expert ? n_rows : T);
+    const PrepPlan plan = by_expert ? fp8_experts_plan(f, small) : w8a8_prep_plan(T, d, r, T <= kW8SmallT);
+    const bool ranges = r > 0 && (by_expert ? plan.ks > 1 : small);  // the product adds up the projection's K ranges itself
     Fp8PrepArgs prep;
-    if (fp8_prepare(x, T, d, b, all ? r : 0, s, T <= kW8SmallT, ranges, !ranges, f, prep, stream) != hipSuccess)
-        return GLOWQ_ERR_HIP;
-    if (r > 0 && !all) {
-        MoeArgs p;
-        std::memset(&p, 0, sizeof(p));
-        p.x = static_cast<const _Float16*>(x);
-        p.T = f.T;
-        p.d = f.d;
-        p.G = f.G;
-        p.row_token = row_token_dev;
-        p.offsets = offsets_dev;
-        p.n_exp = n_exp;
-        p.n_rows = f.n_rows;
-        p.r = r;
-        p.r_pad = f.rp;
-        p.b = static_cast<const _Float16*>(b);
-        p.Rout = s.R;
-        p.err = f.err;
-        f.r_rows = f.n_rows;
-        if (launch_moe_proj(p, ceil_div(n_rows, 16) + active, stream) != hipSuccess) return GLOWQ_ERR_HIP;
-    }
+    if (fp8_prepare(x, T, d, b, r, s, plan, by_expert, ranges, !ranges, f, prep, stream) != hipSuccess) return GLOWQ_ERR_HIP;
     return launch_fp8(f, prep, items, stream) == hipSuccess ? GLOWQ_OK : GLOWQ_ERR_HIP;
 }
 

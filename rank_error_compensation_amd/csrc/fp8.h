@@ -65,7 +65,9 @@ struct Fp8Args {
 
 hipError_t launch_repack_fp8(const uint8_t* codes, const float* scales, int64_t n_out, int64_t k_in, uint8_t* q, float* sz,
                              int32_t* flag, hipStream_t stream);
-hipError_t launch_fp8_prep(const Fp8PrepArgs& a, int tt, int nj, bool join, hipStream_t stream);
+// experts (may be nullptr): the projection by each expert's own B, over row_blocks blocks of 16 tt rows at most.
+hipError_t launch_fp8_prep(const Fp8PrepArgs& a, int tt, int nj, bool join, const struct Fp8Args* experts, int64_t row_blocks,
+                           hipStream_t stream);
 // Large tiles by Fp8Args::tt x rr: 8 x 16 and 8 x 8 on four wavefronts, 4 x 8 on two, times kh teams.
 // items: an upper bound of the launch's work tiles.  p: the preparation of the same call, whose projection ranges a launch
 // with K ranges joins.

@@ -66,56 +66,68 @@ __global__ __launch_bounds__(256) void repack_fp8_scales_kernel(const float* __r
 }
 
 // --------------------------------------------------------------------- token codes and projection
-// Eight inputs of one group by each thread, a group by 16 threads.  The workgroups of the projection come first in the
-// same launch: both read X, neither needs the other.
-__device__ __forceinline__ void quant_group(const Fp8PrepArgs& a, int64_t chunk) {
+// Eight inputs of one group by each thread, a group by 16 threads, U groups in turn with all their loads in flight.  The
+// workgroups of the projection come first in the same launch: both read X, neither needs the other.
+template <int U>
+__device__ __forceinline__ void quant_groups(const Fp8PrepArgs& a, int64_t block) {
     const int per = a.d / 8;
-    const int64_t t = chunk / per;
-    if (t >= a.T) return;  // whole groups of 16 threads: T d is a multiple of 128
-    const int c = (int)(chunk - t * per);
-    const h8 v = load_h8(a.x + (size_t)t * a.d + 8 * (size_t)c);
-    const u4 bits = __builtin_bit_cast(u4, v) & 0x7FFF7FFFu;
-    uint32_t top = 0;  // as fp16 bits: infinities and NaN order above every number
+    const int64_t first = block * (U * kPrepThreads) + threadIdx.x, chunks = (int64_t)a.T * per;
+    h8 v[U];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) top = max(top, max(bits[e] & 0xFFFFu, bits[e] >> 16));
-#define GLOWQ_ROR(N) top = max(top, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)top, 0x120 + N, 0xf, 0xf, false))
-    GLOWQ_ROR(8);
-    GLOWQ_ROR(4);
-    GLOWQ_ROR(2);
-    GLOWQ_ROR(1);
-#undef GLOWQ_ROR
-    const float amax = (float)__builtin_bit_cast(_Float16, (uint16_t)top);
-    const bool finite = top < 0x7C00u;
-    const float scale = finite ? amax / 448.0f : __builtin_nanf("");      // IEEE divisions
-    const float inv = finite && top > 0 ? 448.0f / amax : 0.f;
-    // |x inv| <= 448 (1 + 2^-23): rounds to 448 at most, no saturation needed
-    uint32_t w[2] = {0u, 0u};
-    if (finite) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            int p = __builtin_amdgcn_cvt_pk_fp8_f32((float)v[4 * j] * inv, (float)v[4 * j + 1] * inv, 0, false);
-            p = __builtin_amdgcn_cvt_pk_fp8_f32((float)v[4 * j + 2] * inv, (float)v[4 * j + 3] * inv, p, true);
-            w[j] = (uint32_t)p;
-        }
+    for (int u = 0; u < U; ++u) {
+        const int64_t chunk = first + u * kPrepThreads;
+        v[u] = chunk < chunks ? load_h8(a.x + 8 * chunk) : h8{0, 0, 0, 0, 0, 0, 0, 0};
     }
-    *reinterpret_cast<u2*>(a.xq + (size_t)t * a.d + 8 * (size_t)c) = u2{w[0], w[1]};
-    const int g = c >> 4;
-    if ((c & 15) == 0) a.xs[t * a.gp + g] = scale;
-    if (g == a.d / kGroup - 1 && (c & 15) > 0 && g + (c & 15) < a.gp) a.xs[t * a.gp + g + (c & 15)] = 0.f;  // up to the stride
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int64_t chunk = first + u * kPrepThreads;
+        if (chunk >= chunks) return;  // whole groups of 16 threads: T d is a multiple of 128
+        const int64_t t = chunk / per;
+        const int c = (int)(chunk - t * per);
+        const u4 bits = __builtin_bit_cast(u4, v[u]) & 0x7FFF7FFFu;
+        uint32_t top = 0;  // as fp16 bits: infinities and NaN order above every number
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top = max(top, max(bits[e] & 0xFFFFu, bits[e] >> 16));
+#define GLOWQ_ROR(N) top = max(top, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)top, 0x120 + N, 0xf, 0xf, false))
+        GLOWQ_ROR(8);
+        GLOWQ_ROR(4);
+        GLOWQ_ROR(2);
+        GLOWQ_ROR(1);
+#undef GLOWQ_ROR
+        const float amax = (float)__builtin_bit_cast(_Float16, (uint16_t)top);
+        const bool finite = top < 0x7C00u;
+        const float scale = finite ? amax / 448.0f : __builtin_nanf("");  // IEEE divisions
+        const float inv = finite && top > 0 ? 448.0f / amax : 0.f;
+        // |x inv| <= 448 (1 + 2^-23): rounds to 448 at most, no saturation needed
+        uint32_t w[2] = {0u, 0u};
+        if (finite) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                int p = __builtin_amdgcn_cvt_pk_fp8_f32((float)v[u][4 * j] * inv, (float)v[u][4 * j + 1] * inv, 0, false);
+                p = __builtin_amdgcn_cvt_pk_fp8_f32((float)v[u][4 * j + 2] * inv, (float)v[u][4 * j + 3] * inv, p, true);
+                w[j] = (uint32_t)p;
+            }
+        }
+        *reinterpret_cast<u2*>(a.xq + 8 * chunk) = u2{w[0], w[1]};
+        const int g = c >> 4;
+        if ((c & 15) == 0) a.xs[t * a.gp + g] = scale;
+        // zeros up to the stride
+        if (g == a.d / kGroup - 1 && (c & 15) > 0 && g + (c & 15) < a.gp) a.xs[t * a.gp + g + (c & 15)] = 0.f;
+    }
 }
 
-template <int TT, int NJ>
+template <int TT, int NJ, int U>
 __global__ __launch_bounds__(kPrepThreads) void fp8_prep_kernel(const Fp8PrepArgs a, int proj_blocks) {
     __shared__ f4 red[kPrepWaves / 2 * TT * NJ * 64];
     const int blk = blockIdx.x;
     if (blk >= proj_blocks) {
-        quant_group(a, (int64_t)(blk - proj_blocks) * kPrepThreads + threadIdx.x);
+        quant_groups<U>(a, blk - proj_blocks);
         return;
     }
     const int cols = (a.rp / 16 + NJ - 1) / NJ;
     const int k = blk % a.ks, rest = blk / a.ks, jb = rest % cols, tb = rest / cols;
     const int per = a.range / 32;
-    project_tile<TT, NJ>(a, tb, jb, k * per, min((k + 1) * per, a.d / 32),
+    project_tile<TT, NJ, true>(a, a.b, RowsInOrder<TT>{a.x, a.d}, 16 * TT * tb, a.T, jb, k * per, min((k + 1) * per, a.d / 32),
                          a.part != nullptr ? a.part + (size_t)k * a.T * a.rp : nullptr, red);
 }
 
@@ -131,26 +143,23 @@ struct Work {
     int j0, j1;   // rows of the outputs
 };
 
-// Item of the launch with experts, in the order (expert, row block, block of its rows).  Every wavefront finds its own,
-// four experts a lane.  Offsets out of order or range are clamped and reported by the first workgroup.  SPREAD: XCD x
+// Item of the launch with experts, in the order (expert, one of row_blocks, block of its rows).  Every wavefront finds its
+// own, four experts a lane.  Offsets out of order or range are clamped and reported by the first workgroup.  SPREAD: XCD x
 // (workgroups b with b % 8 == x) takes a run of consecutive items, so that an expert's row block stays in one L2.
 template <bool SPREAD>
-__device__ __forceinline__ bool expert_work(const Fp8Args& a, int rows_per_block, Work& w) {
+__device__ __forceinline__ bool expert_work(const Fp8Args& a, int rows_per_block, int row_blocks, int item, Work& w) {
     const int lane = threadIdx.x & 63;
-    int lo[4], hi[4], nb[4], sum = 0;
-    bool bad = false;
+    int o[5], lo[4], hi[4], nb[4], sum = 0;
+#pragma unroll
+    for (int q = 0; q < 5; ++q) o[q] = a.offsets[min(4 * lane + q, a.n_exp)];  // past the last expert: no rows
+    bool bad = (lane == 0 && o[0] != 0) || (4 * lane + 4 >= a.n_exp && o[4] != a.n_rows);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-        const int e = 4 * lane + q;
-        lo[q] = hi[q] = nb[q] = 0;
-        if (e < a.n_exp) {
-            const int o0 = a.offsets[e], o1 = a.offsets[e + 1];
-            bad |= o0 < 0 || o1 > a.n_rows || o1 < o0 || (e == 0 && o0 != 0) || (e == a.n_exp - 1 && o1 != a.n_rows);
-            lo[q] = min(max(o0, 0), a.n_rows);
-            hi[q] = min(max(o1, lo[q]), a.n_rows);
-            nb[q] = (hi[q] - lo[q] + rows_per_block - 1) / rows_per_block;
-            sum += nb[q];
-        }
+        bad |= o[q] < 0 || o[q + 1] > a.n_rows || o[q + 1] < o[q];
+        lo[q] = min(max(o[q], 0), a.n_rows);
+        hi[q] = min(max(o[q + 1], lo[q]), a.n_rows);
+        nb[q] = 4 * lane + q < a.n_exp ? (hi[q] - lo[q] + rows_per_block - 1) / rows_per_block : 0;
+        sum += nb[q];
     }
     if (bad && blockIdx.x == 0) __hip_atomic_fetch_or(a.err, 2, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     int upto = sum;
@@ -159,17 +168,16 @@ __device__ __forceinline__ bool expert_work(const Fp8Args& a, int rows_per_block
         const int n = __shfl_up(upto, off, 64);
         if (lane >= off) upto += n;
     }
-    int item = blockIdx.x;
     if constexpr (SPREAD) {
-        const int total = __builtin_amdgcn_readlane(upto, 63) * a.row_blocks, run = (total + 7) >> 3;
+        const int total = __builtin_amdgcn_readlane(upto, 63) * row_blocks, run = (total + 7) >> 3;
         if ((item >> 3) >= run) return false;
         item = (item & 7) * run + (item >> 3);
     }
-    int at = (upto - sum) * a.row_blocks, e = 0, blocks = 1, first = 0, l = 0, h = 0;
+    int at = (upto - sum) * row_blocks, e = 0, blocks = 1, first = 0, l = 0, h = 0;
     bool hit = false;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-        const int end = at + nb[q] * a.row_blocks;
+        const int end = at + nb[q] * row_blocks;
         if (item >= at && item < end) hit = true, e = 4 * lane + q, blocks = nb[q], first = at, l = lo[q], h = hi[q];
         at = end;
     }
@@ -195,14 +203,49 @@ __device__ __forceinline__ int fp8_module_of(const Fp8Args& a, int rb) {
     return __builtin_amdgcn_readfirstlane(i);
 }
 
-// Token of output row j (j < j1): itself, or where the list says; one out of range is clamped and reported.
-template <bool EXPERTS>
-__device__ __forceinline__ int token_of(const Fp8Args& a, int j) {
-    if (!EXPERTS || a.row_token == nullptr) return j;
-    const int t = a.row_token[j];
-    if (t >= 0 && t < a.T) return t;
-    __hip_atomic_fetch_or(a.err, 2, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    return t < 0 ? 0 : a.T - 1;
+// Tokens of N output rows: themselves, or where the list says; one out of range is clamped and reported.  The N entries
+// are requested together.
+template <bool EXPERTS, int N>
+__device__ __forceinline__ void tokens_of(const Fp8Args& a, const int (&j)[N], int (&t)[N]) {
+    if (!EXPERTS || a.row_token == nullptr) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) t[i] = j[i];
+        return;
+    }
+    int listed[N];
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < N; ++i) listed[i] = a.row_token[j[i]];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        t[i] = min(max(listed[i], 0), a.T - 1);
+        bad |= t[i] != listed[i];
+    }
+    if (bad) __hip_atomic_fetch_or(a.err, 2, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// Codes and scales of the tokens and, in the first workgroups, the projection of every expert's rows by its own B: R's row j
+// is that of output row j.
+template <int TT, int NJ, int U>
+__global__ __launch_bounds__(kPrepThreads) void fp8_prep_experts_kernel(const Fp8PrepArgs p, const Fp8Args a, int proj_blocks) {
+    __shared__ f4 red[kPrepWaves / 2 * TT * NJ * 64];
+    const int blk = blockIdx.x;
+    if (blk >= proj_blocks) {
+        quant_groups<U>(p, blk - proj_blocks);
+        return;
+    }
+    const int k = blk % p.ks, cols = (p.rp / 16 + NJ - 1) / NJ;
+    Work w;
+    if (!expert_work<false>(a, 16 * TT, cols, blk / p.ks, w)) return;
+    const int per = p.range / 32;
+    auto rows = [&](const int (&j)[TT], const _Float16* (&at)[TT]) {
+        int t[TT];
+        tokens_of<true>(a, j, t);
+#pragma unroll
+        for (int i = 0; i < TT; ++i) at[i] = p.x + (size_t)t[i] * p.d;
+    };
+    project_tile<TT, NJ, true>(p, p.b + (size_t)w.e * p.r * p.d, rows, w.j0, w.j1, w.rb, k * per, min((k + 1) * per, p.d / 32),
+                         p.part != nullptr ? p.part + (size_t)k * a.n_rows * p.rp : nullptr, red);
 }
 
 // Four consecutive rows of output row j, rounded to fp16.
@@ -248,7 +291,7 @@ __global__ __launch_bounds__(64 * kFp8Waves) void fp8_split_kernel(const Fp8Args
     __shared__ f4 red[NW][NT][64];
     Work wk;
     if constexpr (EXPERTS) {
-        if (!expert_work<false>(args, 16 * TT, wk)) return;
+        if (!expert_work<false>(args, 16 * TT, args.row_blocks, blockIdx.x, wk)) return;
     } else {
         wk.e = 0;
         wk.rb = blockIdx.x / args.m_blocks;
@@ -273,10 +316,12 @@ __global__ __launch_bounds__(64 * kFp8Waves) void fp8_split_kernel(const Fp8Args
     }
     const uint8_t* xp[TT];
     const float* xsp[TT];
-    int tok[TT];
+    int tok[TT], rows[TT];
+#pragma unroll
+    for (int tt = 0; tt < TT; ++tt) rows[tt] = min(wk.j0 + 16 * tt + (lane & 15), wk.j1 - 1);  // past the block: its last row
+    tokens_of<EXPERTS>(args, rows, tok);
 #pragma unroll
     for (int tt = 0; tt < TT; ++tt) {
-        tok[tt] = token_of<EXPERTS>(args, min(wk.j0 + 16 * tt + (lane & 15), wk.j1 - 1));  // rows past the block repeat its last
         xp[tt] = args.xq + (size_t)tok[tt] * d + 16 * (lane >> 4);
         xsp[tt] = args.xs + (size_t)tok[tt] * args.gp;
     }
@@ -333,7 +378,9 @@ __global__ __launch_bounds__(64 * kFp8Waves) void fp8_split_kernel(const Fp8Args
     if (args.r > 0) {
         const int r = args.r, arow = rt * 16 + (lane & 15);
         const _Float16* A = M.a + (EXPERTS ? (size_t)wk.e * M.a_step : 0);
-        const int ri = EXPERTS && args.r_by_token ? token_of<EXPERTS>(args, ok ? j : wk.j0) : (ok ? j : wk.j0);
+        int at[1] = {ok ? j : wk.j0}, t[1];
+        tokens_of<EXPERTS>(args, at, t);
+        const int ri = EXPERTS && args.r_by_token ? t[0] : at[0];
         const h8 zero8 = {0, 0, 0, 0, 0, 0, 0, 0};
         for (int kb = 0; kb < args.rp / 32; ++kb) {
             const int col = 32 * kb + 8 * (lane >> 4);
@@ -416,7 +463,7 @@ __global__ __launch_bounds__(64 * WM * WN * KH, 2) void fp8_tile_kernel(const Fp
     Work wk;
     int kr = 0, mb = 0;
     if constexpr (EXPERTS) {
-        if (!expert_work<true>(args, BM, wk)) return;
+        if (!expert_work<true>(args, BM, args.row_blocks, blockIdx.x, wk)) return;
     } else {
         int col;
         if (!tile_place(args, (int)blockIdx.x - join_blocks, mb, col)) return;
@@ -442,15 +489,21 @@ __global__ __launch_bounds__(64 * WM * WN * KH, 2) void fp8_tile_kernel(const Fp
     const int g_last = min(g_begin + max(n_g, 1), args.G) - 1;
     // copy i of wave w fills rows 8 (NC w + i) .. + 7 of the stage; lane l lands at row + l / 8, position l % 8, which
     // holds the row's piece (l % 8) ^ f(row)
-    uint32_t xoff[NC];
+    // (the last entry: the token row whose scales the lane copies)
+    uint32_t xoff[NC], soff;
+    {
+        int rows[NC + 1], tok[NC + 1];
 #pragma unroll
-    for (int i = 0; i < NC; ++i) {
-        const int row = 8 * (NC * wave + i) + (lane >> 3);
-        const uint32_t t = (uint32_t)token_of<EXPERTS>(args, min(j0 + row, j1 - 1));
-        xoff[i] = t * (uint32_t)d + 16 * (uint32_t)((lane & 7) ^ (((row >> 1) & 7) ^ (((row >> 2) ^ (row >> 3)) & 1)));
+        for (int i = 0; i < NC; ++i) rows[i] = min(j0 + 8 * (NC * wave + i) + (lane >> 3), j1 - 1);
+        rows[NC] = min(j0 + 64 * (wave % (BM / 64)) + lane, j1 - 1);
+        tokens_of<EXPERTS>(args, rows, tok);
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            const int row = 8 * (NC * wave + i) + (lane >> 3);
+            xoff[i] = (uint32_t)tok[i] * (uint32_t)d + 16 * (uint32_t)((lane & 7) ^ ((row >> 1) & 7) ^ (((row >> 2) ^ (row >> 3)) & 1));
+        }
+        soff = (uint32_t)tok[NC] * (uint32_t)args.gp * 4u;
     }
-    const int srow = 64 * (wave % (BM / 64)) + lane;  // token row whose scales the lane copies
-    uint32_t soff = (uint32_t)token_of<EXPERTS>(args, min(j0 + srow, j1 - 1)) * (uint32_t)args.gp * 4u;
     const int lr = lane & 15, fr = (lr >> 1) ^ (((lr >> 2) ^ (lr >> 3)) & 1);
     const int rbase = (16 * TT * wm + lr) * 128;
     int rofs0 = rbase + 16 * ((lane >> 4) ^ fr), rofs1 = rbase + 16 * ((4 + (lane >> 4)) ^ fr);
@@ -651,17 +704,23 @@ __global__ __launch_bounds__(64 * WM * WN * KH, 2) void fp8_tile_kernel(const Fp
     // (their results are not stored); columns of A past r are taken as zero, R's are zero up to rp, a multiple of 64.
     if constexpr (MODE == kFp8Correct) {
         const int r = args.r, rp = args.rp;
-        auto r_row = [&](int row) {
-            const int j = min(j0 + row, j1 - 1);
-            return EXPERTS && args.r_by_token ? token_of<EXPERTS>(args, j) : j;
-        };
+        int rrow[NE];  // rows of R that the lane copies
+        {
+            int rows[NE], tok[NE];
+#pragma unroll
+            for (int i = 0; i < NE; ++i) rows[i] = min(j0 + 8 * (NE * wave_all + i) + (lane >> 3), j1 - 1);
+            tokens_of<EXPERTS>(args, rows, tok);
+#pragma unroll
+            for (int i = 0; i < NE; ++i) rrow[i] = EXPERTS && args.r_by_token ? tok[i] : rows[i];
+        }
         auto rcopy = [&](int j, uint8_t* stg) {
             if (64 * j >= rp) return;
             if (args.r_ranges > 0) {  // R as the K ranges' fp32 sums: added in order, rounded once to fp16 here
-                for (int i = threadIdx.x; i < BM * 8; i += 64 * NW * KH) {
-                    const int row = i >> 3, c = i & 7;
+#pragma unroll
+                for (int i = 0; i < NE; ++i) {
+                    const int row = 8 * (NE * wave_all + i) + (lane >> 3), c = lane & 7;
                     *reinterpret_cast<h8*>(stg + row * 128 + 16 * (c ^ ((row >> 1) & 7) ^ (((row >> 2) ^ (row >> 3)) & 1))) =
-                        r_columns(args, r_row(row), 64 * j + 8 * c);
+                        r_columns(args, rrow[i], 64 * j + 8 * c);
                 }
                 return;
             }
@@ -670,7 +729,7 @@ __global__ __launch_bounds__(64 * WM * WN * KH, 2) void fp8_tile_kernel(const Fp
             for (int i = 0; i < NE; ++i) {
                 const int row = 8 * (NE * wave_all + i) + (lane >> 3);
                 const int piece = (lane & 7) ^ ((row >> 1) & 7) ^ (((row >> 2) ^ (row >> 3)) & 1);
-                __builtin_amdgcn_global_load_lds((const void*)(base + (size_t)r_row(row) * rp * 2 + 16 * piece),
+                __builtin_amdgcn_global_load_lds((const void*)(base + (size_t)rrow[i] * rp * 2 + 16 * piece),
                                                  (lds_void*)(stg + 8 * (NE * wave_all + i) * 128), 16, 0, 0);
             }
         };
@@ -797,18 +856,32 @@ hipError_t launch_repack_fp8(const uint8_t* codes, const float* scales, int64_t 
     return hipGetLastError();
 }
 
-template <int TT, int NJ>
-static void launch_fp8_prep_n(const Fp8PrepArgs& a, hipStream_t stream) {
-    const int64_t proj = a.r > 0 ? ceil_div(a.T, 16 * TT) * ceil_div(a.rp / 16, NJ) * a.ks : 0;
-    const int64_t codes = ceil_div((int64_t)a.T * a.d / 8, kPrepThreads);
-    hipLaunchKernelGGL((fp8_prep_kernel<TT, NJ>), dim3((unsigned)(proj + codes)), dim3(kPrepThreads), 0, stream, a, (int)proj);
+// Four groups of loads in flight per thread where there are enough workgroups without.
+constexpr int64_t kQuantWide = (int64_t)1 << 22;  // inputs
+
+template <int TT, int NJ, int U>
+static void launch_fp8_prep_n(const Fp8PrepArgs& a, const Fp8Args* experts, int64_t row_blocks, hipStream_t stream) {
+    const int64_t cols = ceil_div(a.rp / 16, NJ);
+    const int64_t proj = a.r > 0 ? (experts != nullptr ? row_blocks : ceil_div(a.T, 16 * TT)) * cols * a.ks : 0;
+    const dim3 grid((unsigned)(proj + ceil_div((int64_t)a.T * a.d / 8, U * kPrepThreads))), block(kPrepThreads);
+    if (experts != nullptr)
+        hipLaunchKernelGGL((fp8_prep_experts_kernel<TT, NJ, U>), grid, block, 0, stream, a, *experts, (int)proj);
+    else
+        hipLaunchKernelGGL((fp8_prep_kernel<TT, NJ, U>), grid, block, 0, stream, a, (int)proj);
 }
 
-hipError_t launch_fp8_prep(const Fp8PrepArgs& a, int tt, int nj, bool join, hipStream_t stream) {
+template <int TT, int NJ>
+static void launch_fp8_prep_t(const Fp8PrepArgs& a, const Fp8Args* experts, int64_t row_blocks, hipStream_t stream) {
+    if ((int64_t)a.T * a.d >= kQuantWide) launch_fp8_prep_n<TT, NJ, 4>(a, experts, row_blocks, stream);
+    else launch_fp8_prep_n<TT, NJ, 1>(a, experts, row_blocks, stream);
+}
+
+hipError_t launch_fp8_prep(const Fp8PrepArgs& a, int tt, int nj, bool join, const Fp8Args* experts, int64_t row_blocks,
+                           hipStream_t stream) {
     if (a.d % kGroup != 0) return hipErrorInvalidValue;
-    if (nj == 1) launch_fp8_prep_n<1, 1>(a, stream);
-    else if (tt == 1) launch_fp8_prep_n<1, 4>(a, stream);
-    else launch_fp8_prep_n<2, 4>(a, stream);
+    if (nj == 1) launch_fp8_prep_t<1, 1>(a, experts, row_blocks, stream);
+    else if (tt == 1) launch_fp8_prep_t<1, 4>(a, experts, row_blocks, stream);
+    else launch_fp8_prep_t<2, 4>(a, experts, row_blocks, stream);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.r == 0 || a.part == nullptr || !join) return e;
     hipLaunchKernelGGL(fp8_join_kernel, dim3((unsigned)ceil_div((int64_t)a.T * a.rp / 4, 256)), dim3(256), 0, stream, a);

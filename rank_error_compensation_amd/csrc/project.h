@@ -15,25 +15,47 @@ constexpr int kPrepWaves = kPrepThreads / 64;
 // wavefronts take steps in turn (U in flight) and add their tiles through LDS in wavefront order.
 // part != nullptr: fp32 sums of this range to part [T][rp]; else one rounding to fp16 into R.
 // Columns r .. r_pad - 1 are zero.
-template <int TT, int NJ, class A>
-__device__ void project_tile(const A& a, int tb, int jb, int s_begin, int s_end, float* part, f4* red) {
+// Where the inputs of TT rows of the result lie, as the rows themselves do.
+template <int TT>
+struct RowsInOrder {
+    const _Float16* x;
+    int d;
+    __device__ __forceinline__ void operator()(const int (&t)[TT], const _Float16* (&at)[TT]) const {
+#pragma unroll
+        for (int i = 0; i < TT; ++i) at[i] = x + (size_t)t[i] * d;
+    }
+};
+
+// Rows t0 .. of the result, t_end at most; rows(t, at): where the inputs of the rows t lie.
+// RUNS: a wavefront takes U steps in a row (whole lines of X and B, and the wavefronts together spread over the memory
+// channels: rows are often a multiple of their stride apart), else every kPrepWaves-th.
+template <int TT, int NJ, bool RUNS, class A, class Row>
+__device__ void project_tile(const A& a, const _Float16* b, const Row& rows, int t0, int t_end, int jb, int s_begin, int s_end,
+                             float* part, f4* red) {
     constexpr int U = TT * NJ == 1 ? 8 : 4, N = TT * NJ;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    const int kofs = 8 * (lane >> 4), T = a.T, d = a.d, r = a.r, rp = a.rp;
+    const int kofs = 8 * (lane >> 4), d = a.d, r = a.r, rp = a.rp;
     const _Float16 *xr[TT], *br[NJ];
+    {
+        int t[TT];
 #pragma unroll
-    for (int tt = 0; tt < TT; ++tt) xr[tt] = a.x + (size_t)min(16 * (TT * tb + tt) + (lane & 15), T - 1) * d + kofs;
+        for (int tt = 0; tt < TT; ++tt) t[tt] = min(t0 + 16 * tt + (lane & 15), t_end - 1);
+        rows(t, xr);
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) br[j] = a.b + (size_t)min(16 * (NJ * jb + j) + (lane & 15), r - 1) * d + kofs;
+        for (int tt = 0; tt < TT; ++tt) xr[tt] += kofs;
+    }
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) br[j] = b + (size_t)min(16 * (NJ * jb + j) + (lane & 15), r - 1) * d + kofs;
     f4 acc[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) acc[i] = f4{0.f, 0.f, 0.f, 0.f};
-    for (int s0 = s_begin + wave; s0 < s_end; s0 += U * kPrepWaves) {
+    constexpr int kApart = RUNS ? 1 : kPrepWaves;
+    for (int s0 = s_begin + wave * (RUNS ? U : 1); s0 < s_end; s0 += U * kPrepWaves) {
         h8 xv[U][TT], bv[U][NJ];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int k = 32 * min(s0 + u * kPrepWaves, s_end - 1);
+            const int k = 32 * min(s0 + u * kApart, s_end - 1);
 #pragma unroll
             for (int tt = 0; tt < TT; ++tt) xv[u][tt] = load_h8(xr[tt] + k);
 #pragma unroll
@@ -41,7 +63,7 @@ __device__ void project_tile(const A& a, int tb, int jb, int s_begin, int s_end,
         }
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (s0 + u * kPrepWaves < s_end) {
+            if (s0 + u * kApart < s_end) {
 #pragma unroll
                 for (int tt = 0; tt < TT; ++tt)
 #pragma unroll
@@ -71,9 +93,9 @@ __device__ void project_tile(const A& a, int tb, int jb, int s_begin, int s_end,
     const int col = 16 * (NJ * jb + wave % NJ) + (lane & 15);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int t = 16 * (TT * tb + wave / NJ) + 4 * (lane >> 4) + i;
+        const int t = t0 + 16 * (wave / NJ) + 4 * (lane >> 4) + i;
         const float o = col < r ? v[i] : 0.f;
-        if (t < T && col < rp) {
+        if (t < t_end && col < rp) {
             if (part != nullptr) part[(size_t)t * rp + col] = o;
             else a.R[(size_t)t * rp + col] = (_Float16)o;
         }

@@ -162,7 +162,7 @@ __global__ __launch_bounds__(kPrepThreads) void prep_kernel(const PrepArgs a, in
     const int cols = (a.rp / 16 + NJ - 1) / NJ;
     const int k = blk % a.ks, rest = blk / a.ks, jb = rest % cols, tb = rest / cols;
     const int per = a.range / 32;
-    project_tile<TT, NJ>(a, tb, jb, k * per, min((k + 1) * per, a.d / 32),
+    project_tile<TT, NJ, false>(a, a.b, RowsInOrder<TT>{a.x, a.d}, 16 * TT * tb, a.T, jb, k * per, min((k + 1) * per, a.d / 32),
                          a.part != nullptr ? a.part + (size_t)k * a.T * a.rp : nullptr, red);
 }
 
