@@ -765,17 +765,15 @@ hipError_t fp8_prepare(const void* x, int64_t T, int64_t d, const void* b, int32
 }
 
 // The experts' own projections: with few rows an expert 16 columns a workgroup and K ranges of 2048 inputs or more, else 32
-// rows and 64 columns a workgroup and K ranges up to a workgroup a CU.
+// rows and 64 columns a workgroup over all of K.
 PrepPlan fp8_experts_plan(const Fp8Args& f, bool small) {
     PrepPlan p = {1, 1, f.d, 1};
     if (f.r == 0) return p;
-    if (small) {
-        p.ks = (int)std::max<int64_t>(1, std::min<int64_t>(ceil_div(f.d, 2048), 8192 / f.n_rows));
-    } else {
+    if (!small) {
         p.tt = 2, p.nj = 4;
-        const int64_t blocks = (ceil_div(f.n_rows, 32) + std::min(f.n_exp, f.n_rows)) * ceil_div(f.r, 64);
-        p.ks = (int)std::max<int64_t>(1, std::min<int64_t>(256 / blocks, f.d / 1024));
+        return p;
     }
+    p.ks = (int)std::max<int64_t>(1, std::min<int64_t>(ceil_div(f.d, 2048), 8192 / f.n_rows));
     p.range = (int)(ceil_div(ceil_div(f.d, p.ks), 32) * 32);
     p.ks = (int)ceil_div(f.d, p.range);
     return p;

@@ -903,6 +903,7 @@ static hipError_t launch_fp8_split(const Fp8Args& a, int64_t items, hipStream_t 
 // Every XCD takes an eighth of the work, rounded up; workgroups without any return at once.
 template <int WM, int WN, int TT>
 static hipError_t launch_fp8_experts(const Fp8Args& a, const Fp8PrepArgs& p, int64_t items, hipStream_t stream) {
+    if (!a.r_by_token && a.r_ranges > 0) return hipErrorInvalidValue;  // own projections come as R
     const dim3 grid((unsigned)(8 * ceil_div(items, 8))), block(64 * WM * WN);
     if (a.r > 0) hipLaunchKernelGGL((fp8_tile_kernel<WM, WN, TT, 1, kFp8Correct, true>), grid, block, 0, stream, a, p, 0);
     else hipLaunchKernelGGL((fp8_tile_kernel<WM, WN, TT, 1, kFp8Plain, true>), grid, block, 0, stream, a, p, 0);
@@ -937,7 +938,6 @@ static hipError_t launch_fp8_tile(const Fp8Args& a, const Fp8PrepArgs& p, hipStr
 hipError_t launch_fp8(const Fp8Args& a, const Fp8PrepArgs& p, int64_t items, hipStream_t stream) {
     if (a.offsets != nullptr) {
         if (a.rr == 16) return launch_fp8_experts<1, 4, 8>(a, p, items, stream);
-        if (a.rr == 8 && a.tt == 8) return launch_fp8_experts<2, 2, 4>(a, p, items, stream);
         return launch_fp8_split<true>(a, items, stream);
     }
     if (a.rr == 16) return launch_fp8_tile<1, 4, 8, 1, false>(a, p, stream);
