@@ -721,13 +721,28 @@ void choose_fp8_shape(const Call& c, Fp8Args& f) {
     ranges(n, 8);
 }
 
-// And of the experts' product, for `rows` rows an expert on average.
-void choose_fp8_experts_shape(int64_t rows, Fp8Args& f) {
+// And of the experts' product, for `rows` rows an expert on average.  us of the whole call, random choices, a B for each expert:
+//   experts, shape               rows   16 x 16   32 x 32   64 x 32   tile of 128 x 256
+//   60, 2048 -> 1408 + 1408       4       75        68        92         77
+//                                 8       99        82       104         83
+//                                16                116       138         96
+//   32, 2048 -> 1024 (128 tiles) 16       35        31        35         36
+//                                32       53        44        49         37
+//    8, 4096 -> 2816 (88 tiles)  24                 34        45         55
+//                                32                 57        48         56
+//                                64                 73        74         57
+//    4 of 60, 2048 -> 1408 + 1408  1     14.0      15.3
+//    8, 4096 -> 14336              2    106       110
+// A tile's time hardly depends on the rows that it holds, so that it pays as soon as there are enough tiles for the card.
+void choose_fp8_experts_shape(int64_t rows, int64_t active, int32_t m, const glowq_moe_module* mods, Fp8Args& f) {
+    auto set = [&](int tt, int rr) { f.tt = tt, f.rr = rr, f.kh = 1; };
+    int64_t tiles = 0, strips = 0;
+    for (int i = 0; i < m; ++i) tiles += active * ceil_div(mods[i].n_out, 256), strips += active * ceil_div(mods[i].n_out, 16);
     f.ks = 1;
     f.gk = (int32_t)(ceil_div((int64_t)f.G, 4) * 4);
-    f.kh = 1;
-    f.tt = rows <= 16 ? 1 : (rows <= 32 ? 2 : (rows <= 64 ? 4 : 8));
-    f.rr = rows <= 16 ? 1 : (rows <= 64 ? 2 : 16);
+    if (rows > 64 || (rows > 16 && tiles >= 128) || (rows > 8 && tiles >= 256)) return set(8, 16);
+    if (rows > 24) return set(4, 2);
+    rows > 2 || strips > 8192 ? set(2, 2) : set(1, 1);
 }
 
 // Codes and scales of T tokens and the projection by `plan`: of the tokens, or with f.offsets and by_expert of the experts'
@@ -764,18 +779,20 @@ hipError_t fp8_prepare(const void* x, int64_t T, int64_t d, const void* b, int32
     return launch_fp8_prep(p, plan.tt, plan.nj, join, by_expert ? &f : nullptr, blocks, stream);
 }
 
-// The experts' own projections: with few rows an expert 16 columns a workgroup and K ranges of 2048 inputs or more, else 32
-// rows and 64 columns a workgroup over all of K.
+// The experts' own projections: 32 rows and 64 columns a workgroup over all of K where those fill the card, else 16 rows and
+// 16 columns, in front of the small form with K ranges of 2048 inputs or more.  Whole calls with 16 x 16 and with 32 x 64, r = 64:
+//   60 experts 2048 -> 1408 + 1408, 16 rows an expert (90 workgroups of 32 x 64) 103 and 110 us, 32 (120) 114 and 116, 64 (180) 131 and 119;
+//    8 experts 4096 -> 14336, 48 rows (20) 120 and 138, 200 (58) 186 and 194
 PrepPlan fp8_experts_plan(const Fp8Args& f, bool small) {
     PrepPlan p = {1, 1, f.d, 1};
     if (f.r == 0) return p;
-    if (!small) {
+    if (small) {
+        p.ks = (int)std::max<int64_t>(1, std::min<int64_t>(ceil_div(f.d, 2048), 8192 / f.n_rows));
+        p.range = (int)(ceil_div(ceil_div(f.d, p.ks), 32) * 32);
+        p.ks = (int)ceil_div(f.d, p.range);
+    } else if ((ceil_div(f.n_rows, 32) + std::min(f.n_exp, f.n_rows)) * ceil_div(f.r, 64) > 128) {
         p.tt = 2, p.nj = 4;
-        return p;
     }
-    p.ks = (int)std::max<int64_t>(1, std::min<int64_t>(ceil_div(f.d, 2048), 8192 / f.n_rows));
-    p.range = (int)(ceil_div(ceil_div(f.d, p.ks), 32) * 32);
-    p.ks = (int)ceil_div(f.d, p.range);
     return p;
 }
 
@@ -1489,7 +1506,7 @@ int glowq_moe_forward_fp8(const void* x, int64_t T, int64_t d, int32_t n_exp, in
     f.n_mod = m;
     f.r = r;
     f.rp = r > 0 ? (int32_t)w8_r_pad(r) : 0;
-    choose_fp8_experts_shape(ceil_div(n_rows, active), f);
+    choose_fp8_experts_shape(ceil_div(n_rows, active), active, m, mods, f);
     int64_t blocks = 0;
     for (int i = 0; i < m; ++i) {
         Fp8Module& M = f.mod[i];

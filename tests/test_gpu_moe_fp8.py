@@ -91,6 +91,17 @@ def test_many_experts_and_rows_in_order():
             u.check(u.run(), True, "in order")
 
 
+@pytest.mark.parametrize("share", ["expert", "all"])
+@pytest.mark.parametrize("E,T,d,rows,r", [(128, 20, 256, [300], 40), (43, 60, 384, [600, 24], 72), (128, 90, 128, [257, 40], 0), (64, 400, 128, [260, 300], 256)])
+def test_large_tiles_of_few_rows(E, T, d, rows, r, share):
+    """Many experts of about 11, 19, 11 and 20 rows each: tiles that are mostly empty; few tokens and their shared projection."""
+    g = glowq()
+    counts = [(7 * e) % (23 if E == 128 else 39) for e in range(E)]
+    u = Layer(T, d, rows, counts, r, g.MOE_SHARE_EXPERT if share == "expert" else g.MOE_SHARE_ALL, 5)
+    log(f"fp8 experts E={E} T={T} d={d} rows={rows} listed={u.n} r={r} {share}")
+    u.check(u.run(), True, share)
+
+
 @pytest.mark.parametrize("counts", [[3, 2, 0], [140, 0, 150]])
 def test_lists_out_of_range_are_clamped_and_reported(counts):
     g = glowq()
