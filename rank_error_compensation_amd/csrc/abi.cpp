@@ -690,7 +690,11 @@ constexpr size_t kFp8PartBytes = (size_t)16 << 20;
 
 // Launch shape of a group call.
 void choose_fp8_shape(const Call& c, Fp8Args& f) {
-    auto set = [&](int tt, int rr, int kh) { f.tt = tt, f.rr = rr, f.kh = kh; };
+    const int64_t G = c.d / kGroup;
+    auto set = [&](int tt, int rr, int kh) {
+        f.tt = tt, f.rr = rr, f.kh = kh, f.ks = 1;
+        f.gk = (int32_t)(ceil_div(G, 4 * kh) * 4 * kh);
+    };
     auto tiles = [&](int tt, int rr) {
         int64_t n = 0;
         for (int i = 0; i < c.m; ++i) n += ceil_div(ceil_div(c.w[i].n_out, 16), rr);
@@ -698,25 +702,37 @@ void choose_fp8_shape(const Call& c, Fp8Args& f) {
     };
     // K ranges of at least `least` groups up to a tile a CU; whole turns of the ring for every team
     auto ranges = [&](int64_t n, int64_t least) {
-        const int64_t ks = std::max<int64_t>(1, std::min<int64_t>(256 / n, c.d / kGroup / least));
-        f.gk = (int32_t)(ceil_div(ceil_div(c.d / kGroup, ks), 4 * f.kh) * 4 * f.kh);
-        f.ks = (int32_t)ceil_div(c.d / kGroup, f.gk);
+        const int64_t ks = std::max<int64_t>(1, std::min<int64_t>(256 / n, G / least));
+        f.gk = (int32_t)(ceil_div(ceil_div(G, ks), 4 * f.kh) * 4 * f.kh);
+        f.ks = (int32_t)ceil_div(G, f.gk);
     };
-    f.ks = 1;
-    f.gk = (int32_t)(ceil_div(c.d / kGroup, 4) * 4);
-    set(c.T <= 16 ? 1 : (c.T <= 32 ? 2 : 4), c.T <= 16 ? 1 : 2, 1);
+    if (c.T <= 16) return set(1, 1, 1);
+    // 32 x 32 pieces up to 32 tokens, and past 64 while two a CU hold the call and the rows are short (2 x 1408 <- 2048 at
+    // T = 128, 352 pieces: 17 us, 23 in tiles, T = 200, 616: 23 and 23; 4096 <- 1024 at T = 128, 512: 12.5 and 17.4, T = 200,
+    // 896: 20 and 17; 1024 <- 4096 at T = 400, 416: 27 and 28; but 4096 <- 14336 at T = 65, 384: 61 and 34); up to 4096
+    // tokens, whose projection in two ranges w8_part_bytes holds
+    if (c.T <= kW8TinyT || (c.T > kW8SmallT && c.T <= 4096 && G <= 32 && tiles(2, 2) <= 512)) return set(2, 2, 1);
+    // Up to 64 tokens 64 x 32 pieces, or 64 x 128 tiles of four teams where those are many or the rows long (r = 64:
+    // 2 x 11008 <- 4096 at T = 33, 172 tiles, 36 us and 38 in pieces; 4096 <- 14336, 32 tiles, T = 48, 32 and 48, T = 33,
+    // 35 and 40; QKV, 48 tiles, T = 48, 25 and 22), with K ranges of at least 24 groups up to a tile a CU (4096 <- 14336
+    // at T = 48: 32 us in four ranges, 37 in two, 57 in one; 2 x 11008 <- 4096: 38 in one, 45 in two)
     if (c.T <= kW8SmallT) {
-        if (c.T <= kW8TinyT) return;
         const int64_t n = tiles(4, 8);
-        if (n <= 64 && c.T * c.d < ((int64_t)1 << 19)) return;
+        if (n <= 64 && c.T * c.d < ((int64_t)3 << 17)) return set(4, 2, 1);
         set(4, 8, 4);
         return ranges(n, 24);
     }
-    set(8, 16, 1);
-    if (tiles(8, 16) > 256) return;
-    set(8, 8, 1);
+    // 128 x 256 tiles where there is more than one of 128 x 128 a CU (2 x 11008 <- 4096 at T = 200, 344 of 128 x 128: 44 us,
+    // 51 with those; T = 1000, 1376: 109 and 137; QKV at T = 1000, 384: 48 and 53; but T = 600, 240: 42 and 36)
     const int64_t n = tiles(8, 8);
-    if (n > 256 || c.d / kGroup < 16) return;
+    if (n > 256) return set(8, 16, 1);
+    // 128 x 128 tiles, in K ranges of at least 8 groups where they are half a tile a CU or fewer, by two teams of
+    // wavefronts (4096 <- 14336 at T = 65, 32 tiles: 34 us in eight ranges, 36 in four, 43 in two, 62 in one; T = 400,
+    // 128 tiles: 59 in two, 76 in one; QKV at T = 128, 48 tiles: 28.4 in four, 31 in one, T = 200, 96 tiles: 32 and 32).
+    // Two teams without ranges lose to one (QKV at T = 600: 39 and 36), and so do ranges of short rows (2 x 1408 <- 2048
+    // at T = 400, 88 tiles: 30 in two, 24 in one).
+    set(8, 8, 1);
+    if (2 * n > 256 || G < 32) return;
     set(8, 8, 2);
     ranges(n, 8);
 }

@@ -910,8 +910,8 @@ static hipError_t launch_fp8_experts(const Fp8Args& a, const Fp8PrepArgs& p, int
     return hipGetLastError();
 }
 
-// SPLIT: the tile takes K ranges.
-template <int WM, int WN, int TT, int KH, bool SPLIT>
+// SPLIT: the tile is used with K ranges; WHOLE: without.
+template <int WM, int WN, int TT, int KH, bool SPLIT, bool WHOLE>
 static hipError_t launch_fp8_tile(const Fp8Args& a, const Fp8PrepArgs& p, hipStream_t stream) {
     const int64_t join = a.ks > 1 && a.r > 0 && p.part != nullptr
                              ? ceil_div(ceil_div((int64_t)p.T * p.rp / 4, 64 * WM * WN * KH), 8) * 8 : 0;
@@ -929,10 +929,13 @@ static hipError_t launch_fp8_tile(const Fp8Args& a, const Fp8PrepArgs& p, hipStr
             return hipGetLastError();
         }
     }
-    if (a.ks > 1) return hipErrorInvalidValue;
-    if (a.r > 0) hipLaunchKernelGGL((fp8_tile_kernel<WM, WN, TT, KH, kFp8Correct, false>), g, block, 0, stream, a, p, 0);
-    else hipLaunchKernelGGL((fp8_tile_kernel<WM, WN, TT, KH, kFp8Plain, false>), g, block, 0, stream, a, p, 0);
-    return hipGetLastError();
+    if constexpr (WHOLE) {
+        if (a.ks > 1) return hipErrorInvalidValue;
+        if (a.r > 0) hipLaunchKernelGGL((fp8_tile_kernel<WM, WN, TT, KH, kFp8Correct, false>), g, block, 0, stream, a, p, 0);
+        else hipLaunchKernelGGL((fp8_tile_kernel<WM, WN, TT, KH, kFp8Plain, false>), g, block, 0, stream, a, p, 0);
+        return hipGetLastError();
+    }
+    return hipErrorInvalidValue;
 }
 
 hipError_t launch_fp8(const Fp8Args& a, const Fp8PrepArgs& p, int64_t items, hipStream_t stream) {
@@ -940,10 +943,10 @@ hipError_t launch_fp8(const Fp8Args& a, const Fp8PrepArgs& p, int64_t items, hip
         if (a.rr == 16) return launch_fp8_experts<1, 4, 8>(a, p, items, stream);
         return launch_fp8_split<true>(a, items, stream);
     }
-    if (a.rr == 16) return launch_fp8_tile<1, 4, 8, 1, false>(a, p, stream);
+    if (a.rr == 16) return launch_fp8_tile<1, 4, 8, 1, false, true>(a, p, stream);
     if (a.rr == 8 && a.tt == 8)
-        return a.kh == 2 ? launch_fp8_tile<2, 2, 4, 2, true>(a, p, stream) : launch_fp8_tile<2, 2, 4, 1, false>(a, p, stream);
-    if (a.rr == 8) return launch_fp8_tile<1, 2, 4, 4, true>(a, p, stream);
+        return a.kh == 2 ? launch_fp8_tile<2, 2, 4, 2, true, false>(a, p, stream) : launch_fp8_tile<2, 2, 4, 1, false, true>(a, p, stream);
+    if (a.rr == 8) return launch_fp8_tile<1, 2, 4, 4, true, true>(a, p, stream);
     return launch_fp8_split<false>(a, items, stream);
 }
 

@@ -64,7 +64,11 @@ SHAPES = [(1, 128, [16], 0), (1, 256, [1], 8), (1, 4096, [520, 17, 130], 64), (2
           (48, 2176, [300], 128), (64, 1024, [1024, 512, 512], 64), (65, 256, [48, 32], 16), (130, 384, [300, 200], 40),
           (300, 512, [2048, 2048], 128), (8, 2048, [64], 256), (257, 896, [1030, 515], 64), (513, 128, [770], 256),
           (77, 14336, [128], 64), (40, 8192, [256], 8), (70, 2048, [130, 250], 64), (129, 4096, [640], 72), (1025, 640, [300], 0),
-          (129, 1280, [4096, 20], 24), (300, 16384, [160], 8), (2100, 256, [4000], 24), (1400, 640, [2100, 2500, 1301], 0)]
+          (129, 1280, [4096, 20], 24), (300, 16384, [160], 8), (2100, 256, [4000], 24), (1400, 640, [2100, 2500, 1301], 0),
+          (129, 4096, [4500], 72), (300, 16384, [700], 8), (130, 4224, [2000, 40], 24), (70, 14336, [1030], 64), (1100, 4096, [130], 0),
+          (700, 512, [3100], 64), (1030, 384, [300, 200], 40), (1027, 128, [300], 256), (1026, 896, [1030, 515], 64),
+          (1024, 128, [4100], 8), (4096, 4096, [20], 24), (4097, 256, [30], 8), (40, 1024, [9000], 24),
+          (50, 640, [8300], 0), (48, 14336, [260], 72), (33, 12288, [40, 17], 8)]
 
 
 @pytest.mark.parametrize("idx", range(len(SHAPES)), ids=[f"T{s[0]}_d{s[1]}_m{len(s[2])}_r{s[3]}" for s in SHAPES])
@@ -97,9 +101,10 @@ def test_codes_and_scales_in_the_workspace():
 
 def test_extremes_and_exact_sums():
     """Largest codes everywhere; one input a group, where every step is exact."""
-    u = Unit(40, 2048, [64, 20], 0, 3, extremes=True)
-    u.check(u.run(False), False, "extremes")
-    for T in (1, 40, 150):
+    for T, rows in ((40, [64, 20]), (4100, [64, 20]), (260, [2100])):
+        u = Unit(T, 2048, rows, 0, 3, extremes=True)
+        u.check(u.run(False), False, f"extremes T={T}")
+    for T in (1, 40, 150, 4100):
         u = Unit(T, 1024, [150], 0, 4)
         u.x[:] = 0
         u.x[:, ::128] = 2.0
@@ -114,7 +119,7 @@ def test_extremes_and_exact_sums():
         assert abs(float(y[0, 0]) - float(want)) <= 2.0 ** -11 * abs(float(want)) and (y == y[0, 0]).all()
 
 
-@pytest.mark.parametrize("T", [1, 3, 30, 70, 200])
+@pytest.mark.parametrize("T", [1, 3, 30, 70, 200, 1700])
 def test_nan_and_infinity_stay_in_their_token(T):
     u = Unit(T, 640, [300, 20], 16, 5)
     clean = u.run()
@@ -167,8 +172,8 @@ def test_weights_bad_data_and_refusals():
 def test_large_workspace_streams_and_two_calls():
     """A workspace of the largest call for every smaller one; calls on two streams with a workspace each."""
     g = glowq()
-    units = [Unit(T, 1024, [300, 260], 64, T) for T in (300, 70, 20, 1)]
-    ws = torch.full((g.fp8_workspace_bytes(300, 1024, 64),), 0xFF, dtype=torch.uint8, device="cuda")
+    units = [Unit(T, 1024, [300, 260], 64, T) for T in (1100, 300, 70, 20, 1)]
+    ws = torch.full((g.fp8_workspace_bytes(1100, 1024, 64),), 0xFF, dtype=torch.uint8, device="cuda")
     for u in units:
         u.check(u.run(workspace=ws), True, f"T={u.T}")
     want = [u.run() for u in units[:2]]
@@ -182,11 +187,11 @@ def test_large_workspace_streams_and_two_calls():
         assert all(torch.equal(x, y) for x, y in zip(p, q))
 
 
-@pytest.mark.parametrize("T", [1, 24, 70, 300])
-def test_captured_and_replayed(T):
+@pytest.mark.parametrize("T,d", [(1, 1024), (24, 1024), (70, 1024), (300, 1024), (70, 14336), (300, 4096), (1100, 1024), (48, 14336)])
+def test_captured_and_replayed(T, d):
     g = glowq()
-    u = Unit(T, 1024, [300, 260], 64, T)
-    ws = torch.empty(g.fp8_workspace_bytes(T, 1024, 64), dtype=torch.uint8, device="cuda")
+    u = Unit(T, d, [300, 760], 64, T)
+    ws = torch.empty(g.fp8_workspace_bytes(T, d, 64), dtype=torch.uint8, device="cuda")
     x, b, a = u.x.cuda(), u.b.cuda(), [t.cuda() for t in u.a]
     call = lambda: g.group_forward_fp8(x, u.w, b, a, 64, workspace=ws)
     eager = call()
@@ -198,5 +203,5 @@ def test_captured_and_replayed(T):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(p, q) for p, q in zip(ys, eager))
-        x.copy_(torch.randn(T, 1024, generator=torch.Generator().manual_seed(seed)).half())
+        x.copy_(torch.randn(T, d, generator=torch.Generator().manual_seed(seed)).half())
         eager = call()
