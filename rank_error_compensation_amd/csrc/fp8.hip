@@ -546,6 +546,7 @@ __global__ __launch_bounds__(64 * WM * WN * KH, 2) void fp8_tile_kernel(const Fp
     copy_scales(0, sc0);
 #pragma unroll
     for (int i = 0; i < 2 * NC; ++i) copy(i / NC, i < NC ? st0 : st1, i % NC);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int i = 0; i < WA * RR; ++i) wload(i / RR, i / RR, i % RR);
     __builtin_amdgcn_sched_barrier(0);
