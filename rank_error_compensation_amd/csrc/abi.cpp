@@ -795,10 +795,13 @@ hipError_t fp8_prepare(const void* x, int64_t T, int64_t d, const void* b, int32
     return launch_fp8_prep(p, plan.tt, plan.nj, join, by_expert ? &f : nullptr, blocks, stream);
 }
 
-// The experts' own projections: 32 rows and 64 columns a workgroup over all of K where those fill the card, else 16 rows and
-// 16 columns, in front of the small form with K ranges of 2048 inputs or more.  Whole calls with 16 x 16 and with 32 x 64, r = 64:
-//   60 experts 2048 -> 1408 + 1408, 16 rows an expert (90 workgroups of 32 x 64) 103 and 110 us, 32 (120) 114 and 116, 64 (180) 131 and 119;
-//    8 experts 4096 -> 14336, 48 rows (20) 120 and 138, 200 (58) 186 and 194
+// The experts' own projections: 64 rows and 64 columns a workgroup over all of K where those fill half the card, else 32 rows,
+// else 16 rows and 16 columns, in front of the small form with K ranges of 2048 inputs or more.  Whole calls, r = 64:
+//   rows an expert of 60, 2048 -> 1408 + 1408     16    32    64   128   273
+//   16 x 16                                      103   114   131   167   255 us
+//   32 x 64                                      110   116   118   148   215
+//   64 x 64                                                  124   142   206
+//   and of 8, 4096 -> 14336      48 (16 x 16) 120, (32 x 64) 138    200 186, 194    600 (32 x 64) 371, (64 x 64) 371    1200 649, 630
 PrepPlan fp8_experts_plan(const Fp8Args& f, bool small) {
     PrepPlan p = {1, 1, f.d, 1};
     if (f.r == 0) return p;
@@ -806,9 +809,11 @@ PrepPlan fp8_experts_plan(const Fp8Args& f, bool small) {
         p.ks = (int)std::max<int64_t>(1, std::min<int64_t>(ceil_div(f.d, 2048), 8192 / f.n_rows));
         p.range = (int)(ceil_div(ceil_div(f.d, p.ks), 32) * 32);
         p.ks = (int)ceil_div(f.d, p.range);
-    } else if ((ceil_div(f.n_rows, 32) + std::min(f.n_exp, f.n_rows)) * ceil_div(f.r, 64) > 128) {
-        p.tt = 2, p.nj = 4;
+        return p;
     }
+    auto blocks = [&](int64_t rows) { return (ceil_div(f.n_rows, rows) + std::min(f.n_exp, f.n_rows)) * ceil_div(f.r, 64); };
+    if (blocks(64) > 128) p.tt = 4, p.nj = 4;
+    else if (blocks(32) > 128) p.tt = 2, p.nj = 4;
     return p;
 }
 

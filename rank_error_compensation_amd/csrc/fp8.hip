@@ -865,10 +865,8 @@ static void launch_fp8_prep_n(const Fp8PrepArgs& a, const Fp8Args* experts, int6
     const int64_t cols = ceil_div(a.rp / 16, NJ);
     const int64_t proj = a.r > 0 ? (experts != nullptr ? row_blocks : ceil_div(a.T, 16 * TT)) * cols * a.ks : 0;
     const dim3 grid((unsigned)(proj + ceil_div((int64_t)a.T * a.d / 8, U * kPrepThreads))), block(kPrepThreads);
-    if (experts != nullptr)
-        hipLaunchKernelGGL((fp8_prep_experts_kernel<TT, NJ, U>), grid, block, 0, stream, a, *experts, (int)proj);
-    else
-        hipLaunchKernelGGL((fp8_prep_kernel<TT, NJ, U>), grid, block, 0, stream, a, (int)proj);
+    if (experts != nullptr) hipLaunchKernelGGL((fp8_prep_experts_kernel<TT, NJ, U>), grid, block, 0, stream, a, *experts, (int)proj);
+    else if constexpr (TT <= 2) hipLaunchKernelGGL((fp8_prep_kernel<TT, NJ, U>), grid, block, 0, stream, a, (int)proj);
 }
 
 template <int TT, int NJ>
@@ -880,7 +878,9 @@ static void launch_fp8_prep_t(const Fp8PrepArgs& a, const Fp8Args* experts, int6
 hipError_t launch_fp8_prep(const Fp8PrepArgs& a, int tt, int nj, bool join, const Fp8Args* experts, int64_t row_blocks,
                            hipStream_t stream) {
     if (a.d % kGroup != 0) return hipErrorInvalidValue;
-    if (nj == 1) launch_fp8_prep_t<1, 1>(a, experts, row_blocks, stream);
+    if (tt == 4 && experts == nullptr) return hipErrorInvalidValue;
+    if (tt == 4) launch_fp8_prep_t<4, 4>(a, experts, row_blocks, stream);
+    else if (nj == 1) launch_fp8_prep_t<1, 1>(a, experts, row_blocks, stream);
     else if (tt == 1) launch_fp8_prep_t<1, 4>(a, experts, row_blocks, stream);
     else launch_fp8_prep_t<2, 4>(a, experts, row_blocks, stream);
     const hipError_t e = hipGetLastError();

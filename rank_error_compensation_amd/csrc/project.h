@@ -32,7 +32,7 @@ struct RowsInOrder {
 template <int TT, int NJ, bool RUNS, class A, class Row>
 __device__ void project_tile(const A& a, const _Float16* b, const Row& rows, int t0, int t_end, int jb, int s_begin, int s_end,
                              float* part, f4* red) {
-    constexpr int U = TT * NJ == 1 ? 8 : 4, N = TT * NJ;
+    constexpr int U = TT * NJ == 1 ? 8 : (TT * NJ <= 8 ? 4 : 2), N = TT * NJ;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int kofs = 8 * (lane >> 4), d = a.d, r = a.r, rp = a.rp;
@@ -86,18 +86,22 @@ __device__ void project_tile(const A& a, const _Float16* b, const Row& rows, int
         }
     }
     __syncthreads();
-    if (wave >= N) return;
-    f4 v = red[wave * 64 + lane];
 #pragma unroll
-    for (int w = 1; w < H; ++w) v += red[(w * N + wave) * 64 + lane];
-    const int col = 16 * (NJ * jb + wave % NJ) + (lane & 15);
+    for (int n = 0; n < N; n += kPrepWaves) {
+        const int tile = n + wave;
+        if (tile >= N) return;
+        f4 v = red[tile * 64 + lane];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int t = t0 + 16 * (wave / NJ) + 4 * (lane >> 4) + i;
-        const float o = col < r ? v[i] : 0.f;
-        if (t < t_end && col < rp) {
-            if (part != nullptr) part[(size_t)t * rp + col] = o;
-            else a.R[(size_t)t * rp + col] = (_Float16)o;
+        for (int w = 1; w < H; ++w) v += red[(w * N + tile) * 64 + lane];
+        const int col = 16 * (NJ * jb + tile % NJ) + (lane & 15);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int t = t0 + 16 * (tile / NJ) + 4 * (lane >> 4) + i;
+            const float o = col < r ? v[i] : 0.f;
+            if (t < t_end && col < rp) {
+                if (part != nullptr) part[(size_t)t * rp + col] = o;
+                else a.R[(size_t)t * rp + col] = (_Float16)o;
+            }
         }
     }
 }

@@ -102,6 +102,12 @@ def test_large_tiles_of_few_rows(E, T, d, rows, r, share):
     u.check(u.run(), True, share)
 
 
+def test_many_rows_of_few_experts():
+    g = glowq()
+    u = Layer(700, 128, [40], [2100, 0, 4133, 5], 72, g.MOE_SHARE_EXPERT, 6)
+    u.check(u.run(), True, "many rows")
+
+
 @pytest.mark.parametrize("counts", [[3, 2, 0], [140, 0, 150]])
 def test_lists_out_of_range_are_clamped_and_reported(counts):
     g = glowq()
