@@ -144,10 +144,9 @@ struct Work {
 };
 
 // Item of the launch with experts, in the order (expert, one of row_blocks, block of its rows).  Every wavefront finds its
-// own, four experts a lane.  Offsets out of order or range are clamped and reported by the first workgroup.  SPREAD: XCD x
+// own, four experts a lane.  Offsets out of order or range are clamped and reported by the first workgroup.  spread: XCD x
 // (workgroups b with b % 8 == x) takes a run of consecutive items, so that an expert's row block stays in one L2.
-template <bool SPREAD>
-__device__ __forceinline__ bool expert_work(const Fp8Args& a, int rows_per_block, int row_blocks, int item, Work& w) {
+__device__ __forceinline__ bool expert_work(const Fp8Args& a, int rows_per_block, int row_blocks, int item, bool spread, Work& w) {
     const int lane = threadIdx.x & 63;
     int o[5], lo[4], hi[4], nb[4], sum = 0;
 #pragma unroll
@@ -168,7 +167,7 @@ __device__ __forceinline__ bool expert_work(const Fp8Args& a, int rows_per_block
         const int n = __shfl_up(upto, off, 64);
         if (lane >= off) upto += n;
     }
-    if constexpr (SPREAD) {
+    if (spread) {
         const int total = __builtin_amdgcn_readlane(upto, 63) * row_blocks, run = (total + 7) >> 3;
         if ((item >> 3) >= run) return false;
         item = (item & 7) * run + (item >> 3);
@@ -236,7 +235,7 @@ __global__ __launch_bounds__(kPrepThreads) void fp8_prep_experts_kernel(const Fp
     }
     const int k = blk % p.ks, cols = (p.rp / 16 + NJ - 1) / NJ;
     Work w;
-    if (!expert_work<false>(a, 16 * TT, cols, blk / p.ks, w)) return;
+    if (!expert_work(a, 16 * TT, cols, blk / p.ks, p.ks == 1, w)) return;
     const int per = p.range / 32;
     auto rows = [&](const int (&j)[TT], const _Float16* (&at)[TT]) {
         int t[TT];
@@ -291,7 +290,7 @@ __global__ __launch_bounds__(64 * kFp8Waves) void fp8_split_kernel(const Fp8Args
     __shared__ f4 red[NW][NT][64];
     Work wk;
     if constexpr (EXPERTS) {
-        if (!expert_work<false>(args, 16 * TT, args.row_blocks, blockIdx.x, wk)) return;
+        if (!expert_work(args, 16 * TT, args.row_blocks, blockIdx.x, false, wk)) return;
     } else {
         wk.e = 0;
         wk.rb = blockIdx.x / args.m_blocks;
@@ -463,7 +462,7 @@ __global__ __launch_bounds__(64 * WM * WN * KH, 2) void fp8_tile_kernel(const Fp
     Work wk;
     int kr = 0, mb = 0;
     if constexpr (EXPERTS) {
-        if (!expert_work<true>(args, BM, args.row_blocks, blockIdx.x, wk)) return;
+        if (!expert_work(args, BM, args.row_blocks, blockIdx.x, true, wk)) return;
     } else {
         int col;
         if (!tile_place(args, (int)blockIdx.x - join_blocks, mb, col)) return;
@@ -863,10 +862,13 @@ constexpr int64_t kQuantWide = (int64_t)1 << 22;  // inputs
 template <int TT, int NJ, int U>
 static void launch_fp8_prep_n(const Fp8PrepArgs& a, const Fp8Args* experts, int64_t row_blocks, hipStream_t stream) {
     const int64_t cols = ceil_div(a.rp / 16, NJ);
-    const int64_t proj = a.r > 0 ? (experts != nullptr ? row_blocks : ceil_div(a.T, 16 * TT)) * cols * a.ks : 0;
+    const int64_t proj = a.r > 0 ? (experts != nullptr ? 8 * ceil_div(row_blocks * cols, 8) : ceil_div(a.T, 16 * TT) * cols) * a.ks : 0;
     const dim3 grid((unsigned)(proj + ceil_div((int64_t)a.T * a.d / 8, U * kPrepThreads))), block(kPrepThreads);
-    if (experts != nullptr) hipLaunchKernelGGL((fp8_prep_experts_kernel<TT, NJ, U>), grid, block, 0, stream, a, *experts, (int)proj);
-    else if constexpr (TT <= 2) hipLaunchKernelGGL((fp8_prep_kernel<TT, NJ, U>), grid, block, 0, stream, a, (int)proj);
+    if (experts == nullptr) {
+        if constexpr (TT <= 2) hipLaunchKernelGGL((fp8_prep_kernel<TT, NJ, U>), grid, block, 0, stream, a, (int)proj);
+    } else if constexpr (TT > 1 || NJ == 1) {
+        hipLaunchKernelGGL((fp8_prep_experts_kernel<TT, NJ, U>), grid, block, 0, stream, a, *experts, (int)proj);
+    }
 }
 
 template <int TT, int NJ>
@@ -878,7 +880,7 @@ static void launch_fp8_prep_t(const Fp8PrepArgs& a, const Fp8Args* experts, int6
 hipError_t launch_fp8_prep(const Fp8PrepArgs& a, int tt, int nj, bool join, const Fp8Args* experts, int64_t row_blocks,
                            hipStream_t stream) {
     if (a.d % kGroup != 0) return hipErrorInvalidValue;
-    if (tt == 4 && experts == nullptr) return hipErrorInvalidValue;
+    if (experts != nullptr ? tt == 1 && nj == 4 : tt == 4) return hipErrorInvalidValue;
     if (tt == 4) launch_fp8_prep_t<4, 4>(a, experts, row_blocks, stream);
     else if (nj == 1) launch_fp8_prep_t<1, 1>(a, experts, row_blocks, stream);
     else if (tt == 1) launch_fp8_prep_t<1, 4>(a, experts, row_blocks, stream);
