@@ -16,6 +16,15 @@
 // 128 g + 64 m + 16 (l / 16) .. + 15.  A lane's 32 bytes of the step's operand are its pieces of both halves; the
 // activation operand takes the same inputs in the same places, so the order of inputs inside the step does not matter.
 // Rows >= n_out are zero.  Codes of the activations lie in their natural order [T][d], scales [T][G rounded up to 4].
+//
+// Launches: codes, scales and the projection (with K ranges a launch more that adds them, where the product does not), then
+// the product, in pieces whose wavefronts share the input groups (few tokens: one round of loads each) or in tiles; with K
+// ranges of the tiles a last launch joins those.  r = 64, kernels alone / the call from the host, us:
+//   T = 1, 4096 + 2 x 1024 <- 4096         4.7 + 6.5 / 16.5 (two launches from the host; 25 MB of weights in 6.5 us)
+//   T = 77, 4096 <- 14336                  7.5 + 19 + 7.5 / 33.5 (eight ranges: 59 MB of weights, 17 MB of sums)
+//   T = 2048, 2 x 11008 <- 4096            15.5 + 4.5 + 170 / 195 (the tile 2.2 PFLOP/s, the library's product alone 2.25)
+//   T = 1, 4 of 60 experts 2048 -> 2 x 1408    4.7 + 6.7 / 16.8
+//   T = 4095, 60 experts, 4 choices        41 + 148 / 190 (a B each; 1.2 PFLOP/s: a fifth of the tiles' rows are empty)
 #include <algorithm>
 #include <type_traits>
 
@@ -433,6 +442,16 @@ __device__ __forceinline__ bool tile_place(const Fp8Args& args, int block, int& 
 
 enum : int { kFp8Plain = 0, kFp8Correct = 1, kFp8Split = 2 };  // what follows the sums
 
+// --------------------------------------------------------------------- product, tiles
+// 16 TT WM tokens x 64 WN rows a workgroup and team; KH teams of WM x WN wavefronts share the workgroup's input groups.
+// The codes pass a ring of four stages in LDS, filled by the load unit past the registers: a stage row is a token's 128
+// bytes of a group, its eight pieces in an order f(row) that puts the sixteen lanes of a read on all banks.  Weights go
+// straight to registers, one or three groups ahead: a wavefront's 64 rows are nobody else's in the workgroup.  Scales: the
+// tokens' four groups at a time through LDS, the rows' (one each 128 rows: 64 rows have one) from a lane's register.
+// What bounds 128 x 256 tiles at T = 2048, 2 x 11008 <- 4096 (170 us, matrix cores busy 0.67 of the cycles): the loads'
+// issue and return beside the matrix cores (without the weights' loads 136-143, without the codes' 180, without both
+// 123-129; scaling costs nothing), and 2.7 tiles a slot.  256 x 256 on eight wavefronts took the same, 128 x 128 a fifth more.
+
 template <int WM, int WN, int TT, int KH, int MODE, bool EXPERTS>
 __global__ __launch_bounds__(64 * WM * WN * KH, 2) void fp8_tile_kernel(const Fp8Args args, const Fp8PrepArgs prep,
                                                                        int join_blocks) {
@@ -553,9 +572,9 @@ __global__ __launch_bounds__(64 * WM * WN * KH, 2) void fp8_tile_kernel(const Fp
     // Groups v and v + 1 in the stages S = v % 4 and S + 1.  At the barrier their copies have landed, and the scales.  The
     // copies of v + 2 and v + 3 go to stages whose last reads were before this barrier, and so do the scales (at S = 0
     // this turn's for its last two groups, at S = 2 the next turn's for its first two); operands go to slots whose last
-    // steps were issued.  Loads are requested a few with each tile: a burst of them fills the load unit's queue, and a
-    // wavefront that waits there issues no matrix-core steps either (all at the group's start: 204 us for the 200 of
-    // the first case below, 76 of them lost to the 48 KB a group in a timing copy without loads).
+    // steps were issued.  Loads are requested a few with each tile: a burst of
+    // them fills the load unit's queue, and a wavefront that waits there issues no matrix-core steps either (2 x 11008 <- 4096
+    // at T = 2048, the whole call: 200 us with them all at the start of a group, 190 so).
     // The waits count the loads behind the one that is due, so that none may move: the barriers keep the
     // order under any scheduling.
     // A tile's sums are added just before their registers take the next tile's, the last ones after the next barrier.
@@ -856,8 +875,9 @@ hipError_t launch_repack_fp8(const uint8_t* codes, const float* scales, int64_t 
     return hipGetLastError();
 }
 
-// Four groups of loads in flight per thread where there are enough workgroups without.
-constexpr int64_t kQuantWide = (int64_t)1 << 22;  // inputs
+// Four groups of loads in flight per thread from here on, else one (the call on 128 rows, four and one: T = 8000, d = 4096,
+// r = 64 72 and 75 us, T = 4096 58.7 and 59.5, T = 2048 33 and 33; r = 0, T = 2048 17.7 and 16.3).
+constexpr int64_t kQuantWide = (int64_t)1 << 24;  // inputs
 
 template <int TT, int NJ, int U>
 static void launch_fp8_prep_n(const Fp8PrepArgs& a, const Fp8Args* experts, int64_t row_blocks, hipStream_t stream) {

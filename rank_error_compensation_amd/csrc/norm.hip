@@ -7,6 +7,9 @@
 // Rows go to teams of TPR threads that hold V values each.  Workgroups take rows in turn: w and b, and in the
 // gradient the column sums, stay in registers over all rows of a team.  The column sums of the workgroups meet in a
 // second launch, in a fixed order: no atomics, so results do not depend on the order of execution.
+// Bound by memory: 16383 x 4096 fp16 50 us (268 MB at 5.3 TB/s); its gradients at 16384 rows 85 + 2 us (403 MB at 4.7 TB/s;
+// the workgroups' sums and the second launch's start are the rest of the call's 88).  One row of 4096: 3.1 us, a load latency,
+// two sums over the team and a store (11 us a call from the host); 515 x 2048 fp32 gradients 6.4 + 2.1 us.
 #include <algorithm>
 
 #include "glowq.h"
@@ -157,15 +160,19 @@ __global__ __launch_bounds__(norm_threads<TPR>()) void norm_kernel(const S* x, c
     }
 }
 
-constexpr int kBackThreads = 1024;
+// Threads of a workgroup: 1024, or 512 where a thread holds more than 8 values (registers).
+template <int V>
+constexpr int back_threads() {
+    return V <= 8 ? 1024 : 512;
+}
 
 // part [gridDim.x][2][d]: the workgroup's sums of dy xhat and dy, its teams' added in order.
 template <typename S, int TPR, int V, bool NT>
-__global__ __launch_bounds__(kBackThreads) void norm_backward_kernel(const S* dy, const S* x, const float* __restrict__ mean,
+__global__ __launch_bounds__(back_threads<V>()) void norm_backward_kernel(const S* dy, const S* x, const float* __restrict__ mean,
                                                                             const float* __restrict__ rstd,
                                                                             const S* __restrict__ w, int T, int d, S* dx,
                                                                             float* __restrict__ part) {
-    constexpr int N = Piece<S>::N, P = V / N, B = kBackThreads, RG = B / TPR;
+    constexpr int N = Piece<S>::N, P = V / N, B = back_threads<V>(), RG = B / TPR;
     __shared__ float slots[2][B / 64 * 2];
     __shared__ float cols[RG > 1 ? B * N : 1];
     const int sub = threadIdx.x % TPR, team = threadIdx.x / TPR;
@@ -305,7 +312,7 @@ hipError_t launch_norm_n(const NormArgs& a, hipStream_t stream) {
 
 template <typename S, int TPR, int V>
 hipError_t launch_norm_backward_n(const NormArgs& a, hipStream_t stream) {
-    constexpr int B = kBackThreads, RG = B / TPR;
+    constexpr int B = back_threads<V>(), RG = B / TPR;
     const int grid = (int)std::min<int64_t>(ceil_div(a.T, RG), kNormParts);
     const S *dy = static_cast<const S*>(a.dy), *x = static_cast<const S*>(a.x), *w = static_cast<const S*>(a.w);
     if ((int64_t)a.T * a.d * (int64_t)sizeof(S) > kStreamBytes)
@@ -321,6 +328,10 @@ hipError_t launch_norm_backward_n(const NormArgs& a, hipStream_t stream) {
     return hipGetLastError();
 }
 
+// Teams just wide enough: idle threads cost as much as busy ones (2^24 values fp16, us: d = 128 16 threads x 8 values 15.5, 32 x
+// 8 26.6; 512 64 x 8 15.6, 128 x 8 25; 2048 256 x 8 16.4, 512 x 8 25.4), while fewer values a thread cost little (1024: 64 x 16
+// 15.6, 128 x 8 16.3; 4096: 256 x 16 16.7, 512 x 8 17.1, one row 3.4 and 3.1; 16384: 512 x 32 20.2, 1024 x 16 18.8, fp32 25.7
+// and 26.8).
 template <typename S>
 hipError_t launch_norm_t(const NormArgs& a, hipStream_t stream) {
     if (a.d <= 128) return launch_norm_n<S, 16, 8>(a, stream);
@@ -333,15 +344,19 @@ hipError_t launch_norm_t(const NormArgs& a, hipStream_t stream) {
     return launch_norm_n<S, 512, 32>(a, stream);
 }
 
+// As above, at 8 values a thread, whose column sums leave room to request the next row ahead (2^24 values fp16, us: d = 256
+// 32 x 8 23.6, 64 x 8 40; 4096 512 x 8 26.9, 256 x 16 28.5; 8192 1024 x 8 34.6, 512 x 16 36.4, fp32 47.6 and 51.9); above,
+// 512 x 32 (16384: 51 us; 1024 threads x 16 spill: 60).
 template <typename S>
 hipError_t launch_norm_backward_t(const NormArgs& a, hipStream_t stream) {
     if (a.d <= 128) return launch_norm_backward_n<S, 16, 8>(a, stream);
+    if (a.d <= 256) return launch_norm_backward_n<S, 32, 8>(a, stream);
     if (a.d <= 512) return launch_norm_backward_n<S, 64, 8>(a, stream);
     if (a.d <= 1024) return launch_norm_backward_n<S, 128, 8>(a, stream);
     if (a.d <= 2048) return launch_norm_backward_n<S, 256, 8>(a, stream);
     if (a.d <= 4096) return launch_norm_backward_n<S, 512, 8>(a, stream);
     if (a.d <= 8192) return launch_norm_backward_n<S, 1024, 8>(a, stream);
-    return launch_norm_backward_n<S, 1024, 16>(a, stream);
+    return launch_norm_backward_n<S, 512, 32>(a, stream);
 }
 
 }  // namespace

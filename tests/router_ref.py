@@ -162,8 +162,9 @@ def norm_backward(dy, x, mean, rstd, w, kind):
     e1 = (CHAIN + 3) * U32 * np.abs(g).mean(1, keepdims=True)
     e2 = (CHAIN + 6) * U32 * np.abs(g * xh).mean(1, keepdims=True)
     err = rs * (5 * U32 * np.abs(g) + e1 + 3 * U32 * np.abs(c1) + np.abs(xh) * (e2 + 6 * U32 * np.abs(c2))) * 1.01 + U32 * np.abs(dx)
-    # rows in turn in a workgroup, its teams (16 at most), then up to 16 workgroups' sums in a wavefront and 16 wavefronts
-    chain = -(-T // 256) + 16 + 16 + 16 + 6
+    # additions: rows in turn in a team (a 256th of them at most), a workgroup's teams (1024 threads in 16s: 64 at most), then up
+    # to 16 workgroups' sums in a wavefront and 16 wavefronts; 6 steps of the term itself
+    chain = -(-T // 256) + 64 + 16 + 16 + 6
     dw, db = (g0 * xh).sum(0), g0.sum(0)
     return ((dx, err + HALF[kind] * (np.abs(dx) + err) + TINY[kind]),
             (dw, chain * U32 * np.abs(g0 * xh).sum(0) + 2.0 ** -149), (db, chain * U32 * np.abs(g0).sum(0) + 2.0 ** -149))
