@@ -362,13 +362,13 @@ __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(const Rou
     __shared__ float sums[TB][L * EPL];
     const int i = threadIdx.x % L, slot = threadIdx.x / L;
     const int t = blockIdx.x * TB + slot;
-    const bool live = t < a.T;
+    const bool there = t < a.T;
     const int E = a.n_exp, K = a.top_k;
-    const S* row = static_cast<const S*>(a.logits) + (size_t)(live ? t : 0) * E;
+    const S* row = static_cast<const S*>(a.logits) + (size_t)(there ? t : 0) * E;
     const bool softmax = a.score == GLOWQ_SCORE_SOFTMAX;
     int e = -1;
     float dw = 0.f;
-    if (i < K && live) {
+    if (i < K && there) {
         e = a.ids[(size_t)t * K + i];
         dw = a.w[(size_t)t * K + i];
         if (e < -1 || e >= E) {
@@ -378,6 +378,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(const Rou
     }
     const float l = e >= 0 ? (float)row[e] : -INFINITY;
     if (l == -INFINITY) e = -1, dw = 0.f;  // an expert that is out has score 0 whatever its logit does
+    const bool live = lanes_with<L>(e >= 0) != 0;  // else the row is zeros: a refused one's logits may hold NaN
     float* mine = sums[slot];
 #pragma unroll
     for (int j = 0; j < EPL; ++j) mine[i + L * j] = 0.f;
@@ -413,12 +414,12 @@ __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(const Rou
         if (i == r && e >= 0) mine[e] += g;
         wave_sync();
     }
-    if (!live) return;
+    if (!there) return;
     S* out = static_cast<S*>(a.out) + (size_t)t * E;
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
         const int x = i + L * j;
-        if (x < E) out[x] = (S)(softmax && !a.renorm ? p[j] * (mine[x] - dot) : mine[x]);
+        if (x < E) out[x] = (S)(softmax && !a.renorm && live ? p[j] * (mine[x] - dot) : mine[x]);
     }
 }
 

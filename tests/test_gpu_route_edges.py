@@ -1,0 +1,52 @@
+"""The router where rows, biases and scores end: rows without a choice in the gradient, standings of groups that cancel,
+rows of the type's lowest value, renormalised sigmoids too small for a number."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import layer_ref as R
+import router_ref as Q
+from gpu_util import glowq, log
+from test_gpu_moe_route import KINDS, check, made, ws
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    glowq()
+    yield
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("kind", ["f16", "f32"])
+@pytest.mark.parametrize("E,k", [(60, 4), (128, 8), (250, 16), (200, 40)])
+def test_gradient_of_rows_without_a_choice_is_zero(E, k, kind):
+    """Rows that the router refused (NaN, +inf), rows of -inf alone and rows whose choices are all of experts that are out:
+    no choice is live, so that the row is zeros whatever its logits and its weights' gradients are."""
+    g = glowq()
+    lo, _ = made(12, E, kind, 5)
+    clean = lo.clone()
+    lo[1, 7], lo[3, E - 1], lo[4], lo[6, 0] = math.nan, math.inf, -math.inf, math.nan
+    lo[8, :k] = -math.inf
+    none = [1, 3, 4, 6, 8]
+    rest = [t for t in range(12) if t not in none]
+    for score in ("softmax", "sigmoid"):
+        for renorm in (True, False):
+            log(f"route gradient without a choice {E} {k} {kind} {score} renorm={renorm}")
+            w_ = ws()
+            ids, _ = g.moe_route(lo.cuda(), k, score, renorm=renorm, workspace=w_)
+            assert g.workspace_status(w_) == g.ERR_ROUTING
+            assert (ids[[1, 3, 4, 6]] == -1).all()
+            ids[8] = torch.arange(k, dtype=torch.int32)  # experts of logit -inf
+            dw = torch.randn(12, k, generator=torch.Generator().manual_seed(3))
+            dw[4] = math.nan
+            got = g.moe_route_backward(dw.cuda(), lo.cuda(), ids, score, renorm, 2.5, w_)
+            assert g.workspace_status(w_) == g.OK
+            assert (got[none] == 0).all(), (score, renorm, got[none].isnan().any(1).tolist())
+            ref, bound = Q.route_backward(dw[rest], clean[rest], ids[rest], score, renorm, 2.5, kind)
+            R.within(got[rest], ref, bound, f"{score} renorm={renorm}")
