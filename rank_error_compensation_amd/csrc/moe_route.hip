@@ -21,8 +21,10 @@
 //   sigmoid  exp is off by 2 |l| + 4 steps of itself (its argument's rounding, its own), which moves s by s (1 - s) of
 //            that, 1.5 at most; the quotient and the product add 3, the bias one of the value: 6 + |v|
 //   softmax  exp as above, and the sum by one for each of its 20 additions in a row at most, all of s: 32 + |v|
-// So two values further apart than 2^-20 (1 + |v|), or 2^-18 (1 + |v|), are in their exact order, and two sums of two
-// at twice that; a token with a closer pair at a place that matters is decided again in fp64, by the whole wavefront.
+// So two values further apart than 2^-20 (1 + |v|), or 2^-18 (1 + |v|), are in their exact order.  A group's standing is
+// off by half of that for each value in it (values of opposite signs cancel, their errors do not), and the groups that stay are
+// the exact ones if none that is out comes within its error of one that stays within its own.  A token that is closer
+// at a place that matters is decided again in fp64, by the whole wavefront.
 // Bound by the keys' arithmetic (64-bit maxima) where scores decide, else by memory and the launch: 32767 x 256 fp32 logits, 8
 // choices: from 4 of 8 groups with a bias 32 us (34 MB: 1 TB/s), plain softmax 15.5 us; one token 2.6 us; gradient of
 // 16384 x 60, 4 choices 4.4 us (8 MB).
@@ -113,7 +115,7 @@ __device__ __forceinline__ F sigmoid_of(F l) {
 __device__ __forceinline__ float close_to(const RouteArgs& a) { return a.score == GLOWQ_SCORE_SIGMOID ? 0x1p-20f : 0x1p-18f; }
 
 // Standings of the groups from the token's values `by` [E] in LDS (-inf: out): bit g of the answer is set where group g
-// stays.  `near`: two groups are closer than fp32 scores tell apart.
+// stays.  `near`: fp32 scores do not tell apart which ones do.
 template <int L, typename F>
 __device__ __forceinline__ uint32_t groups_that_stay(const F* by, const RouteArgs& a, int i, bool& near) {
     const int n = a.n_exp / a.n_group;
@@ -128,19 +130,25 @@ __device__ __forceinline__ uint32_t groups_that_stay(const F* by, const RouteArg
             b1 = fmax(b1, v);
         }
     }
-    const F stand = a.group_best == 2 && b2 > (F)-INFINITY ? b1 + b2 : b1;
+    F stand = b1, size = (F)1 + fabs(b1);
+    if (a.group_best == 2 && b2 > (F)-INFINITY) {
+        stand += b2;
+        size += (F)1 + fabs(b2);
+    }
     int rank = 0;
 #pragma unroll 4
     for (int h = 0; h < a.n_group; ++h) {
         const F other = __shfl(stand, h, L);
         rank += other > stand || (other == stand && h < i) ? 1 : 0;
     }
-    // the last group that stays and the first that does not (-inf from -inf: NaN, not near)
-    const uint64_t last = lanes_with<L>(i < a.n_group && rank == a.keep_groups - 1);
-    const uint64_t next = lanes_with<L>(i < a.n_group && rank == a.keep_groups);
-    const F in = __shfl(stand, __ffsll((unsigned long long)last) - 1, L), out = __shfl(stand, __ffsll((unsigned long long)next) - 1, L);
-    near = next != 0 && in - out <= (F)(2.f * close_to(a)) * ((F)1 + fabs(in));
-    return (uint32_t)lanes_with<L>(rank < a.keep_groups && i < a.n_group);
+    const bool in = i < a.n_group && rank < a.keep_groups;
+    // the lowest that a group which stays may stand, the highest of one that does not; groups without experts are in their place
+    const F err = (F)(0.5f * close_to(a)) * size;
+    const bool some = stand > (F)-INFINITY;
+    const F low = lanes_max<L>(in && some ? err - stand : (F)-INFINITY);
+    const F high = lanes_max<L>(!in && some ? stand + err : (F)-INFINITY);
+    near = high >= -low;
+    return (uint32_t)lanes_with<L>(in);
 }
 
 // Expert e's group stays.  e / n without a division: e < 256, 1 <= n <= 256.

@@ -50,3 +50,22 @@ def test_gradient_of_rows_without_a_choice_is_zero(E, k, kind):
             assert (got[none] == 0).all(), (score, renorm, got[none].isnan().any(1).tolist())
             ref, bound = Q.route_backward(dw[rest], clean[rest], ids[rest], score, renorm, 2.5, kind)
             R.within(got[rest], ref, bound, f"{score} renorm={renorm}")
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("size", [1.0, 30.0, 100.0, 1000.0, 1e6])
+def test_standings_that_cancel(size, score):
+    """Groups by their two best, which have a bias of B and one of -B (B of its own for every group): the sum is about that of two
+    scores, its error in fp32 that of B, and the groups' scores are as far apart as such an error.  The other experts are out."""
+    gen = torch.Generator().manual_seed(int(size))
+    for E, G, keep in ((16, 4, 1), (64, 8, 3), (256, 16, 7)):
+        n, T = E // G, 400
+        lo = torch.full((T, E), -math.inf)
+        bias = torch.zeros(E)
+        for grp in range(G):
+            B = size * float(torch.rand((), generator=gen))
+            a, b = (grp * n + torch.randperm(n, generator=gen)[:2]).tolist()
+            lo[:, a], lo[:, b] = (1e-6 * size * torch.randn(T, generator=gen) for _ in range(2))
+            bias[a], bias[b] = B, -B
+        log(f"cancelling standings {score} B={size} E={E}")
+        check(lo, 2 * keep, score, bias, G, keep, 2, what=f"cancelling {E}")
