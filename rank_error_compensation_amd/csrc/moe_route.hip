@@ -21,10 +21,11 @@
 //   sigmoid  exp is off by 2 |l| + 4 steps of itself (its argument's rounding, its own), which moves s by s (1 - s) of
 //            that, 1.5 at most; the quotient and the product add 3, the bias one of the value: 6 + |v|
 //   softmax  exp as above, and the sum by one for each of its 20 additions in a row at most, all of s: 32 + |v|
-// So two values further apart than 2^-20 (1 + |v|), or 2^-18 (1 + |v|), are in their exact order.  A group's standing is
-// off by half of that for each value in it (values of opposite signs cancel, their errors do not), and the groups that stay are
-// the exact ones if none that is out comes within its error of one that stays within its own.  A token that is closer
-// at a place that matters is decided again in fp64, by the whole wavefront.
+// So two values further apart than 2^-20 (1 + |v|), or 2^-18 (1 + |v|), are in their exact order.  A group's standing by
+// two, taken as half their sum (which no two numbers overflow), is off by half of that at 1 + the halves of both magnitudes
+// (values of opposite signs cancel, their errors do not), and groups are in their exact order if no one that is out comes within
+// its error of one that stays within its own.  A token that is closer at a place that matters is decided again in fp64, by
+// the whole wavefront.
 // Bound by the keys' arithmetic (64-bit maxima) where scores decide, else by memory and the launch: 32767 x 256 fp32 logits, 8
 // choices: from 4 of 8 groups with a bias 32 us (34 MB: 1 TB/s), plain softmax 15.5 us; one token 2.6 us; gradient of
 // 16384 x 60, 4 choices 4.4 us (8 MB).
@@ -130,10 +131,11 @@ __device__ __forceinline__ uint32_t groups_that_stay(const F* by, const RouteArg
             b1 = fmax(b1, v);
         }
     }
-    F stand = b1, size = (F)1 + fabs(b1);
-    if (a.group_best == 2 && b2 > (F)-INFINITY) {
-        stand += b2;
-        size += (F)1 + fabs(b2);
+    F stand = b1, size = fabs(b1);
+    if (a.group_best == 2) {
+        const F half = b2 > (F)-INFINITY ? (F)0.5 * b2 : (F)0;
+        stand = (F)0.5 * b1 + half;
+        size = (F)0.5 * fabs(b1) + fabs(half);
     }
     int rank = 0;
 #pragma unroll 4
@@ -143,7 +145,7 @@ __device__ __forceinline__ uint32_t groups_that_stay(const F* by, const RouteArg
     }
     const bool in = i < a.n_group && rank < a.keep_groups;
     // the lowest that a group which stays may stand, the highest of one that does not; groups without experts are in their place
-    const F err = (F)(0.5f * close_to(a)) * size;
+    const F err = (F)(0.5f * close_to(a)) * ((F)1 + size);
     const bool some = stand > (F)-INFINITY;
     const F low = lanes_max<L>(in && some ? err - stand : (F)-INFINITY);
     const F high = lanes_max<L>(!in && some ? stand + err : (F)-INFINITY);

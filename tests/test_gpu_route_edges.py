@@ -69,3 +69,19 @@ def test_standings_that_cancel(size, score):
             bias[a], bias[b] = B, -B
         log(f"cancelling standings {score} B={size} E={E}")
         check(lo, 2 * keep, score, bias, G, keep, 2, what=f"cancelling {E}")
+
+
+def test_standings_past_the_largest_number():
+    """Biases of the type's lowest value: a group that they hold down still stands above a group without experts, and its two
+    best add up to more than fp32 holds."""
+    low = -3.4028234663852886e38
+    lo = torch.randn(20, 16, generator=torch.Generator().manual_seed(1))
+    lo[:, :4] = -math.inf
+    lo[:10, 4:6] = -math.inf
+    bias = torch.zeros(16)
+    bias[8:] = low
+    for score in ("softmax", "sigmoid"):
+        for keep in (1, 2, 3):
+            for best in (1, 2):
+                check(lo, 8, score, bias, 4, keep, best, what=f"{score} {keep} {best}")
+        check(lo, 8, score, -bias, 4, 2, 2, what=f"{score} largest")
