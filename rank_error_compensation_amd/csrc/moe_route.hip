@@ -30,6 +30,7 @@
 // choices: from 4 of 8 groups with a bias 32 us (34 MB: 1 TB/s), plain softmax 15.5 us; one token 2.6 us; gradient of
 // 16384 x 60, 4 choices 4.4 us (8 MB).
 #include <algorithm>
+#include <cfloat>
 
 #include "glowq.h"
 #include "layer.h"
@@ -258,7 +259,7 @@ __global__ __launch_bounds__(kRouteThreads, 6) void route_kernel(const RouteArgs
     if (softmax && (SCORED || !a.renorm)) {
 #pragma unroll
         for (int j = 0; j < EPL; ++j) top = fmaxf(top, v[j]);
-        top = fmaxf(lanes_max<L>(top), -3e38f);  // a row without experts: no NaN
+        top = fmaxf(lanes_max<L>(top), -FLT_MAX);  // a row without experts: no NaN
         sum = 0.f;
 #pragma unroll
         for (int j = 0; j < EPL; ++j) sum += __expf(v[j] - top);
@@ -349,7 +350,7 @@ __global__ __launch_bounds__(kRouteThreads, 6) void route_kernel(const RouteArgs
     float w = 0.f;
     if (a.renorm) {
         // the chosen scores over their sum; sigmoids of very low logits as exp(l), from the largest on
-        const float m = fmaxf(lanes_max<L>(l), -3e38f);
+        const float m = fmaxf(lanes_max<L>(l), -FLT_MAX);
         const float s = e < 0 ? 0.f : (softmax || m < -80.f ? expf(l - m) : sigmoid_of(l));
         const float all = lanes_sum<L>(s);
         w = e < 0 ? 0.f : a.scale * (s / all);
@@ -394,7 +395,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(const Rou
     for (int j = 0; j < EPL; ++j) mine[i + L * j] = 0.f;
     float v[EPL], p[EPL], dot = 0.f, g;
     if (a.renorm) {
-        const float m = fmaxf(lanes_max<L>(l), -3e38f);
+        const float m = fmaxf(lanes_max<L>(l), -FLT_MAX);
         const float s = e < 0 ? 0.f : (softmax || m < -80.f ? expf(l - m) : sigmoid_of(l));
         const float all = lanes_sum<L>(s);
         const float share = e < 0 ? 0.f : s / all;
@@ -407,7 +408,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(const Rou
             v[j] = i + L * j < E ? (float)row[i + L * j] : -INFINITY;
             top = fmaxf(top, v[j]);
         }
-        top = fmaxf(lanes_max<L>(top), -3e38f);
+        top = fmaxf(lanes_max<L>(top), -FLT_MAX);
 #pragma unroll
         for (int j = 0; j < EPL; ++j) sum += p[j] = __expf(v[j] - top);
         sum = lanes_sum<L>(sum);

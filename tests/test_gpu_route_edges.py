@@ -85,3 +85,34 @@ def test_standings_past_the_largest_number():
             for best in (1, 2):
                 check(lo, 8, score, bias, 4, keep, best, what=f"{score} {keep} {best}")
         check(lo, 8, score, -bias, 4, 2, 2, what=f"{score} largest")
+
+
+@pytest.mark.parametrize("kind", ["f16", "f32"])
+@pytest.mark.parametrize("E,k", [(60, 4), (128, 8), (256, 8), (100, 20)])
+def test_rows_of_the_lowest_value(E, k, kind):
+    """Logits masked with the type's lowest value instead of -inf: experts of a row of it alone share it evenly, and beside others
+    they have no weight."""
+    g = glowq()
+    low = torch.finfo(KINDS[kind]).min
+    lo, b = made(9, E, kind, 6)
+    lo[0] = low
+    lo[1], lo[1, : k + 2] = -math.inf, low
+    lo[2], lo[2, 5] = low, 1.0
+    lo[3, ::2] = low
+    lo[4], lo[4, 3] = low, low / 2
+    lo[5], lo[5, 3] = -math.inf, low
+    for score in ("softmax", "sigmoid"):
+        for renorm in (True, False):
+            for bias, G, keep, best in ((None, 1, 1, 1), (b, 1, 1, 1), (b, 4, 2, 2), (None, 4, 2, 2)):
+                log(f"lowest {E} {k} {kind} {score} renorm={renorm} bias={bias is not None} groups={G}")
+                ids, w = check(lo, k, score, bias, G, keep, best, renorm, 1.0, f"{score} renorm={renorm}")
+                if renorm:
+                    assert (w.sum(1) - 1).abs().max() < 1e-5
+                if score == "softmax":
+                    live = float((lo[0] == low).sum())
+                    assert (w[0] - (1 / k if renorm else 1 / live)).abs().max() < 1e-6
+                dw = torch.randn(9, k, generator=torch.Generator().manual_seed(3))
+                got = g.moe_route_backward(dw.cuda(), lo.cuda(), ids, score, renorm, 1.0, ws())
+                assert torch.isfinite(got).all()
+                ref, bound = Q.route_backward(dw, lo, ids, score, renorm, 1.0, kind)
+                R.within(got, ref, bound, f"gradient {score} renorm={renorm}")
