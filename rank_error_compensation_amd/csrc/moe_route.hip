@@ -113,6 +113,13 @@ __device__ __forceinline__ F sigmoid_of(F l) {
     return l >= (F)0 ? q : e * q;
 }
 
+// A chosen expert's score next to the others' for logits m at most: softmax over the largest, sigmoid over exp(min(m, 0)), so
+// that scores which no number holds keep their ratios.
+__device__ __forceinline__ float score_beside(float l, float m, bool softmax) {
+    if (softmax) return expf(l - m);
+    return expf(fminf(l, 0.f) - fminf(m, 0.f)) * (1.f / (1.f + expf(-fabsf(l))));
+}
+
 // How near two values may be before fp64 decides (above), for values v about 1 + |v| large.
 __device__ __forceinline__ float close_to(const RouteArgs& a) { return a.score == GLOWQ_SCORE_SIGMOID ? 0x1p-20f : 0x1p-18f; }
 
@@ -349,9 +356,9 @@ __global__ __launch_bounds__(kRouteThreads, 6) void route_kernel(const RouteArgs
     const float l = e >= 0 ? (float)row[e] : -INFINITY;
     float w = 0.f;
     if (a.renorm) {
-        // the chosen scores over their sum; sigmoids of very low logits as exp(l), from the largest on
+        // the chosen scores over their sum
         const float m = fmaxf(lanes_max<L>(l), -FLT_MAX);
-        const float s = e < 0 ? 0.f : (softmax || m < -80.f ? expf(l - m) : sigmoid_of(l));
+        const float s = e < 0 ? 0.f : score_beside(l, m, softmax);
         const float all = lanes_sum<L>(s);
         w = e < 0 ? 0.f : a.scale * (s / all);
     } else if (e >= 0) {
@@ -396,7 +403,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(const Rou
     float v[EPL], p[EPL], dot = 0.f, g;
     if (a.renorm) {
         const float m = fmaxf(lanes_max<L>(l), -FLT_MAX);
-        const float s = e < 0 ? 0.f : (softmax || m < -80.f ? expf(l - m) : sigmoid_of(l));
+        const float s = e < 0 ? 0.f : score_beside(l, m, softmax);
         const float all = lanes_sum<L>(s);
         const float share = e < 0 ? 0.f : s / all;
         const float c = lanes_sum<L>(share * dw);

@@ -116,3 +116,26 @@ def test_rows_of_the_lowest_value(E, k, kind):
                 assert torch.isfinite(got).all()
                 ref, bound = Q.route_backward(dw, lo, ids, score, renorm, 1.0, kind)
                 R.within(got, ref, bound, f"gradient {score} renorm={renorm}")
+
+
+@pytest.mark.parametrize("kind", ["f16", "f32"])
+def test_renormalised_sigmoids_below_the_smallest_number(kind):
+    """Chosen logits whose sigmoids are subnormal or zero in fp32 beside ones that are not: the weights are ratios, with the
+    bits of any other."""
+    g = glowq()
+    rows = [[-75.0, -90.0, -95.0, -100.0], [-75.0, -100.0, -76.0, -75.5], [-20.0, -100.0, -105.0, -90.0], [-17.0, -101.5, -16.5, -17.5],
+            [-79.9, -103.0, -104.0, -110.0], [-80.1, -103.0, -104.0, -110.0], [-1.0, -85.0, -88.0, -0.5], [-5.0, -92.0, -88.5, -90.0],
+            [0.0, -20.0, -80.0, -86.0], [30.0, -20.0, -50.0, 16.0], [-87.0, -103.9, -104.1, -130.0], [-0.0, -1e-3, 1e-3, -12.0]]
+    lo = torch.full((len(rows), 20), -math.inf)
+    lo[:, 3:7] = torch.tensor(rows)
+    lo = lo.to(KINDS[kind])
+    for bias in (None, torch.linspace(-1, 1, 20)):
+        for scale in (1.0, 2.5):
+            check(lo, 4, "sigmoid", bias, scale=scale, what="small sigmoids")
+            check(lo, 3, "sigmoid", bias, scale=scale, what="small sigmoids, three")
+    for k in (2, 3, 4):
+        ids, _ = g.moe_route(lo.cuda(), k, "sigmoid")
+        dw = torch.randn(len(rows), k, generator=torch.Generator().manual_seed(3))
+        got = g.moe_route_backward(dw.cuda(), lo.cuda(), ids, "sigmoid", True, 2.5, ws())
+        ref, bound = Q.route_backward(dw, lo, ids, "sigmoid", True, 2.5, kind)
+        R.within(got, ref, bound, f"gradient {k}")
