@@ -736,14 +736,18 @@ __global__ __launch_bounds__(64 * WM * WN * KH, 2) void fp8_tile_kernel(const Fp
         }
         auto rcopy = [&](int j, uint8_t* stg) {
             if (64 * j >= rp) return;
-            if (args.r_ranges > 0) {  // R as the K ranges' fp32 sums: added in order, rounded once to fp16 here
+            // R as the K ranges' fp32 sums: added in order, rounded once to fp16 here (teams without a K split; the launchers
+            // refuse it elsewhere)
+            if constexpr (KH > 1) {
+                if (args.r_ranges > 0) {
 #pragma unroll
-                for (int i = 0; i < NE; ++i) {
-                    const int row = 8 * (NE * wave_all + i) + (lane >> 3), c = lane & 7;
-                    *reinterpret_cast<h8*>(stg + row * 128 + 16 * (c ^ ((row >> 1) & 7) ^ (((row >> 2) ^ (row >> 3)) & 1))) =
-                        r_columns(args, rrow[i], 64 * j + 8 * c);
+                    for (int i = 0; i < NE; ++i) {
+                        const int row = 8 * (NE * wave_all + i) + (lane >> 3), c = lane & 7;
+                        *reinterpret_cast<h8*>(stg + row * 128 + 16 * (c ^ ((row >> 1) & 7) ^ (((row >> 2) ^ (row >> 3)) & 1))) =
+                            r_columns(args, rrow[i], 64 * j + 8 * c);
+                    }
+                    return;
                 }
-                return;
             }
             const uint8_t* base = static_cast<const uint8_t*>(args.R) + 128 * j;
 #pragma unroll
@@ -848,7 +852,7 @@ __global__ __launch_bounds__(256) void fp8_tile_join_kernel(const Fp8Args args, 
         const h8 zero8 = {0, 0, 0, 0, 0, 0, 0, 0};
         for (int kb = 0; kb < rp / 32; ++kb) {
             const int c = 32 * kb + 8 * (lane >> 4);
-            const h8 bv = r_columns(args, ok ? t : 0, c);
+            const h8 bv = load_h8(static_cast<const _Float16*>(args.R) + (size_t)(ok ? t : 0) * rp + c);
 #pragma unroll
             for (int rr = 0; rr < RR; ++rr) {
                 const int row = (rt0 + rr) * 16 + (lane & 15);
@@ -928,7 +932,7 @@ static hipError_t launch_fp8_split(const Fp8Args& a, int64_t items, hipStream_t 
 // Every XCD takes an eighth of the work, rounded up; workgroups without any return at once.
 template <int WM, int WN, int TT>
 static hipError_t launch_fp8_experts(const Fp8Args& a, const Fp8PrepArgs& p, int64_t items, hipStream_t stream) {
-    if (!a.r_by_token && a.r_ranges > 0) return hipErrorInvalidValue;  // own projections come as R
+    if (a.r_ranges > 0) return hipErrorInvalidValue;  // projections come as R
     const dim3 grid((unsigned)(8 * ceil_div(items, 8))), block(64 * WM * WN);
     if (a.r > 0) hipLaunchKernelGGL((fp8_tile_kernel<WM, WN, TT, 1, kFp8Correct, true>), grid, block, 0, stream, a, p, 0);
     else hipLaunchKernelGGL((fp8_tile_kernel<WM, WN, TT, 1, kFp8Plain, true>), grid, block, 0, stream, a, p, 0);
@@ -942,6 +946,7 @@ static hipError_t launch_fp8_tile(const Fp8Args& a, const Fp8PrepArgs& p, hipStr
                              ? ceil_div(ceil_div((int64_t)p.T * p.rp / 4, 64 * WM * WN * KH), 8) * 8 : 0;
     const int64_t grid = join + 8 * ceil_div((int64_t)a.row_blocks * a.ks, 8) * a.m_blocks;
     if (grid * 64 * WM * WN * KH > (int64_t)UINT32_MAX) return hipErrorInvalidConfiguration;
+    if (a.r_ranges > 0 && (KH == 1 || a.ks > 1)) return hipErrorInvalidValue;  // the projection comes as R
     const dim3 g((unsigned)grid), block(64 * WM * WN * KH);
     if constexpr (SPLIT) {
         if (a.ks > 1) {
