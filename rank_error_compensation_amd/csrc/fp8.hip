@@ -727,9 +727,10 @@ __global__ __launch_bounds__(64 * WM * WN * KH, 2) void fp8_tile_kernel(const Fp
         const int r = args.r, rp = args.rp;
         int rrow[NE];  // rows of R that the lane copies
         {
-            int rows[NE], tok[NE];
+            int rows[NE], tok[NE], first = j0;
+            asm volatile("" : "+s"(first));  // found again: the codes' rows are not kept over the loop (they spilled)
 #pragma unroll
-            for (int i = 0; i < NE; ++i) rows[i] = min(j0 + 8 * (NE * wave_all + i) + (lane >> 3), j1 - 1);
+            for (int i = 0; i < NE; ++i) rows[i] = min(first + 8 * (NE * wave_all + i) + (lane >> 3), j1 - 1);
             tokens_of<EXPERTS>(args, rows, tok);
 #pragma unroll
             for (int i = 0; i < NE; ++i) rrow[i] = EXPERTS && args.r_by_token ? tok[i] : rows[i];

@@ -1,5 +1,6 @@
-"""What the block-scaled e4m3 tiles are compiled to: of the tiles that correct, only the one of four teams reads the projection as
-fp32 K ranges, so that only that one holds the code."""
+"""What the block-scaled e4m3 tiles are compiled to.  A tile whose registers do not suffice moves some of them to scratch memory,
+through the counter that the ring's waits count on; and of the tiles that correct, only the one of four teams reads the
+projection as fp32 K ranges, so that only that one holds the code."""
 import re
 
 from test_fp8_schedule_cpu import assembly
@@ -12,11 +13,12 @@ def tiles(text):
         yield [int(v) for v in re.findall(r"L[ib](\d+)E", m.group(2))], [t for t in lines if not t.startswith((".", ";"))]
 
 
-def test_tiles_hold_only_their_own_code(tmp_path):
+def test_tiles_hold_their_registers_and_only_their_own_code(tmp_path):
     found = list(tiles(assembly("default", tmp_path / "fp8.s")))
     assert len(found) >= 9
     for args, code in found:
         wm, wn, tt, kh, mode, experts = args
+        assert not [t for t in code if t.startswith("scratch_")], (args, "scratch")
         # roundings to fp16, two an instruction: the results alone (of a split launch the projection's join alone), and the
         # K ranges' sums of the projection in the correcting tile of several teams
         rounded = sum(t.startswith(("v_cvt_f16_f32", "v_cvt_pk_f16_f32")) for t in code)
