@@ -11,10 +11,6 @@ namespace {
 constexpr int kPrepThreads = 512;
 constexpr int kPrepWaves = kPrepThreads / 64;
 
-// Sums of R over the 32-input steps [s_begin, s_end) for 16 TT tokens and 16 NJ rank columns: the
-// wavefronts take steps in turn (U in flight) and add their tiles through LDS in wavefront order.
-// part != nullptr: fp32 sums of this range to part [T][rp]; else one rounding to fp16 into R.
-// Columns r .. r_pad - 1 are zero.
 // Where the inputs of TT rows of the result lie, as the rows themselves do.
 template <int TT>
 struct RowsInOrder {
@@ -26,7 +22,11 @@ struct RowsInOrder {
     }
 };
 
-// Rows t0 .. of the result, t_end at most; rows(t, at): where the inputs of the rows t lie.
+// Sums of R over the 32-input steps [s_begin, s_end) for 16 TT rows from t0 on (t_end at most) and 16 NJ rank columns: the
+// wavefronts take steps in turn (U in flight) and add their tiles through LDS in wavefront order.
+// part != nullptr: fp32 sums of this range to part [.][rp]; else one rounding to fp16 into R.
+// Columns r .. r_pad - 1 are zero.
+// rows(t, at): where the inputs of the rows t lie.
 // RUNS: a wavefront takes U steps in a row (whole lines of X and B, and the wavefronts together spread over the memory
 // channels: rows are often a multiple of their stride apart), else every kPrepWaves-th.
 template <int TT, int NJ, bool RUNS, class A, class Row>
