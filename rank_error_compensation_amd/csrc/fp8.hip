@@ -21,12 +21,15 @@
 //
 // Launches: codes, scales and the projection (with K ranges a launch more that adds them, where the product does not), then
 // the product, in pieces whose wavefronts share the input groups (few tokens: one round of loads each) or in tiles; with K
-// ranges of the tiles a last launch joins those.  r = 64, kernels alone / the call from the host, us:
-//   T = 1, 4096 + 2 x 1024 <- 4096         4.7 + 6.5 / 16.5 (two launches from the host; 25 MB of weights in 6.5 us)
-//   T = 77, 4096 <- 14336                  7.5 + 19 + 7.5 / 33.5 (eight ranges: 59 MB of weights, 17 MB of sums)
-//   T = 2048, 2 x 11008 <- 4096            15.5 + 4.5 + 170 / 195 (the tile 2.2 PFLOP/s, the library's product alone 2.25)
-//   T = 1, 4 of 60 experts 2048 -> 2 x 1408    4.7 + 6.7 / 16.8
-//   T = 4095, 60 experts, 4 choices        41 + 148 / 190 (a B each; 1.2 PFLOP/s: a fifth of the tiles' rows are empty)
+// ranges of the tiles a last launch joins those.  r = 64, kernels alone (shortest and mean of 53 warm runs: the clock falls while
+// the large products run) / the call from the host, us:
+//   T = 1, 4096 + 2 x 1024 <- 4096         4.3, 4.9 + 6.1, 7.2 / 16.8 (two launches from the host; 25 MB of weights)
+//   T = 77, 4096 <- 14336                  6.8, 8.1 + 17.8, 19.1 + 7.0, 7.2 / 33.6 (eight ranges: 59 MB of weights, 17 MB of sums)
+//   T = 2048, 2 x 11008 <- 4096            14.2, 15.8 + 4.0, 5.1 + 174, 187 / 199 (the tile 2.15 and 2.0 PFLOP/s, the library's
+//                                          product alone 2.25)
+//   T = 1, 4 of 60 experts 2048 -> 2 x 1408    4.3, 4.9 + 6.3, 7.3 / 17.3
+//   T = 4095, 60 experts, 4 choices        38, 45 + 147, 160 / 190 (a B each; 1.2 PFLOP/s: a fifth of the tiles' token rows
+//                                          are empty, and 2 x 1408 rows are computed as 2 x 1536)
 #include <algorithm>
 #include <type_traits>
 
@@ -424,8 +427,8 @@ __global__ __launch_bounds__(64 * kFp8Waves) void fp8_split_kernel(const Fp8Args
 // workspace, and fp8_tile_join_kernel adds them in order and finishes.
 //
 // What bounds 128 x 256 tiles at T = 2048, 2 x 11008 <- 4096 (matrix cores busy 0.67 of the cycles): the loads'
-// issue and return beside the matrix cores (of 170 us, without the weights' loads 136-143, without the codes' 180, without both
-// 123-129; scaling costs nothing), and 2.7 tiles a slot.  256 x 256 on eight wavefronts took the same, 128 x 128 a fifth more.
+// issue and return beside the matrix cores (the call, 198 us, without the codes' loads 180, without the weights' 142, without
+// both 127; scaling costs nothing), and 2.7 tiles a slot.  256 x 256 on eight wavefronts took the same, 128 x 128 a fifth more.
 typedef __attribute__((address_space(3))) void lds_void;
 template <int I>
 using ic = std::integral_constant<int, I>;

@@ -7,8 +7,8 @@
 // Rows go to teams of TPR threads that hold V values each.  Workgroups take rows in turn: w and b, and in the
 // gradient the column sums, stay in registers over all rows of a team.  The column sums of the workgroups meet in a
 // second launch, in a fixed order: no atomics, so results do not depend on the order of execution.
-// Bound by memory: 16383 x 4096 fp16 50 us (268 MB at 5.3 TB/s); its gradients at 16384 rows 85 + 2 us (403 MB at 4.7 TB/s;
-// the workgroups' sums and the second launch's start are the rest of the call's 88).  One row of 4096: 3.1 us, a load latency,
+// Bound by memory: 16383 x 4096 fp16 50 us (268 MB at 5.3 TB/s); its gradients at 16384 rows 85 + 2 us at their shortest, 90 + 4
+// on average (403 MB at 4.7 and 4.5 TB/s; the call 88.5).  One row of 4096: 3.1 us, a load latency,
 // two sums over the team and a store (11 us a call from the host); 515 x 2048 fp32 gradients 6.4 + 2.1 us.
 #include <algorithm>
 
@@ -331,7 +331,8 @@ hipError_t launch_norm_backward_n(const NormArgs& a, hipStream_t stream) {
 // Teams just wide enough: idle threads cost as much as busy ones (2^24 values fp16, us: d = 128 16 threads x 8 values 15.5, 32 x
 // 8 26.6; 512 64 x 8 15.6, 128 x 8 25; 2048 256 x 8 16.4, 512 x 8 25.4), while fewer values a thread cost little (1024: 64 x 16
 // 15.6, 128 x 8 16.3; 4096: 256 x 16 16.7, 512 x 8 17.1, one row 3.4 and 3.1; 16384: 512 x 32 20.2, 1024 x 16 18.8, fp32 25.7
-// and 26.8).
+// and 26.8).  Between the powers of two a part of the threads is idle (the call, fp16, us: 512 17, 640 21.8, 768 18.9, 1024 17, 1280
+// 22.3, 1536 19.5, 2048 17, 5120 24.9, 12288 31.4; fp32 26 to 31 but 38.7 at 12288).
 template <typename S>
 hipError_t launch_norm_t(const NormArgs& a, hipStream_t stream) {
     if (a.d <= 128) return launch_norm_n<S, 16, 8>(a, stream);
@@ -346,7 +347,8 @@ hipError_t launch_norm_t(const NormArgs& a, hipStream_t stream) {
 
 // As above, at 8 values a thread, whose column sums leave room to request the next row ahead (2^24 values fp16, us: d = 256
 // 32 x 8 23.6, 64 x 8 40; 4096 512 x 8 26.9, 256 x 16 28.5; 8192 1024 x 8 34.6, 512 x 16 36.4, fp32 47.6 and 51.9); above,
-// 512 x 32 (16384: 51 us; 1024 threads x 16 spill: 60).
+// 512 x 32 (16384: 51 us; 1024 threads x 16 spill: 60).  Between the powers of two, as above: 512 25, 640 39, 768 35, 1024 25.5,
+// 1280 39, 1536 30, 2048 26, 5120 37, 12288 53; fp32 512 40, 640 55, 1024 42, 5120 49, 12288 64.
 template <typename S>
 hipError_t launch_norm_backward_t(const NormArgs& a, hipStream_t stream) {
     if (a.d <= 128) return launch_norm_backward_n<S, 16, 8>(a, stream);
