@@ -30,8 +30,8 @@
 // choices: from 4 of 8 groups with a bias 32 us (34 MB: 1 TB/s), plain softmax 15.5 us; one token 2.6 us; gradient of
 // 16384 x 60, 4 choices 4.4 us (8 MB).  131072 tokens: 60 experts, 4 choices 17 us (plain softmax) to 38 (groups, bias), 256
 // experts, 8 choices 52 to 104, 16 choices 146 to 315; gradients of softmax weights 16 (60 experts, 63 MB) and 52 us (256,
-// 268 MB: 5.2 TB/s, as a copy), of the others, which only write the row, 13 and 37.  In groups the LDS rows of a wavefront's four tokens start at the same bank: conflicts for 0.43 of the
-// access cycles.
+// 268 MB: 5.2 TB/s, as a copy), of the others, which only write the row, 13 and 37.  In groups the LDS rows of a wavefront's
+// four tokens start at the same bank: conflicts for 0.43 of the access cycles.
 #include <algorithm>
 #include <cfloat>
 
