@@ -399,11 +399,11 @@ __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(const Rou
     }
     const float l = e >= 0 ? (float)row[e] : -INFINITY;
     if (l == -INFINITY) e = -1, dw = 0.f;  // an expert that is out has score 0 whatever its logit does
-    const bool live = lanes_with<L>(e >= 0) != 0;  // else the row is zeros: a refused one's logits may hold NaN
     float* mine = sums[slot];
 #pragma unroll
     for (int j = 0; j < EPL; ++j) mine[i + L * j] = 0.f;
     float v[EPL], p[EPL], dot = 0.f, g;
+    bool live = false;
     if (a.renorm) {
         const float m = fmaxf(lanes_max<L>(l), -FLT_MAX);
         const float s = e < 0 ? 0.f : score_beside(l, m, softmax);
@@ -412,6 +412,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(const Rou
         const float c = lanes_sum<L>(share * dw);
         g = a.scale * share * (dw - c) * (softmax ? 1.f : sigmoid_of(-l));
     } else if (softmax) {
+        live = lanes_with<L>(e >= 0) != 0;  // else the row is zeros: a refused one's logits may hold NaN
         float top = -INFINITY, sum = 0.f;
 #pragma unroll
         for (int j = 0; j < EPL; ++j) {
@@ -440,7 +441,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(const Rou
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
         const int x = i + L * j;
-        if (x < E) out[x] = (S)(softmax && !a.renorm && live ? p[j] * (mine[x] - dot) : mine[x]);
+        if (x < E) out[x] = (S)(live ? p[j] * (mine[x] - dot) : mine[x]);
     }
 }
 
